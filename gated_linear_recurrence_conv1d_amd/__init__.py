@@ -72,6 +72,17 @@ _lib.rglru_backward_workspace_size.argtypes = [_i] * 5
 _lib.rglru_backward_workspace_size.restype = _sz
 _lib.rglru_backward.argtypes = [_vp] * 19 + [_i] * 5 + [_vp, _sz, _vp]
 _lib.rglru_backward.restype = _i
+_ll = ctypes.c_longlong
+_f = ctypes.c_float
+_lib.rglru_qk_norm_rope.argtypes = [_vp] * 12 + [_i] * 5 + [_ll] * 6 + [_f, _i, _vp]
+_lib.rglru_qk_norm_rope.restype = _i
+_lib.rglru_qk_norm_rope_backward_workspace_size.argtypes = [_i, _i]
+_lib.rglru_qk_norm_rope_backward_workspace_size.restype = _sz
+_lib.rglru_qk_norm_rope_backward.argtypes = ([_vp] * 12 + [_i] * 5 + [_ll] * 6 +
+                                             [_f, _i, _vp, _sz, _vp])
+_lib.rglru_qk_norm_rope_backward.restype = _i
+_lib.rglru_local_attention.argtypes = [_vp] * 6 + [_i] * 5 + [_ll] * 3 + [_i, _i, _f, _i, _vp]
+_lib.rglru_local_attention.restype = _i
 
 
 class RglruError(RuntimeError):
@@ -359,6 +370,227 @@ def rglru_backward(x, conv_w, W_a, b_a, W_x, b_x, Lambda, h0, y, dy, dh_T, dx, d
     _check(_lib.rglru_backward(*ptrs, B, T, D, H, _dt(io), _ptr(workspace, None, "workspace"),
                                workspace.numel() * workspace.element_size(), _stream(stream)),
            "rglru_backward")
+
+
+# ---- the local attention block's operators. Tensors of heads are [..., H, dh] with the heads of a
+# token contiguous and one stride from token to token, so slices of a packed projection need no
+# copy. All tensors of a call live on one device, which need not be the current one; the call runs on
+# `stream`, else on that device's current stream.
+class _Call:
+    """The device, type and stream of one call; checks tensors against them."""
+
+    __slots__ = ("device", "io", "stream")
+
+    def __init__(self, t, name, stream):
+        if not isinstance(t, torch.Tensor):
+            raise TypeError(f"{name}: expected a torch.Tensor")
+        if isinstance(stream, torch.cuda.Stream) and stream.device != t.device:
+            raise ValueError(f"stream: on {stream.device}, {name} on {t.device}")
+        self.device, self.io, self.stream = t.device, t.dtype, stream
+
+    def flat(self, t, dtype, shape, name):
+        """Pointer of a contiguous tensor of this type and shape; None for None."""
+        if t is None:
+            return None
+        _shape(t, shape, name)
+        p = _ptr(t, dtype, name)
+        if t.device != self.device:
+            raise ValueError(f"{name}: on {t.device}, expected {self.device}")
+        return p
+
+    def heads(self, t, lead, H, dh, name):
+        """(pointer, elements from token to token) of a tensor lead + (H, dh); (None, 0) for None."""
+        if t is None:
+            return None, 0
+        if not isinstance(t, torch.Tensor):
+            raise TypeError(f"{name}: expected a torch.Tensor")
+        _shape(t, lead + (H, dh), name)
+        if t.dtype != self.io:
+            raise ValueError(f"{name}: expected {self.io}, got {t.dtype}")
+        if not t.is_cuda or t.device != self.device:
+            raise ValueError(f"{name}: must be a device tensor on {self.device}, is on {t.device}")
+        st = t.stride()
+        if (dh > 1 and st[-1] != 1) or (H > 1 and st[-2] != dh):
+            raise ValueError(f"{name}: the heads of a token must be contiguous")
+        step, reach = H * dh, None  # the innermost leading dimension longer than 1 gives the stride
+        for n, d in zip(reversed(lead), reversed(st[:-2])):
+            if n == 1:
+                continue
+            if reach is None:
+                step = d
+            elif d != reach:
+                raise ValueError(f"{name}: tokens must be one stride apart")
+            reach = d * n
+        if step < H * dh:
+            raise ValueError(f"{name}: tokens overlap")
+        return t.data_ptr(), step
+
+    def run(self, where, fn, *args, keep=()):
+        """fn(*args, stream) on the call's device; `keep`: tensors allocated for it here."""
+        s = self.stream
+        if s is None:
+            s = torch.cuda.current_stream(self.device).cuda_stream
+        else:
+            if not isinstance(s, torch.cuda.Stream):
+                s = torch.cuda.ExternalStream(int(s), device=self.device)
+            for t in keep:  # from the current stream's pool: not reused before this stream is done
+                if t is not None:
+                    t.record_stream(s)
+            s = s.cuda_stream
+        if self.device.index == torch.cuda.current_device():
+            status = fn(*args, s)
+        else:
+            with torch.cuda.device(self.device):
+                status = fn(*args, s)
+        if status != RGLRU_OK:
+            raise RglruError(status, where)
+
+
+def _heads_of(t, name):
+    if not isinstance(t, torch.Tensor):
+        raise TypeError(f"{name}: expected a torch.Tensor")
+    if t.dim() < 3:
+        raise ValueError(f"{name}: expected [..., heads, dh], got shape {tuple(t.shape)}")
+    return tuple(t.shape[:-2]), t.shape[-2], t.shape[-1]
+
+
+def _bytes(t):
+    return 0 if t is None else t.numel() * t.element_size()
+
+
+def rglru_qk_norm_rope(q, k, positions, inv_freq, q_out, k_out, q_w=None, k_w=None, eps=1e-6,
+                       v=None, k_pages=None, v_pages=None, slots=None, stream=None, _keep=()):
+    """q [..., Hq, dh], k, v [..., Hkv, dh]; positions int32 and slots int64 [...]; inv_freq f32
+    [rot / 2]; k_pages, v_pages [pages, page, Hkv, dh]. k_out may be None with slots."""
+    c = _Call(q, "q", stream)
+    lead, Hq, dh = _heads_of(q, "q")
+    Hkv = _heads_of(k, "k")[1]
+    f32 = torch.float32
+    rows = positions.numel()
+    rot = 0 if inv_freq is None else 2 * inv_freq.numel()
+    qp, qs = c.heads(q, lead, Hq, dh, "q")
+    kp, ks = c.heads(k, lead, Hkv, dh, "k")
+    qop, qos = c.heads(q_out, lead, Hq, dh, "q_out")
+    kop, kos = c.heads(k_out, lead, Hkv, dh, "k_out")
+    n_slots = 0
+    vp = vs = kpp = vpp = sp = None
+    if slots is not None:
+        if k_pages is None or v_pages is None or v is None:
+            raise ValueError("slots: needs v, k_pages and v_pages")
+        if k_pages.dim() != 4:
+            raise ValueError(f"k_pages: expected [pages, page, Hkv, dh], got {tuple(k_pages.shape)}")
+        pool = (k_pages.shape[0], k_pages.shape[1], Hkv, dh)
+        n_slots = pool[0] * pool[1]
+        vp, vs = c.heads(v, lead, Hkv, dh, "v")
+        kpp = c.flat(k_pages, c.io, pool, "k_pages")
+        vpp = c.flat(v_pages, c.io, pool, "v_pages")
+        sp = c.flat(slots, torch.int64, lead, "slots")
+    elif k_pages is not None or v_pages is not None:
+        raise ValueError("k_pages, v_pages: need slots")
+    c.run("rglru_qk_norm_rope", _lib.rglru_qk_norm_rope, qp, kp, vp,
+          c.flat(q_w, f32, (dh,), "q_w"), c.flat(k_w, f32, (dh,), "k_w"),
+          c.flat(inv_freq, f32, (rot // 2,), "inv_freq"),
+          c.flat(positions, torch.int32, lead, "positions"), sp, qop, kop, kpp, vpp, rows, Hq, Hkv,
+          dh, rot, qs, ks, vs or 0, qos, kos, n_slots, eps, _dt(c.io), keep=_keep)
+
+
+def qk_norm_rope(q, k, positions, inv_freq, q_w=None, k_w=None, eps=1e-6, v=None, k_pages=None,
+                 v_pages=None, slots=None, q_out=None, k_out=None, stream=None):
+    """Returns (q_out, k_out), new contiguous tensors unless given (q and k themselves: in place)."""
+    new = []
+    if q_out is None:
+        q_out = torch.empty(q.shape, dtype=q.dtype, device=q.device)
+        new.append(q_out)
+    if k_out is None:
+        k_out = torch.empty(k.shape, dtype=k.dtype, device=k.device)
+        new.append(k_out)
+    rglru_qk_norm_rope(q, k, positions, inv_freq, q_out, k_out, q_w, k_w, eps, v, k_pages, v_pages,
+                       slots, stream, _keep=new)
+    return q_out, k_out
+
+
+def rglru_qk_norm_rope_backward_workspace_size(rows, dh) -> int:
+    return int(_lib.rglru_qk_norm_rope_backward_workspace_size(rows, dh))
+
+
+def rglru_qk_norm_rope_backward(q, k, positions, inv_freq, dq_out, dk_out, dq, dk, q_w=None,
+                                k_w=None, dq_w=None, dk_w=None, eps=1e-6, workspace=None,
+                                stream=None, _keep=()):
+    c = _Call(q, "q", stream)
+    lead, Hq, dh = _heads_of(q, "q")
+    Hkv = _heads_of(k, "k")[1]
+    f32 = torch.float32
+    rot = 0 if inv_freq is None else 2 * inv_freq.numel()
+    ptrs, strides = [], []
+    for t, H, name in ((q, Hq, "q"), (k, Hkv, "k"), (dq_out, Hq, "dq_out"),
+                       (dk_out, Hkv, "dk_out"), (dq, Hq, "dq"), (dk, Hkv, "dk")):
+        p, st = c.heads(t, lead, H, dh, name)
+        ptrs.append(p)
+        strides.append(st)
+    wsb = _bytes(workspace)
+    c.run("rglru_qk_norm_rope_backward", _lib.rglru_qk_norm_rope_backward, ptrs[0], ptrs[1],
+          c.flat(q_w, f32, (dh,), "q_w"), c.flat(k_w, f32, (dh,), "k_w"),
+          c.flat(inv_freq, f32, (rot // 2,), "inv_freq"),
+          c.flat(positions, torch.int32, lead, "positions"), *ptrs[2:],
+          c.flat(dq_w, f32, (dh,), "dq_w"), c.flat(dk_w, f32, (dh,), "dk_w"), positions.numel(), Hq,
+          Hkv, dh, rot, *strides, eps, _dt(c.io),
+          c.flat(workspace, None, None if workspace is None else workspace.shape, "workspace"), wsb,
+          keep=_keep)
+
+
+def qk_norm_rope_backward(q, k, positions, inv_freq, dq_out, dk_out, q_w=None, k_w=None, eps=1e-6,
+                          dq=None, dk=None, workspace=None, stream=None):
+    """Returns a dict with dq, dk (new contiguous tensors unless given) and fp32 dq_w, dk_w [dh]
+    (None without weights)."""
+    dev, dh = q.device, q.shape[-1]
+    new = []
+
+    def empty(shape, dtype):
+        new.append(torch.empty(shape, dtype=dtype, device=dev))
+        return new[-1]
+
+    dq = empty(q.shape, q.dtype) if dq is None else dq
+    dk = empty(k.shape, k.dtype) if dk is None else dk
+    dq_w = dk_w = None
+    if q_w is not None:
+        dq_w, dk_w = empty((dh,), torch.float32), empty((dh,), torch.float32)
+        if workspace is None:
+            workspace = empty((rglru_qk_norm_rope_backward_workspace_size(positions.numel(), dh),),
+                              torch.uint8)
+    rglru_qk_norm_rope_backward(q, k, positions, inv_freq, dq_out, dk_out, dq, dk, q_w, k_w, dq_w,
+                                dk_w, eps, workspace, stream, _keep=new)
+    return {"dq": dq, "dk": dk, "dq_w": dq_w, "dk_w": dk_w}
+
+
+def rglru_local_attention(q, k, v, o, window, sinks=0, lens=None, scale=0.0, lse=None, stream=None,
+                          _keep=()):
+    """q [B,T,Hq,dh], k, v [B,T,Hkv,dh], o as q and contiguous, bf16; lens int32 [B]; lse f32
+    [B,Hq,T]."""
+    c = _Call(q, "q", stream)
+    lead, Hq, dh = _heads_of(q, "q")
+    if len(lead) != 2:
+        raise ValueError(f"q: expected [B, T, Hq, dh], got shape {tuple(q.shape)}")
+    B, T = lead
+    Hkv = _heads_of(k, "k")[1]
+    qp, qs = c.heads(q, lead, Hq, dh, "q")
+    kp, ks = c.heads(k, lead, Hkv, dh, "k")
+    vp, vs = c.heads(v, lead, Hkv, dh, "v")
+    c.run("rglru_local_attention", _lib.rglru_local_attention, qp, kp, vp,
+          c.flat(lens, torch.int32, (B,), "lens"), c.flat(o, c.io, (B, T, Hq, dh), "o"),
+          c.flat(lse, torch.float32, (B, Hq, T), "lse"), B, T, Hq, Hkv, dh, qs, ks, vs,
+          min(int(window), 0x7FFFFFFF), min(int(sinks), 0x7FFFFFFF), float(scale), _dt(c.io),
+          keep=_keep)
+
+
+def local_attention(q, k, v, window, sinks=0, lens=None, scale=0.0, want_lse=False, stream=None):
+    """Returns o [B,T,Hq,dh] (bf16), or (o, lse) with lse f32 [B,Hq,T], which the backward needs."""
+    new = [torch.empty(q.shape, dtype=q.dtype, device=q.device)]
+    if want_lse:
+        B, T, Hq, _ = q.shape
+        new.append(torch.empty((B, Hq, T), dtype=torch.float32, device=q.device))
+    rglru_local_attention(q, k, v, new[0], window, sinks, lens, scale, new[1] if want_lse else None,
+                          stream, _keep=new)
+    return tuple(new) if want_lse else new[0]
 
 
 # ---- convenience wrappers (allocate outputs with torch, then call the entry points above) ----

@@ -7,14 +7,19 @@
 #include <cmath>
 
 #include "rglru.h"
+#include "rglru_check.h"
 #include "rglru_launch.h"
 
 namespace {
 
+using rglru::aligned;
+using rglru::align_up;
+using rglru::elem_bytes;
+using rglru::hip_status;
 using rglru::kBF16;
 using rglru::kF32;
+using rglru::overlaps;
 
-constexpr size_t kAlign = 256;         // workspace carve alignment
 // The scan lanes wait on HBM latency, so the chunked plan wants many lanes in flight: chunks of
 // about 64 steps (measured best from 1 to 64 sequences of 2560 channels), shorter when that
 // still leaves fewer than ~8 waves per SIMD; the direct plan once B * D alone gives 2 waves.
@@ -22,18 +27,6 @@ constexpr int kMinChunk = 16;          // smallest chunk the size query provisio
 constexpr int kMaxAutoChunk = 64;      // longest chunk the automatic plan picks
 constexpr long long kTargetLanes = 8LL * 64 * 1024;  // ~8 waves per SIMD on 256 CUs x 4 SIMDs
 constexpr long long kDirectLanes = 128LL * 1024;     // >= 2 waves per SIMD: scan channels whole
-
-size_t align_up(size_t v) { return (v + kAlign - 1) / kAlign * kAlign; }
-
-bool aligned(const void *p, size_t a) { return (reinterpret_cast<uintptr_t>(p) % a) == 0; }
-
-bool overlaps(const void *a, size_t na, const void *b, size_t nb) {
-  if (!a || !b || na == 0 || nb == 0) return false;
-  const uintptr_t a0 = reinterpret_cast<uintptr_t>(a), b0 = reinterpret_cast<uintptr_t>(b);
-  return a0 < b0 + nb && b0 < a0 + na;
-}
-
-size_t elem_bytes(rglru_dtype dt) { return dt == RGLRU_BF16 ? 2 : 4; }
 
 rglru_status check_shape(int B, int T, int D, int H, rglru_dtype dt) {
   if (B < 1 || T < 1 || D < 1 || H < 1) return RGLRU_ERR_INVALID_ARG;
@@ -141,8 +134,6 @@ size_t split_or_fused_bytes(int B, int T, int D, int H, rglru_dtype dt, Kind kin
   return rglru::kCtrlBytes + align_up(pre_bytes(B, T, D, dt)) +
          (kind == kDirect ? 0 : scan_carve(B, D, H, (T + L - 1) / L).total);
 }
-
-rglru_status hip_status(hipError_t e) { return e == hipSuccess ? RGLRU_OK : RGLRU_ERR_HIP; }
 
 }  // namespace
 

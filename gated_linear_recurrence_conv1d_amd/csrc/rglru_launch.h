@@ -106,6 +106,49 @@ bool local_mqa_supported(int dh);
 hipError_t launch_local_mqa(const void *q, const void *k, const void *v, void *o, int B, int T,
                             int Hq, int dh, int window, float scale, hipStream_t s);
 
+// The same with grouped heads, token strides (elements), a length per sequence, sinks and the
+// logarithm of the softmax's denominator (bf16, dh as above).
+struct AttnArgs {
+  const void *q, *k, *v;
+  void *o;
+  float *lse;       // [B][Hq][T] or NULL
+  const int *lens;  // [B] or NULL
+  int B, T, Hq, Hkv, dh;
+  long long q_stride, k_stride, v_stride;
+  int window, sinks;
+  float scale;
+};
+hipError_t launch_local_attention(const AttnArgs &a, hipStream_t s);
+
+// Per-head RMS norm (weights NULL: none) and rotation of q and k; with slots also into the cache
+// (rows whose slot is not in [0, n_slots): not). Strides in elements from row to row.
+constexpr int kRopeMaxDh = 512;
+struct RopeArgs {
+  const void *q, *k, *v;
+  const float *q_w, *k_w, *inv_freq;
+  const int *positions;
+  const long long *slots;
+  void *q_out, *k_out, *k_pages, *v_pages;
+  int rows, Hq, Hkv, dh, rot;
+  long long q_stride, k_stride, v_stride, q_out_stride, k_out_stride, n_slots;
+  float eps;
+};
+hipError_t launch_qk_rope(const RopeArgs &a, int io, hipStream_t s);
+struct RopeBwdArgs {
+  const void *q, *k;
+  const float *q_w, *k_w, *inv_freq;
+  const int *positions;
+  const void *dq_out, *dk_out;
+  void *dq, *dk;
+  float *part;  // [rope_bwd_groups(rows)][2][dh]
+  int rows, Hq, Hkv, dh, rot;
+  long long q_stride, k_stride, dq_out_stride, dk_out_stride, dq_stride, dk_stride;
+  float eps;
+};
+int rope_bwd_groups(int rows);
+hipError_t launch_qk_rope_backward(const RopeBwdArgs &a, float *dq_w, float *dk_w, int io,
+                                   hipStream_t s);
+
 // Backward (gradients of every input and parameter). Time is cut into chunks of kBwdChunk steps
 // for the reverse scan. BwdLayout gives the workspace carve (byte offsets, 256-byte aligned) and
 // the row split of the dW contraction; launch_backward assumes a workspace of layout.total bytes.

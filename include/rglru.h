@@ -225,6 +225,79 @@ rglru_status rglru_local_mqa(const void *q, const void *k, const void *v, void *
                              int Hq, int dh, int window, float scale, rglru_dtype dt,
                              void *stream);
 
+/* ---- The local attention block around its core: norms and rotation, attention with grouped heads,
+ * sinks and gradients, and decoding over a paged cache.
+ * Conventions of these entry points beyond the ones above: tensors of heads are [rows][heads][dh]
+ * with the heads of a row (token) contiguous and `*_stride` elements from row to row (>= heads *
+ * dh), so that q, k and v may be parts of one projection's output; int32 positions and lengths,
+ * int64 slots. Their addresses (and strides) must be multiples of an element, except where 16
+ * bytes are asked for. */
+
+/* Per-head RMS norm of queries and keys with the position rotation in the same pass (the pages name
+ * the block's attention, not its position encoding; this is the usual one of such models):
+ *   n = x / sqrt(mean(x^2) + eps) * w                         (w NULL: n = x)
+ *   y[i] = n[i] cos(phi) - n[j] sin(phi), y[j] = n[j] cos(phi) + n[i] sin(phi), j = i + rot / 2,
+ *   phi = positions[row] * inv_freq[i], i < rot / 2;  y[i] = n[i] for i >= rot.
+ * The angle is formed in fp64 from the fp32 inv_freq, so far positions keep their phase.
+ *  q [rows][Hq][dh], k [rows][Hkv][dh] dtype; q_w, k_w [dh] f32, both or neither NULL
+ *  inv_freq [rot / 2] f32 (NULL only if rot = 0); positions [rows] int32
+ *  q_out, k_out  as q and k; may be q and k themselves (same address and stride); k_out may be NULL
+ *                if the keys go to the cache only
+ *  slots [rows] int64 or NULL: with slots, the rotated keys and the values v [rows][Hkv][dh] are
+ *    also written to row slots[r] of the cache k_pages, v_pages [n_slots][Hkv][dh] (contiguous, both
+ *    dtype; n_slots = pages * page size; slot = page * page size + offset). A slot outside
+ *    [0, n_slots) writes nothing; rows of one call must not share a slot (if they do, which row's
+ *    values stay is undefined). v, k_pages, v_pages are read only with slots.
+ * rot even, 0 <= rot <= dh; dh even, <= 512; eps > 0; dtype f32 or bf16, sums in fp32.
+ * Returns RGLRU_OK or an error code. */
+rglru_status rglru_qk_norm_rope(const void *q, const void *k, const void *v, const float *q_w,
+                                const float *k_w, const float *inv_freq, const int *positions,
+                                const long long *slots, void *q_out, void *k_out, void *k_pages,
+                                void *v_pages, int rows, int Hq, int Hkv, int dh, int rot,
+                                long long q_stride, long long k_stride, long long v_stride,
+                                long long q_out_stride, long long k_out_stride, long long n_slots,
+                                float eps, rglru_dtype dt, void *stream);
+
+/* Gradients through rglru_qk_norm_rope (the cache is not differentiated):
+ *   g = rotation by -phi of dy, xh = x / sqrt(mean(x^2) + eps),
+ *   dw = sum over rows and heads of g xh, dx = (g w - xh mean(g w xh)) / sqrt(mean(x^2) + eps).
+ *  dq_out, dk_out  gradients of q_out and k_out; dq, dk outputs, as q and k; dq may be dq_out and dk
+ *                  dk_out (same address and stride)
+ *  dq_w, dk_w [dh] f32, out (NULL with q_w, k_w)
+ *  workspace       at least rglru_qk_norm_rope_backward_workspace_size(rows, dh) bytes (NULL if
+ *                  q_w is)
+ * Sums are taken in a fixed order: results are bitwise reproducible. */
+size_t rglru_qk_norm_rope_backward_workspace_size(int rows, int dh);
+rglru_status rglru_qk_norm_rope_backward(const void *q, const void *k, const float *q_w,
+                                         const float *k_w, const float *inv_freq,
+                                         const int *positions, const void *dq_out,
+                                         const void *dk_out, void *dq, void *dk, float *dq_w,
+                                         float *dk_w, int rows, int Hq, int Hkv, int dh, int rot,
+                                         long long q_stride, long long k_stride,
+                                         long long dq_out_stride, long long dk_out_stride,
+                                         long long dq_stride, long long dk_stride, float eps,
+                                         rglru_dtype dt, void *workspace, size_t workspace_bytes,
+                                         void *stream);
+
+/* rglru_local_mqa with several key/value heads, sinks, a length per sequence and the softmax's
+ * denominator: query head h reads key/value head h / (Hq / Hkv), and position u is visible to t if
+ *   u <= t and (u > t - window or u < sinks) and t, u < lens[b].
+ *   o[b][t][h] = sum_u softmax_u(scale * <q[b][t][h], k[b][u]>) v[b][u]
+ *  q [B][T][Hq][dh], k, v [B][T][Hkv][dh] bf16, *_stride elements from token to token (a multiple
+ *    of 8; a sequence's tokens are T * stride apart from the next one's), 16-byte aligned
+ *  lens [B] int32 or NULL (all T); values are taken into [0, T]. Rows t >= lens[b]: o = 0, and
+ *    nothing in rows u >= lens[b] of k and v is used (they may hold anything)
+ *  o [B][T][Hq][dh] bf16, contiguous, out; must not overlap the inputs
+ *  lse [B][Hq][T] f32 or NULL, out: ln sum_u exp(scale * s_u); -inf for rows t >= lens[b]
+ *  window >= 1, sinks >= 0; scale > 0, or 0 for 1/sqrt(dh)
+ * An infinite or NaN k or v reaches the rows that see it and no others. Supported: dt = RGLRU_BF16,
+ * dh in {64, 128, 256}, Hq % Hkv == 0, strides <= 2^20, T * stride * 2 <= 2^30 bytes for k and v. */
+rglru_status rglru_local_attention(const void *q, const void *k, const void *v, const int *lens,
+                                   void *o, float *lse, int B, int T, int Hq, int Hkv, int dh,
+                                   long long q_stride, long long k_stride, long long v_stride,
+                                   int window, int sinks, float scale, rglru_dtype dt,
+                                   void *stream);
+
 /* Bytes of device workspace rglru_backward needs for this shape (0 when the shape is invalid).
  * About 4 B (bf16) or 8 B (fp32) of pre-activations, the same again of gate gradients and 4 B of
  * conv-output gradient per element of x, plus chunk summaries and partial sums. */

@@ -83,6 +83,11 @@ _lib.rglru_qk_norm_rope_backward.argtypes = ([_vp] * 12 + [_i] * 5 + [_ll] * 6 +
 _lib.rglru_qk_norm_rope_backward.restype = _i
 _lib.rglru_local_attention.argtypes = [_vp] * 6 + [_i] * 5 + [_ll] * 3 + [_i, _i, _f, _i, _vp]
 _lib.rglru_local_attention.restype = _i
+_lib.rglru_paged_attention_workspace_size.argtypes = [_i] * 9
+_lib.rglru_paged_attention_workspace_size.restype = _sz
+_lib.rglru_paged_attention.argtypes = ([_vp] * 6 + [_i] * 4 + [_ll] + [_i] * 5 +
+                                       [_f, _i, _vp, _sz, _vp])
+_lib.rglru_paged_attention.restype = _i
 
 
 class RglruError(RuntimeError):
@@ -591,6 +596,52 @@ def local_attention(q, k, v, window, sinks=0, lens=None, scale=0.0, want_lse=Fal
     rglru_local_attention(q, k, v, new[0], window, sinks, lens, scale, new[1] if want_lse else None,
                           stream, _keep=new)
     return tuple(new) if want_lse else new[0]
+
+
+def rglru_paged_attention_workspace_size(N, Hq, Hkv, dh, page_size, max_pages, window, sinks,
+                                         dtype) -> int:
+    return int(_lib.rglru_paged_attention_workspace_size(
+        N, Hq, Hkv, dh, page_size, max_pages, min(int(window), 0x7FFFFFFF),
+        min(int(sinks), 0x7FFFFFFF), _dt(dtype)))
+
+
+def rglru_paged_attention(q, k_pages, v_pages, block_table, lens, o, window, sinks=0, scale=0.0,
+                          workspace=None, stream=None, _keep=()):
+    """q [N,Hq,dh], k_pages, v_pages [pages,page,Hkv,dh] of one type (bf16 or f32); block_table
+    int32 [N,max_pages], lens int32 [N]; o as q and contiguous."""
+    c = _Call(q, "q", stream)
+    lead, Hq, dh = _heads_of(q, "q")
+    if len(lead) != 1:
+        raise ValueError(f"q: expected [N, Hq, dh], got shape {tuple(q.shape)}")
+    if k_pages.dim() != 4 or block_table.dim() != 2:
+        raise ValueError("k_pages: expected [pages, page, Hkv, dh]; block_table: [N, max_pages]")
+    pages, page, Hkv, _ = k_pages.shape
+    N, pool = lead[0], (pages, page, Hkv, dh)
+    qp, qs = c.heads(q, lead, Hq, dh, "q")
+    c.run("rglru_paged_attention", _lib.rglru_paged_attention, qp,
+          c.flat(k_pages, c.io, pool, "k_pages"), c.flat(v_pages, c.io, pool, "v_pages"),
+          c.flat(block_table, torch.int32, (N, block_table.shape[1]), "block_table"),
+          c.flat(lens, torch.int32, (N,), "lens"), c.flat(o, c.io, (N, Hq, dh), "o"), N, Hq, Hkv, dh,
+          qs, pages, page, block_table.shape[1], min(int(window), 0x7FFFFFFF),
+          min(int(sinks), 0x7FFFFFFF), float(scale), _dt(c.io),
+          c.flat(workspace, None, None if workspace is None else workspace.shape, "workspace"),
+          _bytes(workspace), keep=_keep)
+
+
+def paged_attention(q, k_pages, v_pages, block_table, lens, window, sinks=0, scale=0.0,
+                    workspace=None, stream=None):
+    """Returns o [N,Hq,dh] of q's type."""
+    new = [torch.empty(q.shape, dtype=q.dtype, device=q.device)]
+    if workspace is None and q.dim() == 3 and k_pages.dim() == 4 and block_table.dim() == 2:
+        n = rglru_paged_attention_workspace_size(q.shape[0], q.shape[1], k_pages.shape[2],
+                                                 q.shape[2], k_pages.shape[1],
+                                                 block_table.shape[1], window, sinks, q.dtype)
+        if n:
+            workspace = torch.empty(n, dtype=torch.uint8, device=q.device)
+            new.append(workspace)
+    rglru_paged_attention(q, k_pages, v_pages, block_table, lens, new[0], window, sinks, scale,
+                          workspace, stream, _keep=new)
+    return new[0]
 
 
 # ---- convenience wrappers (allocate outputs with torch, then call the entry points above) ----

@@ -22,6 +22,7 @@ using rglru::Rows;
 using rglru::same;
 
 constexpr long long kMaxStride = 1LL << 20;  // elements from token to token
+constexpr long long kMaxTokens = 0x7FFFFF00;  // token and cache row indices stay in an int
 
 Rows heads_of(const void *p, size_t rows, int heads, int dh, long long stride, rglru_dtype dt) {
   const size_t e = elem_bytes(dt);
@@ -73,6 +74,40 @@ rglru_status check_attn(int B, int T, int Hq, int Hkv, int dh, long long q_strid
   constexpr long long kRange = 1LL << 30;
   if (T * k_stride * 2 > kRange || T * v_stride * 2 > kRange) return RGLRU_ERR_UNSUPPORTED;
   return RGLRU_OK;
+}
+
+// The kernels' running maximum starts here: below every score that matters, and finite in exp2
+// units.
+float max_floor(float c) { return -2.9e38f / (c > 1.0f ? c : 1.0f); }
+
+rglru_status check_paged(int N, int Hq, int Hkv, int dh, int page_size, int max_pages, int window,
+                         int sinks, rglru_dtype dt) {
+  if (page_size < 1 || max_pages < 1 || window < 1 || sinks < 0) return RGLRU_ERR_INVALID_ARG;
+  const rglru_status st = check_heads(N, Hq, Hkv, dh, dt);
+  if (st != RGLRU_OK) return st;
+  if (Hq % Hkv) return RGLRU_ERR_INVALID_ARG;
+  if (!rglru::local_mqa_supported(dh)) return RGLRU_ERR_UNSUPPORTED;
+  // one grid row per 16 heads of a group; one grid column per (sequence, chunk)
+  if (static_cast<long long>(Hkv) * ((Hq / Hkv + 15) / 16) > 65535) return RGLRU_ERR_UNSUPPORTED;
+  if (static_cast<long long>(N) * Hq > (1LL << 30)) return RGLRU_ERR_UNSUPPORTED;
+  if (static_cast<long long>(max_pages) * page_size >= kMaxTokens) return RGLRU_ERR_UNSUPPORTED;
+  return RGLRU_OK;
+}
+
+rglru::PagedPlan plan_of(int N, int Hq, int Hkv, int page_size, int max_pages, int window,
+                         int sinks, rglru_dtype dt) {
+  return rglru::paged_plan(N, Hq, Hkv, static_cast<long long>(max_pages) * page_size, window, sinks,
+                           dt == RGLRU_BF16 ? kBF16 : kF32);
+}
+
+// The chunks' O, then their (m, l).
+size_t paged_part_bytes(const rglru::PagedPlan &p, int N, int Hq, int dh) {
+  return rglru::align_up(static_cast<size_t>(N) * p.splits * Hq * dh * sizeof(float));
+}
+size_t paged_bytes(const rglru::PagedPlan &p, int N, int Hq, int dh) {
+  if (p.splits == 1) return 0;
+  return paged_part_bytes(p, N, Hq, dh) +
+         rglru::align_up(static_cast<size_t>(N) * p.splits * Hq * 2 * sizeof(float));
 }
 
 }  // namespace
@@ -219,9 +254,62 @@ rglru_status rglru_local_attention(const void *q, const void *k, const void *v, 
   if (overlaps(outs[0], outs[1])) return RGLRU_ERR_INVALID_ARG;
   if (scale == 0.0f) scale = 1.0f / std::sqrt(static_cast<float>(dh));
   const rglru::AttnArgs a = {q, k, v, o, lse, lens, B, T, Hq, Hkv, dh, q_stride, k_stride, v_stride,
-                             window, sinks, scale};
+                             window, sinks, scale, max_floor(scale * 1.4426950408889634f)};
   (void)hipGetLastError();
   return hip_status(rglru::launch_local_attention(a, static_cast<hipStream_t>(stream)));
+}
+
+size_t rglru_paged_attention_workspace_size(int N, int Hq, int Hkv, int dh, int page_size,
+                                            int max_pages, int window, int sinks, rglru_dtype dt) {
+  if (check_paged(N, Hq, Hkv, dh, page_size, max_pages, window, sinks, dt) != RGLRU_OK) return 0;
+  return paged_bytes(plan_of(N, Hq, Hkv, page_size, max_pages, window, sinks, dt), N, Hq, dh);
+}
+
+rglru_status rglru_paged_attention(const void *q, const void *k_pages, const void *v_pages,
+                                   const int *block_table, const int *lens, void *o, int N, int Hq,
+                                   int Hkv, int dh, long long q_stride, int num_pages,
+                                   int page_size, int max_pages, int window, int sinks,
+                                   float scale, rglru_dtype dt, void *workspace,
+                                   size_t workspace_bytes, void *stream) {
+  rglru_status st = check_paged(N, Hq, Hkv, dh, page_size, max_pages, window, sinks, dt);
+  if (st != RGLRU_OK) return st;
+  if (num_pages < 1 || !(scale == scale) || scale < 0.0f || std::isinf(scale))
+    return RGLRU_ERR_INVALID_ARG;
+  if (static_cast<long long>(num_pages) * page_size >= kMaxTokens) return RGLRU_ERR_UNSUPPORTED;
+  if (!q || !k_pages || !v_pages || !block_table || !lens || !o) return RGLRU_ERR_INVALID_ARG;
+  const size_t e = elem_bytes(dt);
+  if (!stride_ok(q_stride, Hq, dh) || q_stride * e % 16) return RGLRU_ERR_INVALID_ARG;
+  const void *vec16[] = {q, k_pages, v_pages};
+  for (const void *p : vec16)
+    if (!aligned(p, 16)) return RGLRU_ERR_INVALID_ARG;
+  if (!aligned(o, e) || !aligned(block_table, 4) || !aligned(lens, 4)) return RGLRU_ERR_INVALID_ARG;
+  const rglru::PagedPlan plan = plan_of(N, Hq, Hkv, page_size, max_pages, window, sinks, dt);
+  const size_t need = paged_bytes(plan, N, Hq, dh);
+  if (need && (!workspace || workspace_bytes < need)) return RGLRU_ERR_WORKSPACE;
+  if (need && !aligned(workspace, 16)) return RGLRU_ERR_INVALID_ARG;
+  const size_t pool = static_cast<size_t>(num_pages) * page_size * Hkv * dh * e;
+  const Rows outs[] = {flat(o, static_cast<size_t>(N) * Hq * dh * e),
+                       flat(need ? workspace : nullptr, need)};
+  const Rows ins[] = {heads_of(q, N, Hq, dh, q_stride, dt), flat(k_pages, pool), flat(v_pages, pool),
+                      flat(block_table, static_cast<size_t>(N) * max_pages * sizeof(int)),
+                      flat(lens, static_cast<size_t>(N) * sizeof(int))};
+  for (const Rows &w : outs)
+    for (const Rows &r : ins)
+      if (overlaps(w, r)) return RGLRU_ERR_INVALID_ARG;
+  if (overlaps(outs[0], outs[1])) return RGLRU_ERR_INVALID_ARG;
+  if (scale == 0.0f) scale = 1.0f / std::sqrt(static_cast<float>(dh));
+  const float c = scale * 1.4426950408889634f;
+  char *ws = static_cast<char *>(workspace);
+  rglru::PagedArgs a = {q,        k_pages, v_pages, block_table, lens,      o,         nullptr,
+                        nullptr,  N,       Hq,      Hkv,         dh,        q_stride,  num_pages,
+                        page_size, max_pages, window, sinks,     c,         max_floor(c)};
+  if (need) {
+    a.part = reinterpret_cast<float *>(ws);
+    a.stat = reinterpret_cast<float *>(ws + paged_part_bytes(plan, N, Hq, dh));
+  }
+  (void)hipGetLastError();
+  return hip_status(rglru::launch_paged_attention(a, plan, dt == RGLRU_BF16 ? kBF16 : kF32,
+                                                  static_cast<hipStream_t>(stream)));
 }
 
 }  // extern "C"

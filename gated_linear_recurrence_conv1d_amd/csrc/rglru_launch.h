@@ -117,8 +117,30 @@ struct AttnArgs {
   long long q_stride, k_stride, v_stride;
   int window, sinks;
   float scale;
+  float floor;  // the running maximum's start: below every score, floor * scale * log2(e) finite
 };
 hipError_t launch_local_attention(const AttnArgs &a, hipStream_t s);
+
+// Attention of one token per sequence over a paged cache; part and stat hold the chunks' O and
+// (m, l) when a row can have more than one (splits > 1).
+struct PagedArgs {
+  const void *q, *k_pages, *v_pages;
+  const int *table, *lens;
+  void *o;
+  float *part;  // [N][splits][Hq][dh]
+  float *stat;  // [N][splits][Hq][2]
+  int N, Hq, Hkv, dh;
+  long long q_stride;
+  int num_pages, page, max_pages, window, sinks;
+  float c;      // scale * log2(e)
+  float floor;  // the running maximum's start: below every score, floor * c finite
+};
+struct PagedPlan {
+  int chunk;   // tiles per workgroup
+  int splits;  // the most chunks a row can have
+};
+PagedPlan paged_plan(int N, int Hq, int Hkv, long long max_len, int window, int sinks, int io);
+hipError_t launch_paged_attention(const PagedArgs &a, const PagedPlan &p, int io, hipStream_t s);
 
 // Per-head RMS norm (weights NULL: none) and rotation of q and k; with slots also into the cache
 // (rows whose slot is not in [0, n_slots): not). Strides in elements from row to row.

@@ -585,7 +585,7 @@ hipError_t launch_local_attention(const AttnArgs &a, hipStream_t s) {
   x.v_stride = static_cast<unsigned>(a.v_stride);
   x.group = a.Hq / a.Hkv;
   x.sinks = std::min(a.sinks, a.T);
-  x.floor = -2.9e38f / std::max(1.0f, a.scale * 1.4426950408889634f);
+  x.floor = a.floor;
   return launch<true>(a.q, a.k, a.v, a.o, a.B, a.T, a.Hq, a.dh, std::min(a.window, a.T), a.scale, x, s);
 }
 

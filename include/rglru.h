@@ -298,6 +298,33 @@ rglru_status rglru_local_attention(const void *q, const void *k, const void *v, 
                                    int window, int sinks, float scale, rglru_dtype dt,
                                    void *stream);
 
+/* Attention of one new token per sequence over a paged key-value cache, split over the cache's
+ * length and joined: the decoding form of rglru_local_attention. Sequence n holds lens[n] tokens, the
+ * new one (already written to the cache, see rglru_qk_norm_rope) among them; token u lies in row u %
+ * page_size of page block_table[n][u / page_size]. Visible: u < lens[n] and (u >= lens[n] - window
+ * or u < sinks).
+ *   o[n][h] = sum_u softmax_u(scale * <q[n][h], k[u]>) v[u], key/value head h / (Hq / Hkv)
+ *  q [N][Hq][dh] dtype, q_stride elements from row to row, 16-byte aligned rows
+ *  k_pages, v_pages [num_pages][page_size][Hkv][dh] dtype, contiguous, 16-byte aligned
+ *  block_table [N][max_pages] int32; only the entries of visible tokens' pages are used (pages before
+ *    the window may have been given back)
+ *  lens [N] int32; 0: o = 0
+ *  o [N][Hq][dh] dtype, contiguous, out
+ *  workspace       at least rglru_paged_attention_workspace_size() bytes (NULL if that is 0);
+ *                  contents on entry are ignored
+ * A row whose length is negative or over max_pages * page_size, or that needs a page outside [0,
+ * num_pages), becomes NaN; nothing outside the pool is read. Supported: f32 and bf16, dh in {64,
+ * 128, 256}, Hq % Hkv == 0, any page_size >= 1, max_pages * page_size and num_pages * page_size
+ * below 2^31 - 256. Sums are taken in a fixed order: results are bitwise reproducible. */
+size_t rglru_paged_attention_workspace_size(int N, int Hq, int Hkv, int dh, int page_size,
+                                            int max_pages, int window, int sinks, rglru_dtype dt);
+rglru_status rglru_paged_attention(const void *q, const void *k_pages, const void *v_pages,
+                                   const int *block_table, const int *lens, void *o, int N, int Hq,
+                                   int Hkv, int dh, long long q_stride, int num_pages,
+                                   int page_size, int max_pages, int window, int sinks,
+                                   float scale, rglru_dtype dt, void *workspace,
+                                   size_t workspace_bytes, void *stream);
+
 /* Bytes of device workspace rglru_backward needs for this shape (0 when the shape is invalid).
  * About 4 B (bf16) or 8 B (fp32) of pre-activations, the same again of gate gradients and 4 B of
  * conv-output gradient per element of x, plus chunk summaries and partial sums. */

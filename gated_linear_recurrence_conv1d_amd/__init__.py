@@ -83,6 +83,11 @@ _lib.rglru_qk_norm_rope_backward.argtypes = ([_vp] * 12 + [_i] * 5 + [_ll] * 6 +
 _lib.rglru_qk_norm_rope_backward.restype = _i
 _lib.rglru_local_attention.argtypes = [_vp] * 6 + [_i] * 5 + [_ll] * 3 + [_i, _i, _f, _i, _vp]
 _lib.rglru_local_attention.restype = _i
+_lib.rglru_local_attention_backward_workspace_size.argtypes = [_i] * 7
+_lib.rglru_local_attention_backward_workspace_size.restype = _sz
+_lib.rglru_local_attention_backward.argtypes = ([_vp] * 10 + [_i] * 5 + [_ll] * 6 +
+                                                [_i, _i, _f, _i, _vp, _sz, _vp])
+_lib.rglru_local_attention_backward.restype = _i
 _lib.rglru_paged_attention_workspace_size.argtypes = [_i] * 9
 _lib.rglru_paged_attention_workspace_size.restype = _sz
 _lib.rglru_paged_attention.argtypes = ([_vp] * 6 + [_i] * 4 + [_ll] + [_i] * 5 +
@@ -596,6 +601,55 @@ def local_attention(q, k, v, window, sinks=0, lens=None, scale=0.0, want_lse=Fal
     rglru_local_attention(q, k, v, new[0], window, sinks, lens, scale, new[1] if want_lse else None,
                           stream, _keep=new)
     return tuple(new) if want_lse else new[0]
+
+
+def rglru_local_attention_backward_workspace_size(B, T, Hq, Hkv, dh, window, sinks=0) -> int:
+    return int(_lib.rglru_local_attention_backward_workspace_size(
+        B, T, Hq, Hkv, dh, min(int(window), 0x7FFFFFFF), min(int(sinks), 0x7FFFFFFF)))
+
+
+def rglru_local_attention_backward(q, k, v, o, lse, do, dq, dk, dv, window, sinks=0, lens=None,
+                                   scale=0.0, workspace=None, stream=None, _keep=()):
+    """o, do as q and contiguous; dq as q, dk and dv as k (slices of a packed gradient are fine)."""
+    c = _Call(q, "q", stream)
+    lead, Hq, dh = _heads_of(q, "q")
+    if len(lead) != 2:
+        raise ValueError(f"q: expected [B, T, Hq, dh], got shape {tuple(q.shape)}")
+    B, T = lead
+    Hkv = _heads_of(k, "k")[1]
+    (qp, qs), (dqp, dqs) = c.heads(q, lead, Hq, dh, "q"), c.heads(dq, lead, Hq, dh, "dq")
+    (kp, ks), (vp, vs), (dkp, dks), (dvp, dvs) = (
+        c.heads(t, lead, Hkv, dh, n) for t, n in ((k, "k"), (v, "v"), (dk, "dk"), (dv, "dv")))
+    full = (B, T, Hq, dh)
+    c.run("rglru_local_attention_backward", _lib.rglru_local_attention_backward, qp, kp, vp,
+          c.flat(lens, torch.int32, (B,), "lens"), c.flat(o, c.io, full, "o"),
+          c.flat(lse, torch.float32, (B, Hq, T), "lse"), c.flat(do, c.io, full, "do"), dqp, dkp, dvp,
+          B, T, Hq, Hkv, dh, qs, ks, vs, dqs, dks, dvs, min(int(window), 0x7FFFFFFF),
+          min(int(sinks), 0x7FFFFFFF), float(scale), _dt(c.io),
+          c.flat(workspace, None, None if workspace is None else workspace.shape, "workspace"),
+          _bytes(workspace), keep=_keep)
+
+
+def local_attention_backward(q, k, v, o, lse, do, window, sinks=0, lens=None, scale=0.0, dq=None,
+                             dk=None, dv=None, workspace=None, stream=None):
+    """Gradients through local_attention(.., want_lse=True). Returns a dict with dq, dk, dv (bf16;
+    new contiguous tensors unless given)."""
+    new = []
+
+    def empty(shape, dtype):
+        new.append(torch.empty(shape, dtype=dtype, device=q.device))
+        return new[-1]
+
+    dq = empty(q.shape, q.dtype) if dq is None else dq
+    dk = empty(k.shape, k.dtype) if dk is None else dk
+    dv = empty(v.shape, v.dtype) if dv is None else dv
+    if workspace is None and q.dim() == 4 and k.dim() == 4:
+        n = rglru_local_attention_backward_workspace_size(*q.shape[:3], k.shape[2], q.shape[3],
+                                                          window, sinks)
+        workspace = empty((n,), torch.uint8)
+    rglru_local_attention_backward(q, k, v, o, lse, do, dq, dk, dv, window, sinks, lens, scale,
+                                   workspace, stream, _keep=new)
+    return {"dq": dq, "dk": dk, "dv": dv}
 
 
 def rglru_paged_attention_workspace_size(N, Hq, Hkv, dh, page_size, max_pages, window, sinks,

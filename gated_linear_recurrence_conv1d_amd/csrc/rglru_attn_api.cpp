@@ -4,6 +4,7 @@
 #include <hip/hip_runtime.h>
 #include <stdint.h>
 
+#include <algorithm>
 #include <cmath>
 
 #include "rglru.h"
@@ -257,6 +258,71 @@ rglru_status rglru_local_attention(const void *q, const void *k, const void *v, 
                              window, sinks, scale, max_floor(scale * 1.4426950408889634f)};
   (void)hipGetLastError();
   return hip_status(rglru::launch_local_attention(a, static_cast<hipStream_t>(stream)));
+}
+
+size_t rglru_local_attention_backward_workspace_size(int B, int T, int Hq, int Hkv, int dh,
+                                                     int window, int sinks) {
+  if (check_attn(B, T, Hq, Hkv, dh, static_cast<long long>(Hq) * dh, static_cast<long long>(Hkv) * dh,
+                 static_cast<long long>(Hkv) * dh, window, sinks, 0.0f, RGLRU_BF16) != RGLRU_OK)
+    return 0;
+  const rglru::AttnBwdPlan p = rglru::attn_bwd_plan(B, T, Hq, Hkv, std::min(window, T), sinks);
+  return rglru::align_up(rglru::attn_bwd_delta_floats(B, T, Hq) * sizeof(float)) +
+         rglru::align_up(rglru::attn_bwd_part_floats(p, B, Hkv, dh) * sizeof(float));
+}
+
+rglru_status rglru_local_attention_backward(
+    const void *q, const void *k, const void *v, const int *lens, const void *o, const float *lse,
+    const void *d_o, void *dq, void *dk, void *dv, int B, int T, int Hq, int Hkv, int dh,
+    long long q_stride, long long k_stride, long long v_stride, long long dq_stride,
+    long long dk_stride, long long dv_stride, int window, int sinks, float scale, rglru_dtype dt,
+    void *workspace, size_t workspace_bytes, void *stream) {
+  rglru_status st =
+      check_attn(B, T, Hq, Hkv, dh, q_stride, k_stride, v_stride, window, sinks, scale, dt);
+  if (st != RGLRU_OK) return st;
+  if (!q || !k || !v || !o || !lse || !d_o || !dq || !dk || !dv) return RGLRU_ERR_INVALID_ARG;
+  if (!stride_ok(dq_stride, Hq, dh) || !stride_ok(dk_stride, Hkv, dh) || !stride_ok(dv_stride, Hkv, dh))
+    return RGLRU_ERR_INVALID_ARG;
+  if (dq_stride % 8 || dk_stride % 8 || dv_stride % 8) return RGLRU_ERR_INVALID_ARG;
+  const void *vec16[] = {q, k, v, o, d_o, dq, dk, dv};
+  for (const void *p : vec16)
+    if (!aligned(p, 16)) return RGLRU_ERR_INVALID_ARG;
+  if (!aligned(lens, 4) || !aligned(lse, 4)) return RGLRU_ERR_INVALID_ARG;
+  const size_t need = rglru_local_attention_backward_workspace_size(B, T, Hq, Hkv, dh, window, sinks);
+  if (!workspace || workspace_bytes < need) return RGLRU_ERR_WORKSPACE;
+  if (!aligned(workspace, 16)) return RGLRU_ERR_INVALID_ARG;
+  const size_t rows = static_cast<size_t>(B) * T;
+  const size_t obytes = rows * Hq * dh * 2;
+  const Rows outs[] = {heads_of(dq, rows, Hq, dh, dq_stride, dt), heads_of(dk, rows, Hkv, dh, dk_stride, dt),
+                       heads_of(dv, rows, Hkv, dh, dv_stride, dt), flat(workspace, need)};
+  const Rows ins[] = {heads_of(q, rows, Hq, dh, q_stride, dt), heads_of(k, rows, Hkv, dh, k_stride, dt),
+                      heads_of(v, rows, Hkv, dh, v_stride, dt), flat(o, obytes), flat(d_o, obytes),
+                      flat(lse, rows * Hq * sizeof(float)),
+                      flat(lens, static_cast<size_t>(B) * sizeof(int))};
+  for (size_t i = 0; i < 4; ++i) {
+    for (const Rows &r : ins)
+      if (overlaps(outs[i], r)) return RGLRU_ERR_INVALID_ARG;
+    for (size_t j = i + 1; j < 4; ++j)
+      if (overlaps(outs[i], outs[j])) return RGLRU_ERR_INVALID_ARG;
+  }
+  if (scale == 0.0f) scale = 1.0f / std::sqrt(static_cast<float>(dh));
+  window = std::min(window, T);
+  sinks = std::min(sinks, T);
+  const rglru::AttnBwdPlan p = rglru::attn_bwd_plan(B, T, Hq, Hkv, window, sinks);
+  char *ws = static_cast<char *>(workspace);
+  rglru::AttnBwdArgs a = {};
+  a.q = q, a.k = k, a.v = v, a.o = o, a.do_ = d_o, a.lse = lse, a.lens = lens;
+  a.dq = dq, a.dk = dk, a.dv = dv;
+  a.delta = reinterpret_cast<float *>(ws);
+  a.part = reinterpret_cast<float *>(
+      ws + rglru::align_up(rglru::attn_bwd_delta_floats(B, T, Hq) * sizeof(float)));
+  a.B = B, a.T = T, a.Hq = Hq, a.Hkv = Hkv, a.group = Hq / Hkv;
+  a.q_stride = q_stride, a.k_stride = k_stride, a.v_stride = v_stride;
+  a.dq_stride = dq_stride, a.dk_stride = dk_stride, a.dv_stride = dv_stride;
+  a.window = window, a.sinks = sinks, a.scale = scale, a.c = scale * 1.4426950408889634f;
+  a.nsb = p.nsb, a.s_sink = p.s_sink, a.s_win = p.s_win, a.slots = p.slots;
+  (void)hipGetLastError();
+  return hip_status(
+      rglru::launch_local_attention_backward(a, dh, static_cast<hipStream_t>(stream)));
 }
 
 size_t rglru_paged_attention_workspace_size(int N, int Hq, int Hkv, int dh, int page_size,

@@ -80,6 +80,9 @@ template <int DH> struct Mqa {
   static constexpr int kLdsBytes = 4 * kKElems * 2 + kXpBytes;
 };
 
+// s c - m c in one FMA is off by the rounding of m c, 2^-24 of it: for scores beyond this (in exp2
+// units) the difference s - m is formed first
+constexpr float kBigScore = 16384.0f;
 constexpr int kSplitKeys = 256;  // P as hi + lo below this many keys per row (see split)
 
 typedef short i16x4_t __attribute__((ext_vector_type(4)));
@@ -362,9 +365,16 @@ __global__ __launch_bounds__(Mqa<DH>::kThreads, 1) void local_mqa_fwd(
     }
     const float mc = m_run * c;
     float pq[2] = {0.0f, 0.0f};
+    if (EXT && __any(fabsf(mc) > kBigScore)) {  // wave-uniform
+#pragma unroll
+      for (int j = 0; j < 16; ++j) sacc[j] = (sacc[j] - m_run) * c;
+    } else {
+#pragma unroll
+      for (int j = 0; j < 16; ++j) sacc[j] = fmaf(sacc[j], c, -mc);
+    }
 #pragma unroll
     for (int j = 0; j < 16; ++j) {
-      const float p = __builtin_amdgcn_exp2f(fmaf(sacc[j], c, -mc));
+      const float p = __builtin_amdgcn_exp2f(sacc[j]);
       sacc[j] = p;
       pq[j >> 3] += p;
     }

@@ -245,11 +245,10 @@ __global__ __launch_bounds__(64 * kPgWaves, 2) void paged_fwd(PagedArgs a, int c
 #pragma unroll
         for (int t = 0; t < M::kOT; ++t) oacc[t] *= corr;
       }
-      const float mc = m_run * a.c;
       float p[M::kVK];
 #pragma unroll
       for (int k = 0; k < M::kVK; ++k) {
-        p[k] = __builtin_amdgcn_exp2f(fmaf(s[k >> 2][k & 3], a.c, -mc));
+        p[k] = __builtin_amdgcn_exp2f((s[k >> 2][k & 3] - m_run) * a.c);
         l_run += p[k];
       }
       // ---- O^T += V^T P^T

@@ -298,6 +298,28 @@ rglru_status rglru_local_attention(const void *q, const void *k, const void *v, 
                                    int window, int sinks, float scale, rglru_dtype dt,
                                    void *stream);
 
+/* Gradients through rglru_local_attention, given its output o, its lse and do = dL/do:
+ *   p = exp(scale s - lse), delta = <do, o>, ds = p (do v^T - delta),
+ *   dq = scale ds k, dk = scale sum over the group's heads of ds^T q, dv = the same sum of p^T do.
+ *  q, k, v, lens, window, sinks, scale and the strides as in the forward
+ *  o, do [B][T][Hq][dh] bf16, contiguous; lse [B][Hq][T] f32, the forward's
+ *  dq [B][T][Hq][dh], dk, dv [B][T][Hkv][dh] bf16, out, with their own strides (multiples of 8); they
+ *    may be parts of one tensor and must not overlap the inputs or each other. Rows t >= lens[b]
+ *    are zero, and nothing in those rows of the inputs is used
+ *  workspace  at least rglru_local_attention_backward_workspace_size() bytes
+ * P and dS enter their products as bf16, sums are fp32 and taken in a fixed order (no floating-point
+ * atomics): results are bitwise reproducible. p comes from the scores and lse, both fp32: scores
+ * (scale * s) beyond 2^16 in magnitude lose its digits. An infinite or NaN input may reach every gradient of
+ * the tiles (128 rows by 64) it is in. */
+size_t rglru_local_attention_backward_workspace_size(int B, int T, int Hq, int Hkv, int dh,
+                                                     int window, int sinks);
+rglru_status rglru_local_attention_backward(
+    const void *q, const void *k, const void *v, const int *lens, const void *o, const float *lse,
+    const void *d_o, void *dq, void *dk, void *dv, int B, int T, int Hq, int Hkv, int dh,
+    long long q_stride, long long k_stride, long long v_stride, long long dq_stride,
+    long long dk_stride, long long dv_stride, int window, int sinks, float scale, rglru_dtype dt,
+    void *workspace, size_t workspace_bytes, void *stream);
+
 /* Attention of one new token per sequence over a paged key-value cache, split over the cache's
  * length and joined: the decoding form of rglru_local_attention. Sequence n holds lens[n] tokens, the
  * new one (already written to the cache, see rglru_qk_norm_rope) among them; token u lies in row u %

@@ -8,6 +8,7 @@ fallback of any kind: if librglru.so is missing or fails to load, importing this
 from __future__ import annotations
 
 import ctypes
+import functools
 import os
 
 import torch
@@ -386,44 +387,65 @@ def rglru_backward(x, conv_w, W_a, b_a, W_x, b_x, Lambda, h0, y, dy, dh_T, dx, d
 # token contiguous and one stride from token to token, so slices of a packed projection need no
 # copy. All tensors of a call live on one device, which need not be the current one; the call runs on
 # `stream`, else on that device's current stream.
-class _Call:
-    """The device, type and stream of one call; checks tensors against them."""
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (
+    lambda index: torch.cuda.current_stream(index).cuda_stream)
 
-    __slots__ = ("device", "io", "stream")
+
+class _Call:
+    """The device, type and stream of one call; checks tensors against them. The checks of tensors
+    that fit take a few attribute reads each: with calls of a few microseconds on the GPU, the
+    host's share is what counts."""
+
+    __slots__ = ("index", "io", "stream")
 
     def __init__(self, t, name, stream):
         if not isinstance(t, torch.Tensor):
             raise TypeError(f"{name}: expected a torch.Tensor")
         if isinstance(stream, torch.cuda.Stream) and stream.device != t.device:
             raise ValueError(f"stream: on {stream.device}, {name} on {t.device}")
-        self.device, self.io, self.stream = t.device, t.dtype, stream
+        self.index, self.io, self.stream = t.get_device(), t.dtype, stream
 
     def flat(self, t, dtype, shape, name):
-        """Pointer of a contiguous tensor of this type and shape; None for None."""
+        """Pointer of a contiguous tensor of this type and shape (None: any); None for None."""
         if t is None:
             return None
-        _shape(t, shape, name)
+        if (isinstance(t, torch.Tensor) and (dtype is None or t.dtype is dtype) and
+                (shape is None or t.shape == shape) and t.get_device() == self.index >= 0 and
+                t.is_contiguous()):
+            return t.data_ptr()
+        if shape is not None and isinstance(t, torch.Tensor):
+            _shape(t, shape, name)
         p = _ptr(t, dtype, name)
-        if t.device != self.device:
-            raise ValueError(f"{name}: on {t.device}, expected {self.device}")
+        if t.get_device() != self.index:
+            raise ValueError(f"{name}: on device {t.get_device()}, expected {self.index}")
         return p
 
-    def heads(self, t, lead, H, dh, name):
-        """(pointer, elements from token to token) of a tensor lead + (H, dh); (None, 0) for None."""
+    def heads(self, t, shape, name):
+        """(pointer, elements from token to token) of a tensor of this shape, (..., H, dh); (None, 0)
+        for None."""
         if t is None:
             return None, 0
+        H, dh = shape[-2:]
+        if (isinstance(t, torch.Tensor) and t.dtype is self.io and t.shape == shape and
+                t.get_device() == self.index >= 0):
+            if t.is_contiguous():
+                return t.data_ptr(), H * dh
+            st = t.stride()  # part of the columns of one tensor
+            if (st[-1] == 1 and st[-2] == dh and st[-3] >= H * dh and
+                    (len(shape) == 3 or len(shape) == 4 and st[0] == st[1] * shape[1])):
+                return t.data_ptr(), st[-3]
         if not isinstance(t, torch.Tensor):
             raise TypeError(f"{name}: expected a torch.Tensor")
-        _shape(t, lead + (H, dh), name)
+        _shape(t, shape, name)
         if t.dtype != self.io:
             raise ValueError(f"{name}: expected {self.io}, got {t.dtype}")
-        if not t.is_cuda or t.device != self.device:
-            raise ValueError(f"{name}: must be a device tensor on {self.device}, is on {t.device}")
+        if not t.is_cuda or t.get_device() != self.index:
+            raise ValueError(f"{name}: must be a device tensor on device {self.index}, is on {t.device}")
         st = t.stride()
         if (dh > 1 and st[-1] != 1) or (H > 1 and st[-2] != dh):
             raise ValueError(f"{name}: the heads of a token must be contiguous")
         step, reach = H * dh, None  # the innermost leading dimension longer than 1 gives the stride
-        for n, d in zip(reversed(lead), reversed(st[:-2])):
+        for n, d in zip(shape[-3::-1], st[-3::-1]):
             if n == 1:
                 continue
             if reach is None:
@@ -439,18 +461,17 @@ class _Call:
         """fn(*args, stream) on the call's device; `keep`: tensors allocated for it here."""
         s = self.stream
         if s is None:
-            s = torch.cuda.current_stream(self.device).cuda_stream
+            s = _raw_stream(self.index)
         else:
             if not isinstance(s, torch.cuda.Stream):
-                s = torch.cuda.ExternalStream(int(s), device=self.device)
+                s = torch.cuda.ExternalStream(int(s), device=self.index)
             for t in keep:  # from the current stream's pool: not reused before this stream is done
-                if t is not None:
-                    t.record_stream(s)
+                t.record_stream(s)
             s = s.cuda_stream
-        if self.device.index == torch.cuda.current_device():
+        if self.index == torch.cuda.current_device():
             status = fn(*args, s)
         else:
-            with torch.cuda.device(self.device):
+            with torch.cuda.device(self.index):
                 status = fn(*args, s)
         if status != RGLRU_OK:
             raise RglruError(status, where)
@@ -461,7 +482,13 @@ def _heads_of(t, name):
         raise TypeError(f"{name}: expected a torch.Tensor")
     if t.dim() < 3:
         raise ValueError(f"{name}: expected [..., heads, dh], got shape {tuple(t.shape)}")
-    return tuple(t.shape[:-2]), t.shape[-2], t.shape[-1]
+    shape = tuple(t.shape)
+    return shape, shape[:-2], shape[-2], shape[-1]
+
+
+def _int32(n):
+    n = int(n)
+    return n if n < 0x7FFFFFFF else 0x7FFFFFFF
 
 
 def _bytes(t):
@@ -473,17 +500,18 @@ def rglru_qk_norm_rope(q, k, positions, inv_freq, q_out, k_out, q_w=None, k_w=No
     """q [..., Hq, dh], k, v [..., Hkv, dh]; positions int32 and slots int64 [...]; inv_freq f32
     [rot / 2]; k_pages, v_pages [pages, page, Hkv, dh]. k_out may be None with slots."""
     c = _Call(q, "q", stream)
-    lead, Hq, dh = _heads_of(q, "q")
-    Hkv = _heads_of(k, "k")[1]
+    qshape, lead, Hq, dh = _heads_of(q, "q")
+    Hkv = _heads_of(k, "k")[2]
+    kshape = lead + (Hkv, dh)
     f32 = torch.float32
     rows = positions.numel()
     rot = 0 if inv_freq is None else 2 * inv_freq.numel()
-    qp, qs = c.heads(q, lead, Hq, dh, "q")
-    kp, ks = c.heads(k, lead, Hkv, dh, "k")
-    qop, qos = c.heads(q_out, lead, Hq, dh, "q_out")
-    kop, kos = c.heads(k_out, lead, Hkv, dh, "k_out")
-    n_slots = 0
-    vp = vs = kpp = vpp = sp = None
+    qp, qs = c.heads(q, qshape, "q")
+    kp, ks = c.heads(k, kshape, "k")
+    qop, qos = c.heads(q_out, qshape, "q_out")
+    kop, kos = c.heads(k_out, kshape, "k_out")
+    n_slots = vs = 0
+    vp = kpp = vpp = sp = None
     if slots is not None:
         if k_pages is None or v_pages is None or v is None:
             raise ValueError("slots: needs v, k_pages and v_pages")
@@ -491,7 +519,7 @@ def rglru_qk_norm_rope(q, k, positions, inv_freq, q_out, k_out, q_w=None, k_w=No
             raise ValueError(f"k_pages: expected [pages, page, Hkv, dh], got {tuple(k_pages.shape)}")
         pool = (k_pages.shape[0], k_pages.shape[1], Hkv, dh)
         n_slots = pool[0] * pool[1]
-        vp, vs = c.heads(v, lead, Hkv, dh, "v")
+        vp, vs = c.heads(v, kshape, "v")
         kpp = c.flat(k_pages, c.io, pool, "k_pages")
         vpp = c.flat(v_pages, c.io, pool, "v_pages")
         sp = c.flat(slots, torch.int64, lead, "slots")
@@ -501,7 +529,7 @@ def rglru_qk_norm_rope(q, k, positions, inv_freq, q_out, k_out, q_w=None, k_w=No
           c.flat(q_w, f32, (dh,), "q_w"), c.flat(k_w, f32, (dh,), "k_w"),
           c.flat(inv_freq, f32, (rot // 2,), "inv_freq"),
           c.flat(positions, torch.int32, lead, "positions"), sp, qop, kop, kpp, vpp, rows, Hq, Hkv,
-          dh, rot, qs, ks, vs or 0, qos, kos, n_slots, eps, _dt(c.io), keep=_keep)
+          dh, rot, qs, ks, vs, qos, kos, n_slots, eps, _dt(c.io), keep=_keep)
 
 
 def qk_norm_rope(q, k, positions, inv_freq, q_w=None, k_w=None, eps=1e-6, v=None, k_pages=None,
@@ -509,10 +537,10 @@ def qk_norm_rope(q, k, positions, inv_freq, q_w=None, k_w=None, eps=1e-6, v=None
     """Returns (q_out, k_out), new contiguous tensors unless given (q and k themselves: in place)."""
     new = []
     if q_out is None:
-        q_out = torch.empty(q.shape, dtype=q.dtype, device=q.device)
+        q_out = torch.empty_like(q, memory_format=torch.contiguous_format)
         new.append(q_out)
     if k_out is None:
-        k_out = torch.empty(k.shape, dtype=k.dtype, device=k.device)
+        k_out = torch.empty_like(k, memory_format=torch.contiguous_format)
         new.append(k_out)
     rglru_qk_norm_rope(q, k, positions, inv_freq, q_out, k_out, q_w, k_w, eps, v, k_pages, v_pages,
                        slots, stream, _keep=new)
@@ -527,14 +555,15 @@ def rglru_qk_norm_rope_backward(q, k, positions, inv_freq, dq_out, dk_out, dq, d
                                 k_w=None, dq_w=None, dk_w=None, eps=1e-6, workspace=None,
                                 stream=None, _keep=()):
     c = _Call(q, "q", stream)
-    lead, Hq, dh = _heads_of(q, "q")
-    Hkv = _heads_of(k, "k")[1]
+    qshape, lead, Hq, dh = _heads_of(q, "q")
+    Hkv = _heads_of(k, "k")[2]
+    kshape = lead + (Hkv, dh)
     f32 = torch.float32
     rot = 0 if inv_freq is None else 2 * inv_freq.numel()
     ptrs, strides = [], []
-    for t, H, name in ((q, Hq, "q"), (k, Hkv, "k"), (dq_out, Hq, "dq_out"),
-                       (dk_out, Hkv, "dk_out"), (dq, Hq, "dq"), (dk, Hkv, "dk")):
-        p, st = c.heads(t, lead, H, dh, name)
+    for t, shape, name in ((q, qshape, "q"), (k, kshape, "k"), (dq_out, qshape, "dq_out"),
+                           (dk_out, kshape, "dk_out"), (dq, qshape, "dq"), (dk, kshape, "dk")):
+        p, st = c.heads(t, shape, name)
         ptrs.append(p)
         strides.append(st)
     wsb = _bytes(workspace)
@@ -544,7 +573,7 @@ def rglru_qk_norm_rope_backward(q, k, positions, inv_freq, dq_out, dk_out, dq, d
           c.flat(positions, torch.int32, lead, "positions"), *ptrs[2:],
           c.flat(dq_w, f32, (dh,), "dq_w"), c.flat(dk_w, f32, (dh,), "dk_w"), positions.numel(), Hq,
           Hkv, dh, rot, *strides, eps, _dt(c.io),
-          c.flat(workspace, None, None if workspace is None else workspace.shape, "workspace"), wsb,
+          c.flat(workspace, None, None, "workspace"), wsb,
           keep=_keep)
 
 
@@ -577,24 +606,25 @@ def rglru_local_attention(q, k, v, o, window, sinks=0, lens=None, scale=0.0, lse
     """q [B,T,Hq,dh], k, v [B,T,Hkv,dh], o as q and contiguous, bf16; lens int32 [B]; lse f32
     [B,Hq,T]."""
     c = _Call(q, "q", stream)
-    lead, Hq, dh = _heads_of(q, "q")
+    qshape, lead, Hq, dh = _heads_of(q, "q")
     if len(lead) != 2:
-        raise ValueError(f"q: expected [B, T, Hq, dh], got shape {tuple(q.shape)}")
+        raise ValueError(f"q: expected [B, T, Hq, dh], got shape {qshape}")
     B, T = lead
-    Hkv = _heads_of(k, "k")[1]
-    qp, qs = c.heads(q, lead, Hq, dh, "q")
-    kp, ks = c.heads(k, lead, Hkv, dh, "k")
-    vp, vs = c.heads(v, lead, Hkv, dh, "v")
+    Hkv = _heads_of(k, "k")[2]
+    kshape = (B, T, Hkv, dh)
+    qp, qs = c.heads(q, qshape, "q")
+    kp, ks = c.heads(k, kshape, "k")
+    vp, vs = c.heads(v, kshape, "v")
     c.run("rglru_local_attention", _lib.rglru_local_attention, qp, kp, vp,
-          c.flat(lens, torch.int32, (B,), "lens"), c.flat(o, c.io, (B, T, Hq, dh), "o"),
+          c.flat(lens, torch.int32, (B,), "lens"), c.flat(o, c.io, qshape, "o"),
           c.flat(lse, torch.float32, (B, Hq, T), "lse"), B, T, Hq, Hkv, dh, qs, ks, vs,
-          min(int(window), 0x7FFFFFFF), min(int(sinks), 0x7FFFFFFF), float(scale), _dt(c.io),
+          _int32(window), _int32(sinks), float(scale), _dt(c.io),
           keep=_keep)
 
 
 def local_attention(q, k, v, window, sinks=0, lens=None, scale=0.0, want_lse=False, stream=None):
     """Returns o [B,T,Hq,dh] (bf16), or (o, lse) with lse f32 [B,Hq,T], which the backward needs."""
-    new = [torch.empty(q.shape, dtype=q.dtype, device=q.device)]
+    new = [torch.empty_like(q, memory_format=torch.contiguous_format)]
     if want_lse:
         B, T, Hq, _ = q.shape
         new.append(torch.empty((B, Hq, T), dtype=torch.float32, device=q.device))
@@ -605,28 +635,28 @@ def local_attention(q, k, v, window, sinks=0, lens=None, scale=0.0, want_lse=Fal
 
 def rglru_local_attention_backward_workspace_size(B, T, Hq, Hkv, dh, window, sinks=0) -> int:
     return int(_lib.rglru_local_attention_backward_workspace_size(
-        B, T, Hq, Hkv, dh, min(int(window), 0x7FFFFFFF), min(int(sinks), 0x7FFFFFFF)))
+        B, T, Hq, Hkv, dh, _int32(window), _int32(sinks)))
 
 
 def rglru_local_attention_backward(q, k, v, o, lse, do, dq, dk, dv, window, sinks=0, lens=None,
                                    scale=0.0, workspace=None, stream=None, _keep=()):
     """o, do as q and contiguous; dq as q, dk and dv as k (slices of a packed gradient are fine)."""
     c = _Call(q, "q", stream)
-    lead, Hq, dh = _heads_of(q, "q")
+    qshape, lead, Hq, dh = _heads_of(q, "q")
     if len(lead) != 2:
-        raise ValueError(f"q: expected [B, T, Hq, dh], got shape {tuple(q.shape)}")
+        raise ValueError(f"q: expected [B, T, Hq, dh], got shape {qshape}")
     B, T = lead
-    Hkv = _heads_of(k, "k")[1]
-    (qp, qs), (dqp, dqs) = c.heads(q, lead, Hq, dh, "q"), c.heads(dq, lead, Hq, dh, "dq")
+    Hkv = _heads_of(k, "k")[2]
+    kshape = (B, T, Hkv, dh)
+    (qp, qs), (dqp, dqs) = c.heads(q, qshape, "q"), c.heads(dq, qshape, "dq")
     (kp, ks), (vp, vs), (dkp, dks), (dvp, dvs) = (
-        c.heads(t, lead, Hkv, dh, n) for t, n in ((k, "k"), (v, "v"), (dk, "dk"), (dv, "dv")))
-    full = (B, T, Hq, dh)
+        c.heads(t, kshape, n) for t, n in ((k, "k"), (v, "v"), (dk, "dk"), (dv, "dv")))
     c.run("rglru_local_attention_backward", _lib.rglru_local_attention_backward, qp, kp, vp,
-          c.flat(lens, torch.int32, (B,), "lens"), c.flat(o, c.io, full, "o"),
-          c.flat(lse, torch.float32, (B, Hq, T), "lse"), c.flat(do, c.io, full, "do"), dqp, dkp, dvp,
-          B, T, Hq, Hkv, dh, qs, ks, vs, dqs, dks, dvs, min(int(window), 0x7FFFFFFF),
-          min(int(sinks), 0x7FFFFFFF), float(scale), _dt(c.io),
-          c.flat(workspace, None, None if workspace is None else workspace.shape, "workspace"),
+          c.flat(lens, torch.int32, (B,), "lens"), c.flat(o, c.io, qshape, "o"),
+          c.flat(lse, torch.float32, (B, Hq, T), "lse"), c.flat(do, c.io, qshape, "do"), dqp, dkp, dvp,
+          B, T, Hq, Hkv, dh, qs, ks, vs, dqs, dks, dvs, _int32(window),
+          _int32(sinks), float(scale), _dt(c.io),
+          c.flat(workspace, None, None, "workspace"),
           _bytes(workspace), keep=_keep)
 
 
@@ -652,11 +682,12 @@ def local_attention_backward(q, k, v, o, lse, do, window, sinks=0, lens=None, sc
     return {"dq": dq, "dk": dk, "dv": dv}
 
 
+@functools.lru_cache(maxsize=256)
 def rglru_paged_attention_workspace_size(N, Hq, Hkv, dh, page_size, max_pages, window, sinks,
                                          dtype) -> int:
     return int(_lib.rglru_paged_attention_workspace_size(
-        N, Hq, Hkv, dh, page_size, max_pages, min(int(window), 0x7FFFFFFF),
-        min(int(sinks), 0x7FFFFFFF), _dt(dtype)))
+        N, Hq, Hkv, dh, page_size, max_pages, _int32(window),
+        _int32(sinks), _dt(dtype)))
 
 
 def rglru_paged_attention(q, k_pages, v_pages, block_table, lens, o, window, sinks=0, scale=0.0,
@@ -664,28 +695,28 @@ def rglru_paged_attention(q, k_pages, v_pages, block_table, lens, o, window, sin
     """q [N,Hq,dh], k_pages, v_pages [pages,page,Hkv,dh] of one type (bf16 or f32); block_table
     int32 [N,max_pages], lens int32 [N]; o as q and contiguous."""
     c = _Call(q, "q", stream)
-    lead, Hq, dh = _heads_of(q, "q")
+    qshape, lead, Hq, dh = _heads_of(q, "q")
     if len(lead) != 1:
-        raise ValueError(f"q: expected [N, Hq, dh], got shape {tuple(q.shape)}")
+        raise ValueError(f"q: expected [N, Hq, dh], got shape {qshape}")
     if k_pages.dim() != 4 or block_table.dim() != 2:
         raise ValueError("k_pages: expected [pages, page, Hkv, dh]; block_table: [N, max_pages]")
     pages, page, Hkv, _ = k_pages.shape
     N, pool = lead[0], (pages, page, Hkv, dh)
-    qp, qs = c.heads(q, lead, Hq, dh, "q")
+    qp, qs = c.heads(q, qshape, "q")
     c.run("rglru_paged_attention", _lib.rglru_paged_attention, qp,
           c.flat(k_pages, c.io, pool, "k_pages"), c.flat(v_pages, c.io, pool, "v_pages"),
           c.flat(block_table, torch.int32, (N, block_table.shape[1]), "block_table"),
-          c.flat(lens, torch.int32, (N,), "lens"), c.flat(o, c.io, (N, Hq, dh), "o"), N, Hq, Hkv, dh,
-          qs, pages, page, block_table.shape[1], min(int(window), 0x7FFFFFFF),
-          min(int(sinks), 0x7FFFFFFF), float(scale), _dt(c.io),
-          c.flat(workspace, None, None if workspace is None else workspace.shape, "workspace"),
+          c.flat(lens, torch.int32, (N,), "lens"), c.flat(o, c.io, qshape, "o"), N, Hq, Hkv, dh,
+          qs, pages, page, block_table.shape[1], _int32(window),
+          _int32(sinks), float(scale), _dt(c.io),
+          c.flat(workspace, None, None, "workspace"),
           _bytes(workspace), keep=_keep)
 
 
 def paged_attention(q, k_pages, v_pages, block_table, lens, window, sinks=0, scale=0.0,
                     workspace=None, stream=None):
     """Returns o [N,Hq,dh] of q's type."""
-    new = [torch.empty(q.shape, dtype=q.dtype, device=q.device)]
+    new = [torch.empty_like(q, memory_format=torch.contiguous_format)]
     if workspace is None and q.dim() == 3 and k_pages.dim() == 4 and block_table.dim() == 2:
         n = rglru_paged_attention_workspace_size(q.shape[0], q.shape[1], k_pages.shape[2],
                                                  q.shape[2], k_pages.shape[1],

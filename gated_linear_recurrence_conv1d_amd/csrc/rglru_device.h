@@ -211,6 +211,12 @@ template <typename P> __device__ __forceinline__ P *wave_uniform(P *p) {
   return reinterpret_cast<P *>((static_cast<uint64_t>(hi) << 32) | lo);
 }
 
+// A value of a table that the kernel does not write, at a wave-uniform place: by scalar load.
+template <typename V> __device__ __forceinline__ V uniform_load(const V *p, long long i) {
+  typedef const __attribute__((address_space(4))) V *const_ptr;
+  return ((const_ptr)p)[i];
+}
+
 // Workgroup barrier that orders LDS accesses only: unlike __syncthreads it does not wait for the
 // wave's outstanding vector memory loads and stores, so they stay in flight across it.
 __device__ __forceinline__ void lds_barrier() {

@@ -70,7 +70,8 @@ template <int KEYS> __host__ __device__ inline Walk walk_of(int len, int W, int 
 
 }  // namespace
 
-// UNI: the page size is a multiple of the tile's keys, so that a tile lies on one page.
+// UNI: the page size is a multiple of 16, so that 16 aligned keys lie on one page: their rows' address
+// is wave-uniform (one scalar table load) plus a constant offset per lane.
 template <typename T, int DH, bool UNI>
 __global__ __launch_bounds__(64 * kPgWaves, 2) void paged_fwd(PagedArgs a, int chunk, int splits) {
   typedef Paged<T, DH> M;
@@ -86,16 +87,16 @@ __global__ __launch_bounds__(64 * kPgWaves, 2) void paged_fwd(PagedArgs a, int c
   const int h0 = (blockIdx.y - kvh * gt) * 16;  // first head of the group's part
   const int nh = min(16, G - h0);
   const int hq = kvh * G + h0;                  // first query head
-  const int raw = a.lens[n];
+  const int raw = uniform_load(a.lens, n);
   const long long cap = static_cast<long long>(a.max_pages) * a.page;
   const bool bad_len = raw < 0 || raw > cap;
   const Walk wk = walk_of<M::kKeys>(bad_len ? 0 : raw, a.window, a.sinks);
   const int t_end = min(wk.nt, (sp + 1) * chunk);
   if (sp > 0 && sp * chunk >= wk.nt) return;    // no such chunk (chunk 0 also serves empty rows)
   const int *table = a.table + static_cast<size_t>(n) * a.max_pages;
-  const size_t row_elems = static_cast<size_t>(a.Hkv) * DH;
-  const T *kp = static_cast<const T *>(a.k_pages) + static_cast<size_t>(kvh) * DH;
-  const T *vp = static_cast<const T *>(a.v_pages) + static_cast<size_t>(kvh) * DH;
+  const size_t row_bytes = static_cast<size_t>(a.Hkv) * DH * sizeof(T);
+  const char *kp = static_cast<const char *>(a.k_pages) + static_cast<size_t>(kvh) * DH * sizeof(T);
+  const char *vp = static_cast<const char *>(a.v_pages) + static_cast<size_t>(kvh) * DH * sizeof(T);
 
   // Q^T operand: head column c16 (heads past the group read the last one; never stored)
   u32x4_t qf[M::kKS];
@@ -114,34 +115,42 @@ __global__ __launch_bounds__(64 * kPgWaves, 2) void paged_fwd(PagedArgs a, int c
   auto tile_base = [&](int i) { return (i < wk.ns ? i : i - wk.ns + wk.win) * M::kKeys; };
   auto seen = [&](int u) { return u < wk.len && (u >= wk.w0 || u < a.sinks); };
 
-  // Where tile i's rows are: UNI one page (its first row, wave-uniform), else a row per key.
+  // Where tile i's rows are: UNI the first row of each 16 keys (wave-uniform), else a row per key.
   struct At {
-    size_t base;               // UNI: element offset of the tile's first key row
+    size_t base[M::kSub];      // UNI: byte offset of the 16 keys' first row
     int krow[M::kSub];         // else: pool rows of this lane's K keys and V keys
     int vrow[M::kVK];
-  };
-  auto page_of = [&](int u) {  // table entry of position u, valid for u < len; 0 and bad outside
-    const int p = table[u / a.page];
-    const bool ok = p >= 0 && p < a.num_pages;
-    return ok ? p : -1;
   };
   auto locate = [&](int i) {
     At at;
     const int u0 = tile_base(i);
     if constexpr (UNI) {
-      // a tile of the walk has a visible position, so its page has to be there
-      int p = __builtin_amdgcn_readfirstlane(page_of(u0));
-      if (p < 0) bad = 1;
-      at.base = (static_cast<size_t>(max(p, 0)) * a.page + u0 % a.page) * row_elems;
+#pragma unroll
+      for (int s = 0; s < M::kSub; ++s) {
+        const int u = u0 + 16 * s;
+        // some of the 16 visible? (if not, their page need not be there: row 0 stands in)
+        const bool need = u < wk.len && (u + 16 > wk.w0 || u < a.sinks);
+        int page = 0, first = 0;
+        if (need) {
+          const int t = u / a.page;
+          page = uniform_load(table, t);
+          first = u - t * a.page;
+          if (page < 0 || page >= a.num_pages) {
+            bad = 1;
+            page = first = 0;
+          }
+        }
+        at.base[s] = (static_cast<size_t>(page) * a.page + first) * row_bytes;
+      }
     } else {
       const int u = u0 + (lane & (M::kKeys - 1));
       int row = 0;
       if (seen(u)) {
-        const int p = page_of(u);
-        if (p < 0)
+        const int t = u / a.page, p = table[t];
+        if (p < 0 || p >= a.num_pages)
           bad = 1;
         else
-          row = p * a.page + u % a.page;
+          row = p * a.page + (u - t * a.page);
       }
 #pragma unroll
       for (int s = 0; s < M::kSub; ++s) at.krow[s] = __shfl(row, 16 * s + c16, 64);
@@ -152,34 +161,37 @@ __global__ __launch_bounds__(64 * kPgWaves, 2) void paged_fwd(PagedArgs a, int c
   };
   u32x4_t kf[M::kSub][M::kKS];
   uint32_t vf[M::kVK][M::kVB][M::kVW];
+  const unsigned kof = static_cast<unsigned>(c16 * row_bytes) + g * 16;
+  const unsigned vof = static_cast<unsigned>(4 * g * row_bytes) + c16 * (M::kE * sizeof(T));
   auto load_k = [&](const At &at) {
 #pragma unroll
     for (int s = 0; s < M::kSub; ++s) {
-      const T *p;
+      const char *p;
       if constexpr (UNI)
-        p = kp + at.base + (static_cast<size_t>(16 * s + c16) * row_elems + g * (M::kDims / 4));
+        p = wave_uniform(kp + at.base[s]) + kof;
       else
-        p = kp + static_cast<size_t>(at.krow[s]) * row_elems + g * (M::kDims / 4);
+        p = kp + static_cast<size_t>(at.krow[s]) * row_bytes + g * 16;
 #pragma unroll
-      for (int i = 0; i < M::kKS; ++i) kf[s][i] = *reinterpret_cast<const u32x4_t *>(p + i * M::kDims);
+      for (int i = 0; i < M::kKS; ++i) kf[s][i] = *reinterpret_cast<const u32x4_t *>(p + i * 64);
     }
   };
   auto load_v = [&](const At &at) {
 #pragma unroll
     for (int k = 0; k < M::kVK; ++k) {
-      const T *p;
+      const char *p;
       if constexpr (UNI)
-        p = vp + at.base + (static_cast<size_t>(16 * (k >> 2) + 4 * g + (k & 3)) * row_elems + c16 * M::kE);
+        p = wave_uniform(vp + at.base[k >> 2] + (k & 3) * row_bytes) + vof;
       else
-        p = vp + static_cast<size_t>(at.vrow[k]) * row_elems + c16 * M::kE;
+        p = vp + static_cast<size_t>(at.vrow[k]) * row_bytes + c16 * (M::kE * sizeof(T));
 #pragma unroll
       for (int b = 0; b < M::kVB; ++b) {
+        const char *pb = p + b * 16 * M::kE * sizeof(T);
         if constexpr (M::kVW == 4) {
-          const u32x4_t v = *reinterpret_cast<const u32x4_t *>(p + b * 16 * M::kE);
+          const u32x4_t v = *reinterpret_cast<const u32x4_t *>(pb);
 #pragma unroll
           for (int e = 0; e < 4; ++e) vf[k][b][e] = v[e];
         } else {
-          const u32x2_t v = *reinterpret_cast<const u32x2_t *>(p + b * 16 * M::kE);
+          const u32x2_t v = *reinterpret_cast<const u32x2_t *>(pb);
           vf[k][b][0] = v[0];
           vf[k][b][1] = v[1];
         }
@@ -339,40 +351,65 @@ __global__ __launch_bounds__(64 * kPgWaves, 2) void paged_fwd(PagedArgs a, int c
 // 64 lanes with DH / 64 values each.
 template <typename T, int DH>
 __global__ __launch_bounds__(256) void paged_join(PagedArgs a, int chunk, int splits) {
-  constexpr int V = DH / 64;
+  constexpr int V = DH / 64, kAt = 4;
   __shared__ float ro[4][DH], rl[4], rm[4];
   const int n = blockIdx.x / a.Hq, h = blockIdx.x - n * a.Hq;
   const int lane = threadIdx.x & 63, w = threadIdx.x >> 6;
-  const int raw = a.lens[n];
+  const int raw = uniform_load(a.lens, n);
+  const size_t r0 = static_cast<size_t>(n) * splits * a.Hq + h;
+  float m = a.floor, l = 0.0f, acc[V] = {};
+  float2 st[kAt];
+  float x[kAt][V];
+  auto load = [&](int s0) {
+#pragma unroll
+    for (int j = 0; j < kAt; ++j) {
+      const size_t r = r0 + static_cast<size_t>(min(s0 + 4 * j, splits - 1)) * a.Hq;
+      st[j] = *reinterpret_cast<const float2 *>(a.stat + 2 * r);
+#pragma unroll
+      for (int i = 0; i < V; ++i) x[j][i] = a.part[r * DH + lane + 64 * i];
+    }
+  };
+  // the first chunks are read before the length says how many there are (what is not used may hold
+  // anything): one round trip less for the common few chunks
+  load(w);
   if (raw < 0 || raw > static_cast<long long>(a.max_pages) * a.page) return;
   const Walk wk = walk_of<Paged<T, DH>::kKeys>(raw, a.window, a.sinks);
-  if (wk.nt <= chunk) return;
+  if (wk.nt <= chunk) return;  // not split, or empty
   const int used = (wk.nt + chunk - 1) / chunk;
-  const size_t r0 = static_cast<size_t>(n) * splits * a.Hq + h;
-  float m = a.floor;
-  for (int s = w * 64 + lane; s < used; s += 256) m = fmaxf(m, a.stat[2 * (r0 + static_cast<size_t>(s) * a.Hq)]);
+  for (int s0 = w; s0 < used; s0 += 4 * kAt) {
+    if (s0 != w) load(s0);
 #pragma unroll
-  for (int o = 1; o < 64; o <<= 1) m = fmaxf(m, __shfl_xor(m, o, 64));
-  if (lane == 0) rm[w] = m;
-  __syncthreads();
-  m = fmaxf(fmaxf(rm[0], rm[1]), fmaxf(rm[2], rm[3]));
-  float acc[V] = {}, l = 0.0f;
-#pragma unroll 4
-  for (int s = w; s < used; s += 4) {
-    const size_t r = r0 + static_cast<size_t>(s) * a.Hq;
-    const float f = __builtin_amdgcn_exp2f((a.stat[2 * r] - m) * a.c);
-    l = fmaf(a.stat[2 * r + 1], f, l);
+    for (int j = 0; j < kAt; ++j) {
+      if (s0 + 4 * j >= used) continue;
+      const float mn = fmaxf(m, st[j].x);
+      const float fo = __builtin_amdgcn_exp2f((m - mn) * a.c);
+      const float fn = __builtin_amdgcn_exp2f((st[j].x - mn) * a.c);
+      m = mn;
+      l = fmaf(st[j].y, fn, l * fo);
 #pragma unroll
-    for (int i = 0; i < V; ++i) acc[i] = fmaf(a.part[r * DH + lane + 64 * i], f, acc[i]);
+      for (int i = 0; i < V; ++i) acc[i] = fmaf(x[j][i], fn, acc[i] * fo);
+    }
   }
 #pragma unroll
   for (int i = 0; i < V; ++i) ro[w][lane + 64 * i] = acc[i];
-  if (lane == 0) rl[w] = l;
+  if (lane == 0) {
+    rl[w] = l;
+    rm[w] = m;
+  }
   __syncthreads();
-  const float lt = (rl[0] + rl[1]) + (rl[2] + rl[3]);
-  for (int d = threadIdx.x; d < DH; d += 256)
-    Elem<T>::store(static_cast<T *>(a.o), (static_cast<size_t>(n) * a.Hq + h) * DH + d,
-                   ((ro[0][d] + ro[1][d]) + (ro[2][d] + ro[3][d])) / lt);
+  const float mt = fmaxf(fmaxf(rm[0], rm[1]), fmaxf(rm[2], rm[3]));
+  float f[4], lt = 0.0f;
+#pragma unroll
+  for (int k = 0; k < 4; ++k) {
+    f[k] = __builtin_amdgcn_exp2f((rm[k] - mt) * a.c);
+    lt = fmaf(rl[k], f[k], lt);
+  }
+  for (int d = threadIdx.x; d < DH; d += 256) {
+    float o = 0.0f;
+#pragma unroll
+    for (int k = 0; k < 4; ++k) o = fmaf(ro[k][d], f[k], o);
+    Elem<T>::store(static_cast<T *>(a.o), (static_cast<size_t>(n) * a.Hq + h) * DH + d, o / lt);
+  }
 }
 
 // Tiles per chunk and the most chunks a row can have. Chunks of 4 tiles (one per wave) at least;
@@ -387,7 +424,7 @@ PagedPlan paged_plan(int N, int Hq, int Hkv, long long max_len, int window, int 
       (static_cast<long long>(len) + keys - 1) / keys,
       (static_cast<long long>(std::min(window, len)) + keys - 1) / keys + 1 + w.ns);
   const long long groups = static_cast<long long>(N) * Hkv * ((G + 15) / 16);
-  constexpr long long kTarget = 1024;  // workgroups: 2 fit a CU at a time
+  constexpr long long kTarget = 512;  // workgroups: two fit a CU at a time (registers, LDS)
   long long chunk = (most * groups + kTarget - 1) / kTarget;
   chunk = std::max<long long>((chunk + kPgWaves - 1) / kPgWaves * kPgWaves, kPgWaves);
   PagedPlan p;
@@ -402,7 +439,7 @@ namespace {
 template <typename T, int DH> hipError_t launch(const PagedArgs &a, const PagedPlan &p, hipStream_t s) {
   const int G = a.Hq / a.Hkv;
   const dim3 grid(static_cast<unsigned>(a.N) * p.splits, a.Hkv * ((G + 15) / 16));
-  if (a.page % Paged<T, DH>::kKeys == 0)
+  if (a.page % 16 == 0)
     paged_fwd<T, DH, true><<<grid, 64 * kPgWaves, 0, s>>>(a, p.chunk, p.splits);
   else
     paged_fwd<T, DH, false><<<grid, 64 * kPgWaves, 0, s>>>(a, p.chunk, p.splits);

@@ -14,9 +14,11 @@
 // Both directions read and write each value once and are bound by memory. A head's values are
 // held as chunk pairs: lane c of a head's dh / (2 E) lanes has the 16-byte chunk (E values) of
 // pair elements i and the chunk of their partners i + rot / 2, so that the rotation needs no
-// exchange, and the norm's sum crosses 4..32 lanes only. A lane keeps its chunk index over all
-// heads and rows, hence its weights and frequencies stay in registers and its angles are formed
-// once per row for all heads.
+// exchange, and the norm's sum crosses 4..32 lanes only. A wave works through a run of (row, pass)
+// items, a pass being 64 / LPH heads of one row, with the next items' loads in flight (a ring of
+// kAhead items: without it a wave waits for memory once per pass; 79 us against RING_FWD at B8 T2048
+// Hq10 dh256 bf16); a row's angles are formed once for all its passes. Weights and frequencies stay in
+// LDS: in registers they would halve the number of waves.
 #include "rglru_launch.h"
 #include "rglru_mfma.h"
 
@@ -77,10 +79,19 @@ template <> struct Chunk<float> {
   }
 };
 
-// Sum over groups of N neighbouring lanes (N a power of two), the result in every lane.
+// Sum over groups of N neighbouring lanes (N a power of two), the result in every lane: within 16
+// lanes by data-parallel moves (neighbours, pairs, quads by a half-row mirror, eights by a row
+// mirror), beyond by lane exchanges.
+template <int CTRL> __device__ __forceinline__ float dpp_add(float v) {
+  return v + __int_as_float(__builtin_amdgcn_update_dpp(0, __float_as_int(v), CTRL, 0xF, 0xF, true));
+}
 template <int N> __device__ __forceinline__ float group_sum(float v) {
+  if constexpr (N > 1) v = dpp_add<0xB1>(v);   // quad_perm 1,0,3,2
+  if constexpr (N > 2) v = dpp_add<0x4E>(v);   // quad_perm 2,3,0,1
+  if constexpr (N > 4) v = dpp_add<0x141>(v);  // row_half_mirror
+  if constexpr (N > 8) v = dpp_add<0x140>(v);  // row_mirror
 #pragma unroll
-  for (int o = 1; o < N; o <<= 1) v += __shfl_xor(v, o, 64);
+  for (int o = 16; o < N; o <<= 1) v += __shfl_xor(v, o, 64);
   return v;
 }
 
@@ -88,104 +99,165 @@ constexpr int kRopeWaves = 4;  // waves per workgroup
 
 }  // namespace
 
-// A wave takes (row, part) tasks: parts of a row share its head passes (a pass: 64 / LPH heads of
-// q, of k, or of v on its way to the cache). With many rows a wave takes whole rows.
-template <typename T, int LPH>
-__global__ __launch_bounds__(64 * kRopeWaves) void qk_rope_fwd(RopeArgs a, int parts) {
-  constexpr int E = Chunk<T>::E;
-  constexpr int HPP = 64 / LPH;  // heads per pass
-  constexpr int DH = 2 * E * LPH;
-  const int lane = threadIdx.x & 63;
-  const int c = lane % LPH, hsub = lane / LPH;
-  const int half = a.rot / 2;
-  const bool rotated = c * E < half;
-  const int lo = rotated ? c * E : a.rot + 2 * (c * E - half);
-  const int hi = rotated ? lo + half : lo + E;
-  const bool norm = a.q_w != nullptr;
-  float wq[2 * E], wk[2 * E];
-  double fr[E];
-#pragma unroll
-  for (int e = 0; e < E; ++e) {
-    wq[e] = norm ? a.q_w[lo + e] : 1.0f;
-    wq[E + e] = norm ? a.q_w[hi + e] : 1.0f;
-    wk[e] = norm ? a.k_w[lo + e] : 1.0f;
-    wk[E + e] = norm ? a.k_w[hi + e] : 1.0f;
-    fr[e] = rotated ? static_cast<double>(a.inv_freq[c * E + e]) * kInvTwoPi : 0.0;
+// What a lane keeps through all items: its chunk pair's place in a head.
+template <typename T, int LPH> struct RopeLane {
+  static constexpr int E = Chunk<T>::E;
+  static constexpr int HPP = 64 / LPH;  // heads per pass
+  static constexpr int DH = 2 * E * LPH;
+  int c, hsub, lo, hi;
+  bool rotated;
+  __device__ __forceinline__ RopeLane(int rot) {
+    const int lane = threadIdx.x & 63;
+    c = lane % LPH;
+    hsub = lane / LPH;
+    const int half = rot / 2;
+    rotated = c * E < half;
+    lo = rotated ? c * E : rot + 2 * (c * E - half);
+    hi = rotated ? lo + half : lo + E;
   }
+  // sine and cosine of this lane's E angles (0 and 1 where it has none)
+  __device__ __forceinline__ void angles(int pos, const double *freq, float (&sn)[E],
+                                         float (&cs)[E]) const {
+#pragma unroll
+    for (int e = 0; e < E; ++e) sincos_turns<T>(turns_of(pos, freq[c * E + e]), sn[e], cs[e]);
+  }
+};
+
+// Weights (1 without norm) and frequencies in turns (0 beyond rot / 2) to LDS.
+template <int DH>
+__device__ __forceinline__ void stage_tables(const float *q_w, const float *k_w, const float *inv_freq,
+                                             int rot, float (&wl)[2][DH], double (&fl)[DH / 2]) {
+  for (int i = threadIdx.x; i < DH; i += 64 * kRopeWaves) {
+    wl[0][i] = q_w ? q_w[i] : 1.0f;
+    wl[1][i] = q_w ? k_w[i] : 1.0f;
+    if (i < DH / 2) fl[i] = i < rot / 2 ? static_cast<double>(inv_freq[i]) * kInvTwoPi : 0.0;
+  }
+  __syncthreads();
+}
+
+constexpr int kAhead = 4;     // items in flight per wave, forward
+constexpr int kAheadBwd = 2;  // and backward (twice the loads per item)
+
+// Items (row, pass), pass: heads of q, then of k, then of v on its way to the cache; wave i takes
+// items i per .. (i + 1) per - 1.
+template <typename T, int LPH>
+__global__ __launch_bounds__(64 * kRopeWaves) void qk_rope_fwd(RopeArgs a, int per) {
+  typedef RopeLane<T, LPH> L;
+  constexpr int E = L::E, HPP = L::HPP, DH = L::DH;
+  __shared__ float wl[2][DH];
+  __shared__ double fl[DH / 2];
+  stage_tables<DH>(a.q_w, a.k_w, a.inv_freq, a.rot, wl, fl);
+  const L me(a.rot);
+  const bool norm = a.q_w != nullptr;
   const int qp = (a.Hq + HPP - 1) / HPP, kp = (a.Hkv + HPP - 1) / HPP;
   const int passes = qp + kp + (a.slots ? kp : 0);
-  const long long tasks = static_cast<long long>(a.rows) * parts;
-  const long long nw = static_cast<long long>(gridDim.x) * kRopeWaves;
-  for (long long task = static_cast<long long>(blockIdx.x) * kRopeWaves + (threadIdx.x >> 6);
-       task < tasks; task += nw) {
-    const int row = static_cast<int>(task / parts);
-    const int part = static_cast<int>(task - static_cast<long long>(row) * parts);
-    const int pos = a.positions[row];
-    float sn[E], cs[E];
-#pragma unroll
-    for (int e = 0; e < E; ++e) sincos_turns<T>(turns_of(pos, fr[e]), sn[e], cs[e]);
-    long long slot = a.slots ? a.slots[row] : -1;
-    if (slot >= a.n_slots) slot = -1;
-    for (int p = part; p < passes; p += parts) {
-      const bool isq = p < qp, isv = p >= qp + kp;
-      const int h = (isq ? p : isv ? p - qp - kp : p - qp) * HPP + hsub;
-      const bool on = h < (isq ? a.Hq : a.Hkv);
+  const long long items = static_cast<long long>(a.rows) * passes;
+  const long long wave = static_cast<long long>(blockIdx.x) * kRopeWaves +
+                         __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const long long f0 = wave * per;
+  if (f0 >= items) return;
+  const int n = static_cast<int>(min(static_cast<long long>(per), items - f0));
+  struct Item {
+    u32x4_t lo, hi;
+  } ring[kAhead];
+  struct At {
+    int row, p;
+  };
+  const int row0 = static_cast<int>(f0 / passes);
+  At head = {row0, static_cast<int>(f0 - static_cast<long long>(row0) * passes)}, cur = head;
+  auto step = [&](At &at) {
+    if (++at.p == passes) {
+      at.p = 0;
+      ++at.row;
+    }
+  };
+  auto head_of = [&](int p) { return (p < qp ? p : p < qp + kp ? p - qp : p - qp - kp) * HPP + me.hsub; };
+  auto load = [&](Item &it) {
+    const bool isq = head.p < qp, isv = head.p >= qp + kp;
+    const int h = head_of(head.p);
+    it.lo = it.hi = u32x4_t{};
+    if (h < (isq ? a.Hq : a.Hkv)) {
       const T *src = static_cast<const T *>(isq ? a.q : isv ? a.v : a.k) +
-                     static_cast<size_t>(row) * (isq ? a.q_stride : isv ? a.v_stride : a.k_stride) +
+                     static_cast<size_t>(head.row) * (isq ? a.q_stride : isv ? a.v_stride : a.k_stride) +
                      static_cast<size_t>(h) * DH;
-      u32x4_t vl = {}, vh = {};
-      if (on) {
-        vl = *reinterpret_cast<const u32x4_t *>(src + lo);
-        vh = *reinterpret_cast<const u32x4_t *>(src + hi);
+      it.lo = *reinterpret_cast<const u32x4_t *>(src + me.lo);
+      it.hi = *reinterpret_cast<const u32x4_t *>(src + me.hi);
+    }
+    step(head);
+  };
+  int row = -1;
+  long long slot = -1;
+  float sn[E], cs[E];
+  auto process = [&](const Item &it) {
+    if (cur.row != row) {
+      row = cur.row;
+      me.angles(uniform_load(a.positions, row), fl, sn, cs);
+      slot = a.slots ? uniform_load(a.slots, row) : -1;
+      if (slot >= a.n_slots) slot = -1;
+    }
+    const bool isq = cur.p < qp, isv = cur.p >= qp + kp;
+    const int h = head_of(cur.p);
+    const bool on = h < (isq ? a.Hq : a.Hkv);
+    step(cur);
+    const size_t cache_at =
+        (static_cast<size_t>(slot < 0 ? 0 : slot) * a.Hkv + static_cast<size_t>(h)) * DH;
+    if (isv) {  // values go to the cache as they are
+      if (on && slot >= 0) {
+        T *dst = static_cast<T *>(a.v_pages) + cache_at;
+        *reinterpret_cast<u32x4_t *>(dst + me.lo) = it.lo;
+        *reinterpret_cast<u32x4_t *>(dst + me.hi) = it.hi;
       }
-      const size_t cache_at =
-          (static_cast<size_t>(slot < 0 ? 0 : slot) * a.Hkv + static_cast<size_t>(h)) * DH;
-      if (isv) {  // values go to the cache as they are
-        if (on && slot >= 0) {
-          T *dst = static_cast<T *>(a.v_pages) + cache_at;
-          *reinterpret_cast<u32x4_t *>(dst + lo) = vl;
-          *reinterpret_cast<u32x4_t *>(dst + hi) = vh;
-        }
-        continue;
-      }
-      float xl[E], xh[E];
-      Chunk<T>::unpack(vl, xl);
-      Chunk<T>::unpack(vh, xh);
-      if (norm) {
-        float ss = 0.0f;
+      return;
+    }
+    float xl[E], xh[E];
+    Chunk<T>::unpack(it.lo, xl);
+    Chunk<T>::unpack(it.hi, xh);
+    if (norm) {
+      float ss = 0.0f;
 #pragma unroll
-        for (int e = 0; e < E; ++e) ss = fmaf(xl[e], xl[e], fmaf(xh[e], xh[e], ss));
-        ss = group_sum<LPH>(ss);
-        const float r = 1.0f / sqrtf(fmaf(ss, 1.0f / DH, a.eps));
+      for (int e = 0; e < E; ++e) ss = fmaf(xl[e], xl[e], fmaf(xh[e], xh[e], ss));
+      ss = group_sum<LPH>(ss);
+      const float r = 1.0f / sqrtf(fmaf(ss, 1.0f / DH, a.eps));
+      const float *w = wl[isq ? 0 : 1];
 #pragma unroll
-        for (int e = 0; e < E; ++e) {
-          xl[e] *= r * (isq ? wq[e] : wk[e]);
-          xh[e] *= r * (isq ? wq[E + e] : wk[E + e]);
-        }
+      for (int e = 0; e < E; ++e) {
+        xl[e] *= r * w[me.lo + e];
+        xh[e] *= r * w[me.hi + e];
       }
-      if (rotated) {
+    }
+    if (me.rotated) {
 #pragma unroll
-        for (int e = 0; e < E; ++e) {
-          const float l = xl[e], g = xh[e];
-          xl[e] = l * cs[e] - g * sn[e];
-          xh[e] = g * cs[e] + l * sn[e];
-        }
+      for (int e = 0; e < E; ++e) {
+        const float l = xl[e], g = xh[e];
+        xl[e] = l * cs[e] - g * sn[e];
+        xh[e] = g * cs[e] + l * sn[e];
       }
-      if (!on) continue;
-      vl = Chunk<T>::pack(xl);
-      vh = Chunk<T>::pack(xh);
-      T *out = static_cast<T *>(isq ? a.q_out : a.k_out);
-      if (out) {
-        out += static_cast<size_t>(row) * (isq ? a.q_out_stride : a.k_out_stride) +
-               static_cast<size_t>(h) * DH;
-        *reinterpret_cast<u32x4_t *>(out + lo) = vl;
-        *reinterpret_cast<u32x4_t *>(out + hi) = vh;
-      }
-      if (!isq && slot >= 0) {
-        T *dst = static_cast<T *>(a.k_pages) + cache_at;
-        *reinterpret_cast<u32x4_t *>(dst + lo) = vl;
-        *reinterpret_cast<u32x4_t *>(dst + hi) = vh;
-      }
+    }
+    if (!on) return;
+    const u32x4_t vl = Chunk<T>::pack(xl), vh = Chunk<T>::pack(xh);
+    T *out = static_cast<T *>(isq ? a.q_out : a.k_out);
+    if (out) {
+      out += static_cast<size_t>(row) * (isq ? a.q_out_stride : a.k_out_stride) +
+             static_cast<size_t>(h) * DH;
+      *reinterpret_cast<u32x4_t *>(out + me.lo) = vl;
+      *reinterpret_cast<u32x4_t *>(out + me.hi) = vh;
+    }
+    if (!isq && slot >= 0) {
+      T *dst = static_cast<T *>(a.k_pages) + cache_at;
+      *reinterpret_cast<u32x4_t *>(dst + me.lo) = vl;
+      *reinterpret_cast<u32x4_t *>(dst + me.hi) = vh;
+    }
+  };
+#pragma unroll
+  for (int k = 0; k < kAhead; ++k)
+    if (k < n) load(ring[k]);
+  for (int i = 0; i < n; i += kAhead) {
+#pragma unroll
+    for (int k = 0; k < kAhead; ++k) {
+      if (i + k >= n) break;
+      const Item it = ring[k];
+      if (i + k + kAhead < n) load(ring[k]);
+      process(it);
     }
   }
 }
@@ -287,101 +359,127 @@ __global__ __launch_bounds__(64 * kRopeWaves) void qk_rope_fwd_any(RopeArgs a) {
   }
 }
 
-// Backward. Each workgroup walks rows blockIdx.x, blockIdx.x + gridDim.x, .. (a wave whole rows),
-// keeps the weights' gradients of its chunk columns in registers and writes one partial row per
-// workgroup, part[blockIdx.x][2][dh] (q, k); rope_dw_sum adds the rows in order. The grid depends
-// on the sizes alone, so the sums are bitwise reproducible.
+// Backward. Items and waves as in the forward (no cache passes). A wave keeps the weights' gradients
+// of its chunk columns in registers; a workgroup writes one partial row, part[blockIdx.x][2][dh] (q,
+// k), and rope_dw_sum adds the rows in order. The grid depends on the sizes alone, so the sums are
+// bitwise reproducible.
 template <typename T, int LPH>
-__global__ __launch_bounds__(64 * kRopeWaves) void qk_rope_bwd(RopeBwdArgs a) {
-  constexpr int E = Chunk<T>::E;
-  constexpr int HPP = 64 / LPH;
-  constexpr int DH = 2 * E * LPH;
+__global__ __launch_bounds__(64 * kRopeWaves, 3) void qk_rope_bwd(RopeBwdArgs a, int per) {
+  typedef RopeLane<T, LPH> L;
+  constexpr int E = L::E, HPP = L::HPP, DH = L::DH;
+  __shared__ float wl[2][DH];
+  __shared__ double fl[DH / 2];
   __shared__ float red[kRopeWaves][2][DH];
-  const int lane = threadIdx.x & 63, w = threadIdx.x >> 6;
-  const int c = lane % LPH, hsub = lane / LPH;
-  const int half = a.rot / 2;
-  const bool rotated = c * E < half;
-  const int lo = rotated ? c * E : a.rot + 2 * (c * E - half);
-  const int hi = rotated ? lo + half : lo + E;
+  stage_tables<DH>(a.q_w, a.k_w, a.inv_freq, a.rot, wl, fl);
+  const L me(a.rot);
   const bool norm = a.q_w != nullptr;
-  float wq[2 * E], wk[2 * E], aq[2 * E], ak[2 * E];
-  double fr[E];
-#pragma unroll
-  for (int e = 0; e < E; ++e) {
-    wq[e] = norm ? a.q_w[lo + e] : 1.0f;
-    wq[E + e] = norm ? a.q_w[hi + e] : 1.0f;
-    wk[e] = norm ? a.k_w[lo + e] : 1.0f;
-    wk[E + e] = norm ? a.k_w[hi + e] : 1.0f;
-    aq[e] = aq[E + e] = ak[e] = ak[E + e] = 0.0f;
-    fr[e] = rotated ? static_cast<double>(a.inv_freq[c * E + e]) * kInvTwoPi : 0.0;
-  }
+  const int w = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int qp = (a.Hq + HPP - 1) / HPP, kp = (a.Hkv + HPP - 1) / HPP;
-  const long long nw = static_cast<long long>(gridDim.x) * kRopeWaves;
-  for (long long row = static_cast<long long>(blockIdx.x) * kRopeWaves + w; row < a.rows; row += nw) {
-    const int pos = a.positions[row];
-    float sn[E], cs[E];
-#pragma unroll
-    for (int e = 0; e < E; ++e) sincos_turns<T>(turns_of(pos, fr[e]), sn[e], cs[e]);
-    auto pass = [&](bool isq, int p, const float (&wt)[2 * E], float (&acc)[2 * E]) {
-      const int h = p * HPP + hsub;
-      const bool on = h < (isq ? a.Hq : a.Hkv);
+  const int passes = qp + kp;
+  const long long items = static_cast<long long>(a.rows) * passes;
+  const long long f0 = min(items, (static_cast<long long>(blockIdx.x) * kRopeWaves + w) * per);
+  const int n = static_cast<int>(min(static_cast<long long>(per), items - f0));
+  struct Item {
+    u32x4_t gl, gh, xl, xh;
+  } ring[kAheadBwd];
+  struct At {
+    int row, p;
+  };
+  const int row0 = static_cast<int>(f0 / passes);
+  At head = {row0, static_cast<int>(f0 - static_cast<long long>(row0) * passes)}, cur = head;
+  auto step = [&](At &at) {
+    if (++at.p == passes) {
+      at.p = 0;
+      ++at.row;
+    }
+  };
+  auto load = [&](Item &it) {
+    const bool isq = head.p < qp;
+    const int h = (isq ? head.p : head.p - qp) * HPP + me.hsub;
+    it.gl = it.gh = it.xl = it.xh = u32x4_t{};
+    if (h < (isq ? a.Hq : a.Hkv)) {
       const size_t hoff = static_cast<size_t>(h) * DH;
       const T *g = static_cast<const T *>(isq ? a.dq_out : a.dk_out) +
-                   static_cast<size_t>(row) * (isq ? a.dq_out_stride : a.dk_out_stride) + hoff;
-      u32x4_t gl = {}, gh = {}, vl = {}, vh = {};
-      if (on) {
-        gl = *reinterpret_cast<const u32x4_t *>(g + lo);
-        gh = *reinterpret_cast<const u32x4_t *>(g + hi);
-        if (norm) {
-          const T *x = static_cast<const T *>(isq ? a.q : a.k) +
-                       static_cast<size_t>(row) * (isq ? a.q_stride : a.k_stride) + hoff;
-          vl = *reinterpret_cast<const u32x4_t *>(x + lo);
-          vh = *reinterpret_cast<const u32x4_t *>(x + hi);
-        }
-      }
-      float dl[E], dh[E];
-      Chunk<T>::unpack(gl, dl);
-      Chunk<T>::unpack(gh, dh);
-      if (rotated) {
-#pragma unroll
-        for (int e = 0; e < E; ++e) {
-          const float l = dl[e], q = dh[e];
-          dl[e] = l * cs[e] + q * sn[e];
-          dh[e] = q * cs[e] - l * sn[e];
-        }
-      }
+                   static_cast<size_t>(head.row) * (isq ? a.dq_out_stride : a.dk_out_stride) + hoff;
+      it.gl = *reinterpret_cast<const u32x4_t *>(g + me.lo);
+      it.gh = *reinterpret_cast<const u32x4_t *>(g + me.hi);
       if (norm) {
-        float xl[E], xh[E];
-        Chunk<T>::unpack(vl, xl);
-        Chunk<T>::unpack(vh, xh);
-        float ss = 0.0f, st = 0.0f;
-#pragma unroll
-        for (int e = 0; e < E; ++e) {
-          ss = fmaf(xl[e], xl[e], fmaf(xh[e], xh[e], ss));
-          st = fmaf(dl[e] * wt[e], xl[e], fmaf(dh[e] * wt[E + e], xh[e], st));
-        }
-        ss = group_sum<LPH>(ss);
-        st = group_sum<LPH>(st);
-        const float r = 1.0f / sqrtf(fmaf(ss, 1.0f / DH, a.eps));
-        const float m = st * r * (1.0f / DH);  // mean(g w xh)
-#pragma unroll
-        for (int e = 0; e < E; ++e) {
-          const float nl = xl[e] * r, nh = xh[e] * r;
-          acc[e] = fmaf(dl[e], nl, acc[e]);
-          acc[E + e] = fmaf(dh[e], nh, acc[E + e]);
-          dl[e] = r * fmaf(-nl, m, dl[e] * wt[e]);
-          dh[e] = r * fmaf(-nh, m, dh[e] * wt[E + e]);
-        }
+        const T *x = static_cast<const T *>(isq ? a.q : a.k) +
+                     static_cast<size_t>(head.row) * (isq ? a.q_stride : a.k_stride) + hoff;
+        it.xl = *reinterpret_cast<const u32x4_t *>(x + me.lo);
+        it.xh = *reinterpret_cast<const u32x4_t *>(x + me.hi);
       }
-      if (on) {
-        T *d = static_cast<T *>(isq ? a.dq : a.dk) +
-               static_cast<size_t>(row) * (isq ? a.dq_stride : a.dk_stride) + hoff;
-        *reinterpret_cast<u32x4_t *>(d + lo) = Chunk<T>::pack(dl);
-        *reinterpret_cast<u32x4_t *>(d + hi) = Chunk<T>::pack(dh);
+    }
+    step(head);
+  };
+  float aq[2 * E] = {}, ak[2 * E] = {};
+  int row = -1;
+  float sn[E], cs[E];
+  auto grad = [&](const Item &it, const float *wt, float (&acc)[2 * E], float (&dl)[E], float (&dh)[E]) {
+    Chunk<T>::unpack(it.gl, dl);
+    Chunk<T>::unpack(it.gh, dh);
+    if (me.rotated) {
+#pragma unroll
+      for (int e = 0; e < E; ++e) {
+        const float l = dl[e], q = dh[e];
+        dl[e] = l * cs[e] + q * sn[e];
+        dh[e] = q * cs[e] - l * sn[e];
       }
-    };
-    for (int p = 0; p < qp; ++p) pass(true, p, wq, aq);
-    for (int p = 0; p < kp; ++p) pass(false, p, wk, ak);
+    }
+    if (!norm) return;
+    float xl[E], xh[E];
+    Chunk<T>::unpack(it.xl, xl);
+    Chunk<T>::unpack(it.xh, xh);
+    float ss = 0.0f, st = 0.0f;
+#pragma unroll
+    for (int e = 0; e < E; ++e) {
+      ss = fmaf(xl[e], xl[e], fmaf(xh[e], xh[e], ss));
+      st = fmaf(dl[e] * wt[me.lo + e], xl[e], fmaf(dh[e] * wt[me.hi + e], xh[e], st));
+    }
+    ss = group_sum<LPH>(ss);
+    st = group_sum<LPH>(st);
+    const float r = 1.0f / sqrtf(fmaf(ss, 1.0f / DH, a.eps));
+    const float m = st * r * (1.0f / DH);  // mean(g w xh)
+#pragma unroll
+    for (int e = 0; e < E; ++e) {
+      const float nl = xl[e] * r, nh = xh[e] * r;
+      acc[e] = fmaf(dl[e], nl, acc[e]);
+      acc[E + e] = fmaf(dh[e], nh, acc[E + e]);
+      dl[e] = r * fmaf(-nl, m, dl[e] * wt[me.lo + e]);
+      dh[e] = r * fmaf(-nh, m, dh[e] * wt[me.hi + e]);
+    }
+  };
+  auto process = [&](const Item &it) {
+    if (cur.row != row) {
+      row = cur.row;
+      me.angles(uniform_load(a.positions, row), fl, sn, cs);
+    }
+    const bool isq = cur.p < qp;
+    const int h = (isq ? cur.p : cur.p - qp) * HPP + me.hsub;
+    step(cur);
+    float dl[E], dh[E];
+    if (isq)
+      grad(it, wl[0], aq, dl, dh);
+    else
+      grad(it, wl[1], ak, dl, dh);
+    if (h < (isq ? a.Hq : a.Hkv)) {
+      T *d = static_cast<T *>(isq ? a.dq : a.dk) +
+             static_cast<size_t>(row) * (isq ? a.dq_stride : a.dk_stride) + static_cast<size_t>(h) * DH;
+      *reinterpret_cast<u32x4_t *>(d + me.lo) = Chunk<T>::pack(dl);
+      *reinterpret_cast<u32x4_t *>(d + me.hi) = Chunk<T>::pack(dh);
+    }
+  };
+#pragma unroll
+  for (int k = 0; k < kAheadBwd; ++k)
+    if (k < n) load(ring[k]);
+  for (int i = 0; i < n; i += kAheadBwd) {
+#pragma unroll
+    for (int k = 0; k < kAheadBwd; ++k) {
+      if (i + k >= n) break;
+      const Item it = ring[k];
+      if (i + k + kAheadBwd < n) load(ring[k]);
+      process(it);
+    }
   }
   if (!norm) return;
   // the wave's head groups (lanes c, c + LPH, ..), then the workgroup's waves
@@ -393,13 +491,13 @@ __global__ __launch_bounds__(64 * kRopeWaves) void qk_rope_bwd(RopeBwdArgs a) {
       ak[e] += __shfl_xor(ak[e], o, 64);
     }
   }
-  if (hsub == 0) {
+  if (me.hsub == 0) {
 #pragma unroll
     for (int e = 0; e < E; ++e) {
-      red[w][0][lo + e] = aq[e];
-      red[w][0][hi + e] = aq[E + e];
-      red[w][1][lo + e] = ak[e];
-      red[w][1][hi + e] = ak[E + e];
+      red[w][0][me.lo + e] = aq[e];
+      red[w][0][me.hi + e] = aq[E + e];
+      red[w][1][me.lo + e] = ak[e];
+      red[w][1][me.hi + e] = ak[E + e];
     }
   }
   __syncthreads();
@@ -546,6 +644,19 @@ bool chunked(int dh, int rot, int io, const void *const *ptrs, int np, const lon
 
 }  // namespace
 
+namespace {
+
+// Items of one wave: enough waves for the chip, whole rows once a wave has more than one (a row's
+// angles are then formed once).
+constexpr long long kFwdWaves = 8192;
+int items_per_wave(int rows, int passes, long long waves) {
+  const long long items = static_cast<long long>(rows) * passes;
+  const long long per = (items + waves - 1) / waves;
+  return static_cast<int>(per <= 1 ? 1 : (per + passes - 1) / passes * passes);
+}
+
+}  // namespace
+
 hipError_t launch_qk_rope(const RopeArgs &a, int io, hipStream_t s) {
   const void *ptrs[] = {a.q, a.k, a.v, a.q_out, a.k_out, a.k_pages, a.v_pages};
   const long long st[] = {a.q_stride, a.k_stride, a.v ? a.v_stride : 0, a.q_out_stride,
@@ -564,22 +675,20 @@ hipError_t launch_qk_rope(const RopeArgs &a, int io, hipStream_t s) {
   const int lph = a.dh / (io == kBF16 ? 16 : 8), hpp = 64 / lph;
   const int kp = (a.Hkv + hpp - 1) / hpp;
   const int passes = (a.Hq + hpp - 1) / hpp + kp + (a.slots ? kp : 0);
-  // one wave per pass while that leaves the chip unfilled, else one wave per row
-  const int parts = static_cast<long long>(a.rows) * passes <= 4096 ? passes : 1;
-  const long long tasks = static_cast<long long>(a.rows) * parts;
-  const unsigned grid =
-      static_cast<unsigned>(std::min<long long>((tasks + kRopeWaves - 1) / kRopeWaves, 4096));
+  const int per = items_per_wave(a.rows, passes, kFwdWaves);
+  const long long waves = (static_cast<long long>(a.rows) * passes + per - 1) / per;
+  const unsigned grid = static_cast<unsigned>((waves + kRopeWaves - 1) / kRopeWaves);
   if (io == kBF16) {
     switch (a.dh) {
-      case 64: qk_rope_fwd<bf16_t, 4><<<grid, kThr, 0, s>>>(a, parts); break;
-      case 128: qk_rope_fwd<bf16_t, 8><<<grid, kThr, 0, s>>>(a, parts); break;
-      default: qk_rope_fwd<bf16_t, 16><<<grid, kThr, 0, s>>>(a, parts); break;
+      case 64: qk_rope_fwd<bf16_t, 4><<<grid, kThr, 0, s>>>(a, per); break;
+      case 128: qk_rope_fwd<bf16_t, 8><<<grid, kThr, 0, s>>>(a, per); break;
+      default: qk_rope_fwd<bf16_t, 16><<<grid, kThr, 0, s>>>(a, per); break;
     }
   } else {
     switch (a.dh) {
-      case 64: qk_rope_fwd<float, 8><<<grid, kThr, 0, s>>>(a, parts); break;
-      case 128: qk_rope_fwd<float, 16><<<grid, kThr, 0, s>>>(a, parts); break;
-      default: qk_rope_fwd<float, 32><<<grid, kThr, 0, s>>>(a, parts); break;
+      case 64: qk_rope_fwd<float, 8><<<grid, kThr, 0, s>>>(a, per); break;
+      case 128: qk_rope_fwd<float, 16><<<grid, kThr, 0, s>>>(a, per); break;
+      default: qk_rope_fwd<float, 32><<<grid, kThr, 0, s>>>(a, per); break;
     }
   }
   return hipGetLastError();
@@ -596,6 +705,10 @@ hipError_t launch_qk_rope_backward(const RopeBwdArgs &a, float *dq_w, float *dk_
                           a.dk_out_stride, a.dq_stride, a.dk_stride};
   const int kThr = 64 * kRopeWaves;
   const unsigned grid = static_cast<unsigned>(rope_bwd_groups(a.rows));
+  const int hpp = 64 / std::max(1, a.dh / (io == kBF16 ? 16 : 8));
+  const int passes = hpp < 1 ? 1 : (a.Hq + hpp - 1) / hpp + (a.Hkv + hpp - 1) / hpp;
+  const long long items = static_cast<long long>(a.rows) * passes, waves = static_cast<long long>(grid) * kRopeWaves;
+  const int per = static_cast<int>((items + waves - 1) / waves);
   if (!chunked(a.dh, a.rot, io, ptrs, 6, st, 6)) {
     if (io == kBF16)
       qk_rope_bwd_any<bf16_t><<<grid, kThr, 0, s>>>(a);
@@ -603,15 +716,15 @@ hipError_t launch_qk_rope_backward(const RopeBwdArgs &a, float *dq_w, float *dk_
       qk_rope_bwd_any<float><<<grid, kThr, 0, s>>>(a);
   } else if (io == kBF16) {
     switch (a.dh) {
-      case 64: qk_rope_bwd<bf16_t, 4><<<grid, kThr, 0, s>>>(a); break;
-      case 128: qk_rope_bwd<bf16_t, 8><<<grid, kThr, 0, s>>>(a); break;
-      default: qk_rope_bwd<bf16_t, 16><<<grid, kThr, 0, s>>>(a); break;
+      case 64: qk_rope_bwd<bf16_t, 4><<<grid, kThr, 0, s>>>(a, per); break;
+      case 128: qk_rope_bwd<bf16_t, 8><<<grid, kThr, 0, s>>>(a, per); break;
+      default: qk_rope_bwd<bf16_t, 16><<<grid, kThr, 0, s>>>(a, per); break;
     }
   } else {
     switch (a.dh) {
-      case 64: qk_rope_bwd<float, 8><<<grid, kThr, 0, s>>>(a); break;
-      case 128: qk_rope_bwd<float, 16><<<grid, kThr, 0, s>>>(a); break;
-      default: qk_rope_bwd<float, 32><<<grid, kThr, 0, s>>>(a); break;
+      case 64: qk_rope_bwd<float, 8><<<grid, kThr, 0, s>>>(a, per); break;
+      case 128: qk_rope_bwd<float, 16><<<grid, kThr, 0, s>>>(a, per); break;
+      default: qk_rope_bwd<float, 32><<<grid, kThr, 0, s>>>(a, per); break;
     }
   }
   hipError_t e = hipGetLastError();

@@ -12,7 +12,8 @@ LIB = os.path.join(PKG, "librglru.so")
 SOURCES = ["rglru_api.cpp", "rglru_gates.hip", "rglru_scan.hip", "rglru_decode.hip",
            "rglru_fused.hip", "rglru_backward.hip", "rglru_bwd_tiles.hip", "rglru_bwd_fused.hip",
            "rglru_mqa.hip", "rglru_noalloc.hip", "rglru_attn_api.cpp", "rglru_rope.hip",
-           "rglru_paged.hip", "rglru_mqa_bwd.hip"]
+           "rglru_paged.hip", "rglru_mqa_bwd.hip",
+           "rglru_attn.hip"]
 HIPCC = os.environ.get("HIPCC", "/opt/rocm/bin/hipcc")
 
 FLAGS = [

@@ -1,0 +1,126 @@
+// rglru_attn.h -- what the local attention kernels share: blocks of key, value or query rows in LDS, how
+// they are filled and read as MFMA operands, and the mask.
+//
+// Rows arrive by direct buffer-to-LDS loads. The 16-byte chunk c of row r lies at c ^ f(r), with f chosen
+// so that both the row reads (16 consecutive rows at one chunk) and the transposing reads (4
+// consecutive rows at 4 consecutive chunks) of a pass fall on different banks.
+#pragma once
+
+#include "rglru_mfma.h"
+
+namespace rglru {
+namespace attn {
+
+constexpr int kRawWord3 = 0x00020000;  // buffer descriptor word 3: raw 32-bit data, no swizzle
+constexpr float kLn2Inv = 1.4426950408889634f;
+
+typedef short i16x4_t __attribute__((ext_vector_type(4)));
+typedef __attribute__((address_space(3))) i16x4_t lds_i16x4_t;
+typedef __attribute__((address_space(3))) u32x4_t lds_u32x4_t;
+typedef float f32x4_t __attribute__((ext_vector_type(4)));
+
+constexpr int kWg = 4;         // waves per workgroup
+constexpr int kOwn = 32 * kWg; // rows (attn_dq) or keys (attn_dkv) per workgroup
+constexpr int kBlk = 32;       // rows per LDS block
+
+// A block of kBlk rows of DH bf16 in LDS, and the ways it is filled and read.
+template <int DH> struct Blk {
+  static constexpr unsigned kRowBytes = DH * 2;
+  static constexpr unsigned kBytes = kBlk * kRowBytes;  // one block
+  static constexpr unsigned kSlot = 2 * kBytes;         // a ring slot: a block of K (Q), one of V (dO)
+  static constexpr int kCPR = DH / 8;                 // 16-byte chunks per row
+  static constexpr int kRPI = 64 / kCPR;              // rows per wave-wide 16-byte load
+  static constexpr int kLPW = kBlk / kRPI / kWg;      // loads per wave and block
+  static constexpr int kKS = DH / 16;                 // k-steps over d
+  static constexpr int kDT = DH / 32;                 // 32-wide d tiles
+  // chunk swizzle: rows of 128 bytes (DH 64) share a 256-byte bank line in pairs
+  __device__ __forceinline__ static int swz(int r) {
+    return DH == 64 ? 4 * ((r >> 1) & 1) + ((r >> 2) & 3) : 4 * (r & 3) + ((r >> 2) & 3);
+  }
+  // the buffer of a block's rows: those of the sequence from `base` on, at most kBlk (rows past its
+  // end then read zero, whatever lies there; rows <= 0: all)
+  __device__ __forceinline__ static __amdgpu_buffer_rsrc_t rsrc(const bf16_t *base,
+                                                                unsigned row_bytes, int rows) {
+    return __builtin_amdgcn_make_buffer_rsrc(
+        const_cast<bf16_t *>(wave_uniform(base)), static_cast<short>(0),
+        rows > 0 ? static_cast<int>(row_bytes * static_cast<unsigned>(min(rows, kBlk) - 1)) + DH * 2 : 0,
+        kRawWord3);
+  }
+  // this wave's ii-th load of the block's rows to LDS byte address dst
+  __device__ __forceinline__ static void load(__amdgpu_buffer_rsrc_t src, unsigned row_bytes,
+                                              int ii, int w, int lane, unsigned dst) {
+    const int i = w + kWg * ii;
+    const int row = i * kRPI + lane / kCPR;
+    const unsigned off = static_cast<unsigned>(row) * row_bytes +
+                         static_cast<unsigned>(((lane % kCPR) ^ swz(row)) * 16);
+    dma_16b(src, off, static_cast<unsigned>(__builtin_amdgcn_readfirstlane(dst + i * 1024)));
+  }
+  // A block's two reads, from byte addresses that depend on the lane only through one register: the
+  // row length and every block start are multiples of the bits that the steps change by XOR.
+  // row_lane / col_lane: the lane's part for step 0, to be added to the block's address.
+  __device__ __forceinline__ static unsigned row_lane(int lane) {
+    const int r = lane & 31;
+    return r * kRowBytes + (((lane >> 5) ^ swz(r)) * 16);
+  }
+  // A operand, k = d of step s: 8 values of row lane % 32
+  __device__ __forceinline__ static bf16x8_t rows(unsigned at, int s) {
+    return __builtin_bit_cast(bf16x8_t, *(lds_u32x4_t *)static_cast<uintptr_t>(at ^ (32u * s)));
+  }
+  __device__ __forceinline__ static unsigned col_lane(int lane) {
+    const int half = lane >> 5, r4 = (lane & 15) >> 2;
+    const int cl = 2 * ((lane >> 4) & 1) + ((lane & 3) >> 1);
+    const int rj = DH == 64 ? r4 >> 1 : r4;
+    return (4 * half + r4) * kRowBytes + 64 * rj + 16 * (cl ^ half) + 8 * (lane & 1);
+  }
+  // A operand, rows d = 32 j + lane % 32, k = block rows 16 st + (4 h.., 8 + 4 h..), h = lane / 32:
+  // the accumulator's row order
+  __device__ __forceinline__ static bf16x8_t cols(unsigned at, int st, int j) {
+    const unsigned p = (at ^ (64u * j)) + 16 * st * kRowBytes;
+    const i16x4_t x = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_i16x4_t *)static_cast<uintptr_t>(p));
+    const i16x4_t y = __builtin_amdgcn_ds_read_tr16_b64_v4i16(
+        (lds_i16x4_t *)static_cast<uintptr_t>((at ^ (64u * j) ^ 32u) + (16 * st + 8) * kRowBytes));
+    const uint2 ux = __builtin_bit_cast(uint2, x), uy = __builtin_bit_cast(uint2, y);
+    const u32x4_t u = {ux.x, ux.y, uy.x, uy.y};
+    return __builtin_bit_cast(bf16x8_t, u);
+  }
+};
+
+// Pins the order of a run of N steps of R LDS reads and M MFMAs each: the reads D steps ahead, no
+// further (the compiler else hoists more of them than there are registers).
+template <int N, int R, int M, int D> __device__ __forceinline__ void read_ahead() {
+#pragma unroll
+  for (int i = 0; i < D && i < N; ++i) __builtin_amdgcn_sched_group_barrier(0x100, R, 0);
+#pragma unroll
+  for (int i = 0; i < N; ++i) {
+    __builtin_amdgcn_sched_group_barrier(0x008, M, 0);
+    if (i + D < N) __builtin_amdgcn_sched_group_barrier(0x100, R, 0);
+  }
+}
+
+// An integer that is the same in every lane, kept in a scalar register (quotients run on the vector
+// unit).
+__device__ __forceinline__ int uni(int v) { return __builtin_amdgcn_readfirstlane(v); }
+
+// Key row kr sees query row t (t, kr < len checked apart).
+__device__ __forceinline__ bool sees(int t, int u, int W, int sinks) {
+  return u <= t && (u > t - W || u < sinks);
+}
+
+__device__ __forceinline__ int clamp_len(const int *lens, int b, int T) {
+  return lens ? min(max(uniform_load(lens, b), 0), T) : T;
+}
+
+// The key blocks that query rows q0 .. q0 + rows - 1 of a sequence of len tokens need, in order: those
+// with sinks before the window's first block, then the window's.
+struct BlockWalk {
+  int win, ns, n;  // the window's first block; sink blocks; blocks in all
+  __device__ __forceinline__ BlockWalk(int q0, int rows, int len, int W, int sinks) {
+    win = max(0, q0 - W + 1) / kBlk;
+    ns = min((sinks + kBlk - 1) / kBlk, win);
+    n = ns + (min(len, q0 + rows) - 1) / kBlk + 1 - win;
+  }
+  __device__ __forceinline__ int first_row(int i) const { return (i < ns ? i : i - ns + win) * kBlk; }
+};
+
+}  // namespace attn
+}  // namespace rglru

@@ -1,0 +1,319 @@
+// rglru_attn.hip -- local attention with grouped heads, sinks, a length per sequence and strided tokens,
+// forward, bf16 on gfx950 (rglru_local_attention).
+//
+//   o[t] = sum_u p_u v_u,  p_u = exp(scale s_u - lse),  s_u = <q_t, k_u>,
+//   u <= t and (u > t - W or u < sinks), t and u below the sequence's length.
+//
+// One pass over the visible keys with a running maximum m and sum l per row. Both contractions put a
+// query row in each lane: S^T = K Q^T (A = K rows from LDS, B = q in registers for the kernel's life) and
+// O^T += V^T P^T (A = V^T from LDS by transposing reads, B = P). The accumulator layout of S^T is already the
+// B operand's of the second, so P never leaves its lane. A wave owns 32 RT rows and all of dh; four
+// waves are a workgroup, two workgroups share a CU, and each wave works alone between the barriers
+// (one per 32-key block), so that one wave's matrix work runs beside another's exponentials. Within a
+// wave the product with V lags by one block, beside the block's softmax (not where P is split: its lo
+// half would not fit in the registers over that time). Per block the LDS serves, for
+// four waves, dh / 16 row reads and as many transposing ones (half the rate), which is what bounds RT =
+// 1; with RT = 2 (dh <= 128) every read feeds two MFMAs.
+#include "rglru_attn.h"
+#include "rglru_launch.h"
+
+#include <algorithm>
+#include <type_traits>
+
+namespace rglru {
+
+using namespace attn;
+
+namespace {
+
+// P enters P V as bf16 hi + lo in workgroups where some row sees fewer keys: there the rounding of P to
+// bf16 does not average out (a row's worst element then stays near 4e-3 of the output's rms instead of
+// up to 4e-2; with 256 keys or more bf16 alone is below 9e-3)
+constexpr int kSplitKeys = 256;
+// s c - m c in one FMA is off by the rounding of m c, 2^-24 of it: for scores beyond this (in exp2
+// units) the difference s - m is formed first
+constexpr float kBigScore = 16384.0f;
+
+}  // namespace
+
+// o of one row from the definition alone, one key at a time (DH / 64 values of every row per lane).
+// Only for rows whose o came out non-finite although their scores are finite: the tile's P V adds
+// 0 * v for the keys that a row does not see, which is not 0 where v is infinite or NaN.
+template <int DH>
+__device__ __forceinline__ void exact_row(const bf16_t *q, const bf16_t *k, const bf16_t *v, bf16_t *o,
+                                          const AttnArgs &x, float c, int t, int lane) {
+  constexpr int kPer = DH / 64;
+  float qv[kPer], a[kPer] = {};
+#pragma unroll
+  for (int i = 0; i < kPer; ++i) qv[i] = bf16_to_f32(q[lane * kPer + i]);
+  float m = x.floor, l = 0.0f;
+  const int lo = max(0, t - x.window + 1);
+  for (int u = x.sinks > 0 ? 0 : lo; u <= t;) {
+    float s = 0.0f;
+#pragma unroll
+    for (int i = 0; i < kPer; ++i)
+      s = fmaf(qv[i], bf16_to_f32(k[static_cast<size_t>(u) * x.k_stride + lane * kPer + i]), s);
+#pragma unroll
+    for (int e = 1; e < 64; e <<= 1) s += __shfl_xor(s, e, 64);
+    const float mn = fmaxf(m, s);
+    const float corr = __builtin_amdgcn_exp2f((m - mn) * c);
+    const float p = __builtin_amdgcn_exp2f((s - mn) * c);
+    m = mn;
+    l = l * corr + p;
+#pragma unroll
+    for (int i = 0; i < kPer; ++i)
+      a[i] = a[i] * corr + p * bf16_to_f32(v[static_cast<size_t>(u) * x.v_stride + lane * kPer + i]);
+    ++u;
+    if (u == x.sinks && u < lo) u = lo;
+  }
+#pragma unroll
+  for (int i = 0; i < kPer; ++i) o[lane * kPer + i] = f32_to_bf16(a[i] / l);
+}
+
+template <int DH, int RT>
+__global__ __launch_bounds__(64 * kWg, 2) void attn_fwd(AttnArgs x) {
+  typedef Blk<DH> K;
+  constexpr int kRows = 32 * RT * kWg;  // per workgroup
+  __shared__ __attribute__((aligned(1024))) unsigned char smem[5 * K::kBytes];  // K[2], V[3]
+  const unsigned lds = lds_addr(smem);
+  const int tid = threadIdx.x, w = uni(tid >> 6), lane = tid & 63;
+  const int lrow = lane & 31, half = lane >> 5;
+  const int T = x.T, Hq = x.Hq, W = x.window, sinks = x.sinks;
+  const float c = x.scale * kLn2Inv;
+  // heavy first: query blocks from the last one down, all (sequence, head) pairs of one together
+  const int nbh = x.B * Hq, nqb = (T + kRows - 1) / kRows;
+  const int qi = uni(blockIdx.x / nbh), bh = blockIdx.x - qi * nbh;
+  const int q0 = (nqb - 1 - qi) * kRows;
+  const int b = uni(bh / Hq), h = bh - b * Hq;
+  const int kvh = uni(h / (Hq / x.Hkv));
+  const int len = clamp_len(x.lens, b, T);
+  const size_t tok = static_cast<size_t>(b) * T;
+  const size_t ostride = static_cast<size_t>(Hq) * DH;
+  bf16_t *const o_ = static_cast<bf16_t *>(x.o) + tok * ostride + static_cast<size_t>(h) * DH;
+  float *const lse_ = x.lse ? x.lse + (static_cast<size_t>(b) * Hq + h) * T : nullptr;
+  if (q0 >= len) {  // no row of the block belongs to the sequence
+    for (int i = tid; i < kRows * (DH / 8); i += 64 * kWg) {
+      const int t = q0 + i / (DH / 8);
+      if (t < T) *reinterpret_cast<u32x4_t *>(o_ + static_cast<size_t>(t) * ostride + (i % (DH / 8)) * 8) = u32x4_t{};
+    }
+    for (int i = tid; lse_ && i < kRows; i += 64 * kWg)
+      if (q0 + i < T) lse_[q0 + i] = -__builtin_inff();
+    return;
+  }
+  const int qw = q0 + 32 * RT * w;  // this wave's first row; its rows: qw + 32 r + lrow
+  const bf16_t *const q_ = static_cast<const bf16_t *>(x.q) + tok * x.q_stride + static_cast<size_t>(h) * DH;
+  const bf16_t *const k_ = static_cast<const bf16_t *>(x.k) + tok * x.k_stride + static_cast<size_t>(kvh) * DH;
+  const bf16_t *const v_ = static_cast<const bf16_t *>(x.v) + tok * x.v_stride + static_cast<size_t>(kvh) * DH;
+  bf16x8_t qf[RT][K::kKS];
+#pragma unroll
+  for (int r = 0; r < RT; ++r) {
+    const bf16_t *qp = q_ + static_cast<size_t>(min(qw + 32 * r + lrow, T - 1)) * x.q_stride + 8 * half;
+#pragma unroll
+    for (int s = 0; s < K::kKS; ++s) qf[r][s] = load_bf16x8(qp + 16 * s);
+  }
+  // complete these loads here: the compiler does not see the LDS loads that share their counter
+#pragma unroll
+  for (int r = 0; r < RT; ++r)
+#pragma unroll
+    for (int s = 0; s < K::kKS; ++s) asm volatile("" ::"v"(qf[r][s]));
+  const BlockWalk walk(q0, kRows, len, W, sinks);
+  const unsigned krb = static_cast<unsigned>(x.k_stride) * 2, vrb = static_cast<unsigned>(x.v_stride) * 2;
+  auto load_block = [&](int i, int vslot) {
+    const int u0 = walk.first_row(i);
+    const __amdgpu_buffer_rsrc_t ks = K::rsrc(k_ + static_cast<size_t>(u0) * x.k_stride, krb, len - u0);
+    const __amdgpu_buffer_rsrc_t vs = K::rsrc(v_ + static_cast<size_t>(u0) * x.v_stride, vrb, len - u0);
+#pragma unroll
+    for (int ii = 0; ii < K::kLPW; ++ii) {
+      K::load(ks, krb, ii, w, lane, lds + (i & 1) * K::kBytes);
+      K::load(vs, vrb, ii, w, lane, lds + (2 + vslot) * K::kBytes);
+    }
+  };
+  const unsigned row_lane = K::row_lane(lane), col_lane = K::col_lane(lane);
+
+  unsigned odd[RT];  // rows to do again
+  // the whole walk and the stores, P as bf16 (kSplit: as bf16 hi + lo)
+  auto run = [&](auto split_c) {
+    constexpr bool kSplit = decltype(split_c)::value;
+    f32x16_t acc[RT][K::kDT];  // O^T
+    float m[RT], l[RT];        // running maximum (of raw scores), and this half's sum
+    u32x4_t p[RT][2], pl[RT][2];  // the last block's P: two 16-key steps, hi (and lo)
+#pragma unroll
+    for (int r = 0; r < RT; ++r) {
+#pragma unroll
+      for (int j = 0; j < K::kDT; ++j) acc[r][j] = f32x16_t{};
+      m[r] = x.floor;
+      l[r] = 0.0f;
+      p[r][0] = p[r][1] = u32x4_t{};
+    }
+    auto products = [&](int vslot) {
+      const unsigned at = lds + (2 + vslot) * K::kBytes + col_lane;
+#pragma unroll
+      for (int st = 0; st < 2; ++st)
+#pragma unroll
+        for (int j = 0; j < K::kDT; ++j) {
+          const bf16x8_t vt = K::cols(at, st, j);
+#pragma unroll
+          for (int r = 0; r < RT; ++r) {
+            acc[r][j] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(
+                vt, __builtin_bit_cast(bf16x8_t, p[r][st]), acc[r][j], 0, 0, 0);
+            if constexpr (kSplit)
+              acc[r][j] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(
+                  vt, __builtin_bit_cast(bf16x8_t, pl[r][st]), acc[r][j], 0, 0, 0);
+          }
+        }
+    };
+    bool ran = false;            // the last block was visible: its P is still to go into O
+    int vs = 0, vsp = 0;         // V slots of this block and the last
+    load_block(0, 0);
+    for (int i = 0; i < walk.n; ++i) {
+      __builtin_amdgcn_s_waitcnt(0x0F70);  // vmcnt(0): this wave's rows of block i landed
+      lds_barrier();                        // everyone's landed; everyone is done with block i - 2's V
+      const int vsn = vs == 2 ? 0 : vs + 1;
+      if (i + 1 < walk.n) load_block(i + 1, vsn);
+      const int U = walk.first_row(i);
+      const bool vis = U <= qw + 32 * RT - 1 && (U + 31 > qw - W || U < sinks) && qw < len;
+      // (after the last visible block once more, all masked: its P into O, then P = 0)
+      if (vis || (ran && !kSplit)) {
+        f32x16_t s[RT];
+#pragma unroll
+        for (int r = 0; r < RT; ++r) s[r] = f32x16_t{};
+        const unsigned at = lds + (i & 1) * K::kBytes + row_lane;
+#pragma unroll
+        for (int d = 0; d < K::kKS; ++d) {
+          const bf16x8_t kr = K::rows(at, d);
+#pragma unroll
+          for (int r = 0; r < RT; ++r)
+            s[r] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(kr, qf[r][d], s[r], 0, 0, 0);
+        }
+        if constexpr (!kSplit) products(vsp);  // the last block's (the first: P = 0)
+        const bool full = U + 31 <= qw && (U > qw + 32 * RT - 1 - W || U + 31 < sinks) && U + 31 < len;
+        if (!full) {
+#pragma unroll
+          for (int r = 0; r < RT; ++r)
+#pragma unroll
+            for (int e = 0; e < 16; ++e) {
+              const int u = U + 8 * (e >> 2) + 4 * half + (e & 3);
+              s[r][e] = sees(qw + 32 * r + lrow, u, W, sinks) && u < len ? s[r][e] : -__builtin_inff();
+            }
+        }
+#pragma unroll
+        for (int r = 0; r < RT; ++r) {
+          float mx = fmaxf(s[r][0], s[r][1]), my = fmaxf(s[r][2], s[r][3]);
+#pragma unroll
+          for (int e = 4; e < 16; e += 2) {
+            mx = fmaxf(mx, s[r][e]);
+            my = fmaxf(my, s[r][e + 1]);
+          }
+          float lo, hi;
+          halves(fmaxf(mx, my), lo, hi);
+          mx = fmaxf(fmaxf(lo, hi), x.floor);
+          // O and l are kept relative to a maximum that is raised only when a row's grows by more than
+          // 2^8: they share it, so the result does not change, and the rescale is rare
+          const bool raise = (mx - m[r]) * c > 8.0f;
+          if (__any(raise)) {
+            const float mn = raise ? mx : m[r];
+            const float corr = __builtin_amdgcn_exp2f((m[r] - mn) * c);
+            l[r] *= corr;
+            m[r] = mn;
+#pragma unroll
+            for (int j = 0; j < K::kDT; ++j) acc[r][j] *= corr;
+          }
+          const float mc = m[r] * c;
+          if (__any(fabsf(mc) > kBigScore)) {
+#pragma unroll
+            for (int e = 0; e < 16; ++e) s[r][e] = (s[r][e] - m[r]) * c;
+          } else {
+#pragma unroll
+            for (int e = 0; e < 16; ++e) s[r][e] = fmaf(s[r][e], c, -mc);
+          }
+          float l0 = 0.0f, l1 = 0.0f;
+#pragma unroll
+          for (int e = 0; e < 16; e += 2) {
+            const float a = __builtin_amdgcn_exp2f(s[r][e]), bb = __builtin_amdgcn_exp2f(s[r][e + 1]);
+            l0 += a;
+            l1 += bb;
+            const uint32_t hw = pack_bf16x2(a, bb);
+            p[r][e >> 3][(e >> 1) & 3] = hw;
+            if constexpr (kSplit) pl[r][e >> 3][(e >> 1) & 3] = pack_bf16x2(a - bf16lo(hw), bb - bf16hi(hw));
+          }
+          l[r] += l0 + l1;
+        }
+        if constexpr (kSplit) products(vs);
+      }
+      ran = vis;
+      vsp = vs;
+      vs = vsn;
+    }
+    if constexpr (!kSplit) products(vsp);
+    // normalise and store; lane = row, accumulator e of tile j is d = 32 j + 8 (e / 4) + 4 half + e % 4
+#pragma unroll
+    for (int r = 0; r < RT; ++r) {
+      float lo, hi;
+      halves(l[r], lo, hi);
+      const float lt = lo + hi;
+      const int t = qw + 32 * r + lrow;
+      const bool in = t < len;
+      const float inv = 1.0f / lt;
+      float worst = 0.0f;
+#pragma unroll
+      for (int j = 0; j < K::kDT; ++j)
+#pragma unroll
+        for (int e = 0; e < 16; ++e) {
+          acc[r][j][e] = in ? acc[r][j][e] * inv : 0.0f;
+          worst = fmaf(0.0f, acc[r][j][e], worst);  // NaN if any is not finite
+        }
+      if (t < T) {
+        bf16_t *op = o_ + static_cast<size_t>(t) * ostride + 4 * half;
+#pragma unroll
+        for (int j = 0; j < K::kDT; ++j)
+#pragma unroll
+          for (int g = 0; g < 4; ++g)
+            *reinterpret_cast<uint2 *>(op + 32 * j + 8 * g) =
+                make_uint2(pack_bf16x2(acc[r][j][4 * g], acc[r][j][4 * g + 1]),
+                           pack_bf16x2(acc[r][j][4 * g + 2], acc[r][j][4 * g + 3]));
+        // ln of the denominator sum_u exp(scale s_u) = scale m + ln l
+        if (lse_ && half == 0)
+          lse_[t] = in ? (m[r] * c + __builtin_amdgcn_logf(lt)) * 0.6931471805599453f : -__builtin_inff();
+      }
+      const unsigned long long rows = __ballot(in && !(worst == 0.0f) && lt < __builtin_inff());
+      odd[r] = static_cast<unsigned>(rows | (rows >> 32));
+    }
+  };
+  if (min(q0 + 1, W) < kSplitKeys)
+    run(std::true_type{});
+  else
+    run(std::false_type{});
+  // rows with finite scores and a non-finite o: again, key by key
+#pragma unroll
+  for (int r = 0; r < RT; ++r)
+    while (odd[r]) {
+      const int t = qw + 32 * r + __builtin_ctz(odd[r]);
+      odd[r] &= odd[r] - 1;
+      exact_row<DH>(q_ + static_cast<size_t>(t) * x.q_stride, k_, v_, o_ + static_cast<size_t>(t) * ostride,
+                    x, c, t, lane);
+    }
+}
+
+namespace {
+
+template <int DH, int RT> hipError_t launch(const AttnArgs &a, hipStream_t s) {
+  const unsigned nq = static_cast<unsigned>((a.T + 32 * RT * kWg - 1) / (32 * RT * kWg));
+  attn_fwd<DH, RT><<<nq * a.B * a.Hq, 64 * kWg, 0, s>>>(a);
+  return hipGetLastError();
+}
+
+}  // namespace
+
+hipError_t launch_local_attention(const AttnArgs &args, hipStream_t s) {
+  AttnArgs a = args;
+  a.window = std::min(a.window, a.T);
+  a.sinks = std::min(a.sinks, a.T);
+  switch (a.dh) {
+    case 64: return launch<64, 1>(a, s);
+    case 128: return launch<128, 1>(a, s);
+    case 256: return launch<256, 1>(a, s);
+  }
+  return hipErrorInvalidValue;
+}
+
+}  // namespace rglru

@@ -266,7 +266,7 @@ size_t rglru_local_attention_backward_workspace_size(int B, int T, int Hq, int H
                  static_cast<long long>(Hkv) * dh, window, sinks, 0.0f, RGLRU_BF16) != RGLRU_OK)
     return 0;
   const rglru::AttnBwdPlan p = rglru::attn_bwd_plan(B, T, Hq, Hkv, std::min(window, T), sinks);
-  return rglru::align_up(rglru::attn_bwd_delta_floats(B, T, Hq) * sizeof(float)) +
+  return rglru::align_up(rglru::attn_bwd_stat_bytes(B, T, Hq)) +
          rglru::align_up(rglru::attn_bwd_part_floats(p, B, Hkv, dh) * sizeof(float));
 }
 
@@ -312,9 +312,9 @@ rglru_status rglru_local_attention_backward(
   rglru::AttnBwdArgs a = {};
   a.q = q, a.k = k, a.v = v, a.o = o, a.do_ = d_o, a.lse = lse, a.lens = lens;
   a.dq = dq, a.dk = dk, a.dv = dv;
-  a.delta = reinterpret_cast<float *>(ws);
+  a.stat = reinterpret_cast<float2 *>(ws);
   a.part = reinterpret_cast<float *>(
-      ws + rglru::align_up(rglru::attn_bwd_delta_floats(B, T, Hq) * sizeof(float)));
+      ws + rglru::align_up(rglru::attn_bwd_stat_bytes(B, T, Hq)));
   a.B = B, a.T = T, a.Hq = Hq, a.Hkv = Hkv, a.group = Hq / Hkv;
   a.q_stride = q_stride, a.k_stride = k_stride, a.v_stride = v_stride;
   a.dq_stride = dq_stride, a.dk_stride = dk_stride, a.dv_stride = dv_stride;

@@ -184,6 +184,21 @@ __device__ __forceinline__ void dma_16b(__amdgpu_buffer_rsrc_t rsrc, unsigned vo
       : "v"(voff), "s"(lds_base), "s"(rsrc));
 }
 
+// The same with 4 bytes per lane (256 bytes).
+__device__ __forceinline__ void dma_4b(__amdgpu_buffer_rsrc_t rsrc, unsigned voff,
+                                       unsigned lds_base) {
+  unsigned saved;
+  asm volatile(
+      "s_mov_b32 %0, m0\n\t"
+      "s_mov_b32 m0, %2\n\t"
+      "s_nop 0\n\t"
+      "buffer_load_dword %1, %3, 0 offen lds\n\t"
+      "s_nop 0\n\t"
+      "s_mov_b32 m0, %0"
+      : "=&s"(saved)
+      : "v"(voff), "s"(lds_base), "s"(rsrc));
+}
+
 // LDS byte address of a __shared__ pointer (the low half of its generic address), wave-uniform.
 __device__ __forceinline__ unsigned lds_addr(const void *p) {
   return __builtin_amdgcn_readfirstlane(static_cast<unsigned>(reinterpret_cast<uintptr_t>(p)));

@@ -121,8 +121,8 @@ struct AttnArgs {
 };
 hipError_t launch_local_attention(const AttnArgs &a, hipStream_t s);
 
-// Its backward. delta [B][Hq][T] and part (dK, dV partial sums of the key blocks that are split) lie
-// in the workspace; key blocks with sinks have s_sink splits, the others s_win.
+// Its backward. stat [B][Hq][T] (lse in exp2 units, delta) and part (dK, dV partial sums of the key
+// blocks that are split) lie in the workspace; key blocks with sinks have s_sink splits, the others s_win.
 struct AttnBwdPlan {
   int nsb, s_sink, s_win;  // key blocks with sinks; splits of those and of the others
   int slots;               // workgroups per (sequence, key/value head)
@@ -132,7 +132,8 @@ struct AttnBwdArgs {
   const float *lse;
   const int *lens;  // [B] or NULL
   void *dq, *dk, *dv;
-  float *delta, *part;
+  float2 *stat;
+  float *part;
   int B, T, Hq, Hkv, group;
   long long q_stride, k_stride, v_stride, dq_stride, dk_stride, dv_stride;
   int window, sinks;
@@ -140,7 +141,7 @@ struct AttnBwdArgs {
   int nsb, s_sink, s_win, slots;
 };
 AttnBwdPlan attn_bwd_plan(int B, int T, int Hq, int Hkv, int window, int sinks);
-size_t attn_bwd_delta_floats(int B, int T, int Hq);
+size_t attn_bwd_stat_bytes(int B, int T, int Hq);
 size_t attn_bwd_part_floats(const AttnBwdPlan &p, int B, int Hkv, int dh);
 hipError_t launch_local_attention_backward(const AttnBwdArgs &a, int dh, hipStream_t s);
 

@@ -38,16 +38,9 @@
 // so that four lanes that read four consecutive key rows at 16 consecutive d hand each of 16 lanes
 // one d over the four keys; the V rows' chunks are XOR-swizzled so that the 8 rows one read
 // touches fall on different banks.
-//
-// local_mqa_fwd<DH, true> is the same kernel for rglru_local_attention: several key/value heads
-// (query head h reads head h / G), token strides, a length per sequence, the first `sinks`
-// positions visible to all later ones, and the logarithm of the softmax's denominator. The block
-// walk then goes over the blocks that hold sinks before those of the window; a sequence's buffer
-// ends at its length, so that rows past it read zero whatever is there.
 #include "rglru_launch.h"
 #include "rglru_mfma.h"
 
-#include <algorithm>
 #include <type_traits>
 
 namespace rglru {
@@ -80,9 +73,6 @@ template <int DH> struct Mqa {
   static constexpr int kLdsBytes = 4 * kKElems * 2 + kXpBytes;
 };
 
-// s c - m c in one FMA is off by the rounding of m c, 2^-24 of it: for scores beyond this (in exp2
-// units) the difference s - m is formed first
-constexpr float kBigScore = 16384.0f;
 constexpr int kSplitKeys = 256;  // P as hi + lo below this many keys per row (see split)
 
 typedef short i16x4_t __attribute__((ext_vector_type(4)));
@@ -90,60 +80,10 @@ typedef __attribute__((address_space(3))) i16x4_t lds_i16x4_t;
 typedef __attribute__((address_space(3))) u32x4_t lds_u32x4_t;
 typedef __attribute__((address_space(3))) float lds_float_t;
 
-// What rglru_local_attention has beyond rglru_local_mqa.
-struct MqaExt {
-  const int *lens;        // [B] or NULL
-  float *lse;             // [B][Hq][T] or NULL
-  size_t q_stride;        // elements from token to token
-  unsigned k_stride, v_stride;
-  int group;              // query heads per key/value head
-  int sinks;
-  float floor;            // the running maximum's start: below every score, floor * c finite
-};
-
-// o of one row from the definition alone, one key at a time (DH / 64 values of every key row per
-// lane; the lanes keep the columns d0 + lane.. < d0 + DH / 2 of o). Only for rows whose o came out
-// non-finite although their scores are finite: the tile's P.V adds 0 * v for the keys that a row
-// does not see, which is not 0 where v is infinite or NaN.
 template <int DH>
-__device__ __forceinline__ void exact_row(const bf16_t *q, const bf16_t *k, const bf16_t *v,
-                                          bf16_t *o, const MqaExt &x, int t, int W, float c, int d0,
-                                          int lane) {
-  constexpr int kPer = DH / 64;
-  float qv[kPer];
-#pragma unroll
-  for (int i = 0; i < kPer; ++i) qv[i] = bf16_to_f32(q[lane * kPer + i]);
-  float m = x.floor, l = 0.0f, a[2] = {0.0f, 0.0f};
-  const int lo = max(0, t - W + 1);
-  for (int u = x.sinks > 0 ? 0 : lo; u <= t;) {
-    float s = 0.0f;
-#pragma unroll
-    for (int i = 0; i < kPer; ++i)
-      s = fmaf(qv[i], bf16_to_f32(k[static_cast<size_t>(u) * x.k_stride + lane * kPer + i]), s);
-#pragma unroll
-    for (int e = 1; e < 64; e <<= 1) s += __shfl_xor(s, e, 64);
-    const float mn = fmaxf(m, s);
-    const float corr = __builtin_amdgcn_exp2f((m - mn) * c);
-    const float p = __builtin_amdgcn_exp2f((s - mn) * c);
-    m = mn;
-    l = l * corr + p;
-#pragma unroll
-    for (int i = 0; i < 2; ++i)
-      if (lane + 64 * i < DH / 2)
-        a[i] = a[i] * corr +
-               p * bf16_to_f32(v[static_cast<size_t>(u) * x.v_stride + d0 + lane + 64 * i]);
-    ++u;
-    if (u == x.sinks && u < lo) u = lo;
-  }
-#pragma unroll
-  for (int i = 0; i < 2; ++i)
-    if (lane + 64 * i < DH / 2) o[d0 + lane + 64 * i] = f32_to_bf16(a[i] / l);
-}
-
-template <int DH, bool EXT>
 __global__ __launch_bounds__(Mqa<DH>::kThreads, 1) void local_mqa_fwd(
     const bf16_t *__restrict__ q, const bf16_t *__restrict__ k, const bf16_t *__restrict__ v,
-    bf16_t *__restrict__ o, int T, int Hq, int W, float c, MqaExt x) {  // c = scale * log2(e)
+    bf16_t *__restrict__ o, int T, int Hq, int W, float c) {  // c = scale * log2(e)
   typedef Mqa<DH> M;
   __shared__ __attribute__((aligned(16))) unsigned char smem[M::kLdsBytes];
   bf16_t *const Kbuf = reinterpret_cast<bf16_t *>(smem);  // [2][kKElems]
@@ -168,26 +108,9 @@ __global__ __launch_bounds__(Mqa<DH>::kThreads, 1) void local_mqa_fwd(
   const int b = (lin % nbh) / Hq;
   const int qw = q0 + 32 * (w >> 1);  // the pair's first row
   const int qr = qw + lrow;           // this lane's row
-  const size_t ostride = static_cast<size_t>(Hq) * DH;  // elements per position of o (and q)
-  const size_t qstride = EXT ? x.q_stride : ostride;
-  const unsigned kstride = EXT ? x.k_stride : DH, vstride = EXT ? x.v_stride : DH;
-  const size_t kvoff = EXT ? static_cast<size_t>(h / x.group) * DH : 0;
-  const bf16_t *kb_ = k + static_cast<size_t>(b) * T * kstride + kvoff;
-  const bf16_t *vb_ = v + static_cast<size_t>(b) * T * vstride + kvoff;
-  const int sinks = EXT ? x.sinks : 0;
-  // this sequence's tokens
-  const int len = EXT && x.lens ? min(max(x.lens[b], 0), T) : T;
-  if (EXT && q0 >= len) {  // no row of the block belongs to the sequence: o = 0, lse = -inf
-    for (int i = tid; i < M::kQB * (DH / 8); i += M::kThreads) {
-      const int t = q0 + i / (DH / 8);
-      if (t < T)
-        *reinterpret_cast<u32x4_t *>(o + (static_cast<size_t>(b) * T + t) * ostride +
-                                     static_cast<size_t>(h) * DH + (i % (DH / 8)) * 8) = u32x4_t{};
-    }
-    if (x.lse && tid < M::kQB && q0 + tid < T)
-      x.lse[(static_cast<size_t>(b) * Hq + h) * T + q0 + tid] = -__builtin_inff();
-    return;
-  }
+  const size_t qstride = static_cast<size_t>(Hq) * DH;  // elements per position of q and o
+  const bf16_t *kb_ = k + static_cast<size_t>(b) * T * DH;
+  const bf16_t *vb_ = v + static_cast<size_t>(b) * T * DH;
   // this wave's P-exchange slot (its P; before that, the partner's row maxima) and the partner's
   lds_u32x4_t *const xp_me = xp + w * 4 * 64;
   lds_u32x4_t *const xp_pa = xp + (w ^ 1) * 4 * 64;
@@ -216,15 +139,8 @@ __global__ __launch_bounds__(Mqa<DH>::kThreads, 1) void local_mqa_fwd(
   const bool split = min(q0 + 1, W) < kSplitKeys;
   // keys this workgroup needs: [lo, hi]
   const int lo = max(0, q0 - W + 1);
-  const int hi = min(len - 1, q0 + M::kQB - 1);
-  const int kb_last = hi / M::kKB;
-  // the blocks [0, ns) that hold sinks before the window's first block, then the window's
-  const int ns = EXT ? min((sinks + M::kKB - 1) / M::kKB, lo / M::kKB) : 0;
-  const int kb_win = lo / M::kKB, kb_first = EXT && ns > 0 ? 0 : kb_win;
-  auto next_block = [&](int kb) { return EXT && kb + 1 == ns ? kb_win : kb + 1; };
-  // K and V buffer of a block: alternating along the walk
-  const int skip = EXT ? (kb_win - ns) & 1 : 0;
-  auto buf_of = [&](int kb) { return EXT ? (kb ^ (kb >= kb_win ? skip : 0)) & 1 : kb & 1; };
+  const int hi = min(T - 1, q0 + M::kQB - 1);
+  const int kb_first = lo / M::kKB, kb_last = hi / M::kKB;
 
   // ---- staging by direct buffer-to-LDS loads (no registers; rows past T read zero: each buffer
   // covers exactly sequence b). K: chunk c of row r sits at c ^ (r & 15) (fewer bits when a row
@@ -232,11 +148,9 @@ __global__ __launch_bounds__(Mqa<DH>::kThreads, 1) void local_mqa_fwd(
   // LDS serves in one pass, hit 16 different chunk slots. V: chunk c of row r at c ^ 4 (r & 7)
   // (within the row), so that the 4-chunk runs of 8 consecutive rows fall on different banks.
   const __amdgpu_buffer_rsrc_t kseq = __builtin_amdgcn_make_buffer_rsrc(
-      const_cast<bf16_t *>(EXT ? wave_uniform(kb_) : kb_), static_cast<short>(0),
-      EXT ? (static_cast<int>(kstride) * (len - 1) + DH) * 2 : T * DH * 2, kRawWord3);
+      const_cast<bf16_t *>(kb_), static_cast<short>(0), T * DH * 2, kRawWord3);
   const __amdgpu_buffer_rsrc_t vseq = __builtin_amdgcn_make_buffer_rsrc(
-      const_cast<bf16_t *>(EXT ? wave_uniform(vb_) : vb_), static_cast<short>(0),
-      EXT ? (static_cast<int>(vstride) * (len - 1) + DH) * 2 : T * DH * 2, kRawWord3);
+      const_cast<bf16_t *>(vb_), static_cast<short>(0), T * DH * 2, kRawWord3);
   const int krow_l = lane / M::kCPR, kchunk_p = lane % M::kCPR;  // this lane's (row, slot)
   // this wave's ii-th load of block kb's K rows (or V rows) into buffer dst; kb < 0 fills dst
   // with zeros without touching memory (its offsets lie past the buffer's range). A wave that
@@ -245,9 +159,8 @@ __global__ __launch_bounds__(Mqa<DH>::kThreads, 1) void local_mqa_fwd(
   auto load_rows = [&](bool isv, int ii, int kb, int dst_buf) {
     const int i = w + M::kWaves * ii;
     const int row = i * M::kRPI + krow_l;
-    const unsigned rb = (isv ? vstride : kstride) * 2;  // bytes from row to row
-    const unsigned rowoff = (kb < 0 ? kNoRows : static_cast<unsigned>(kb * M::kKB) * rb) +
-                            static_cast<unsigned>(row) * rb;
+    const unsigned rowoff = (kb < 0 ? kNoRows : static_cast<unsigned>(kb * M::kKB * DH * 2)) +
+                            static_cast<unsigned>(row * DH * 2);
     const int sw = isv ? (4 * (row & 7)) & (M::kCPR - 1) : row & M::kKSw;
     const unsigned off = rowoff + static_cast<unsigned>((kchunk_p ^ sw) * 16);
     const bf16_t *dst = (isv ? Vbuf : Kbuf) + dst_buf * M::kKElems + i * 512;
@@ -272,17 +185,16 @@ __global__ __launch_bounds__(Mqa<DH>::kThreads, 1) void local_mqa_fwd(
     vbase = vr * DH + 8 * ((d0 >> 3) & 3) + (d0 & 7);
     vx = 32 * ((side * M::kDT) ^ (vsw >> 2));
   }
-  const float floor_m = EXT ? x.floor : -1e30f;
-  float m_run = floor_m, l_run = 0.0f;  // finite start: fully masked blocks give p = 0, corr = 1
+  float m_run = -1e30f, l_run = 0.0f;  // finite start: fully masked blocks give p = 0, corr = 1
   int kn = -1, kn_buf = 0;             // the K rows loading in segment B: block, buffer
   f32x16_t sacc = f32x16_t{};          // S^T of this wave's 32 keys, then their P
-  float mx = floor_m;                  // this block's row max over my keys
+  float mx = -1e30f;                   // this block's row max over my keys
   u32x4_t pown[4];                     // my P: (step 0 hi, lo, step 1 hi, lo)
 
   // does any (key, row) pair of the pair's rows see each other in block kb?
   auto visible = [&](int kb) {
     const int K0 = kb * M::kKB;
-    return K0 <= qw + 31 && (K0 + M::kKB - 1 > qw - W || K0 < sinks) && qw < len;
+    return K0 <= qw + 31 && K0 + M::kKB - 1 > qw - W && qw < T;
   };
 
   // ---- S^T = K Q^T for this wave's 32 keys x 32 rows of block kb, one accumulator chain (K
@@ -290,7 +202,7 @@ __global__ __launch_bounds__(Mqa<DH>::kThreads, 1) void local_mqa_fwd(
   // the MFMAs), then the mask and the row max over my keys, stored for the partner
   auto block_s = [&](int kb, auto with_loads) {
     constexpr bool kLd = decltype(with_loads)::value;  // this block's V rows, between the MFMAs
-    const bf16_t *Ks = Kbuf + buf_of(kb) * M::kKElems;
+    const bf16_t *Ks = Kbuf + (kb & 1) * M::kKElems;
     sacc = f32x16_t{};
     auto kfrag = [&](int s) {
       const int r = 32 * side + lrow;
@@ -302,7 +214,7 @@ __global__ __launch_bounds__(Mqa<DH>::kThreads, 1) void local_mqa_fwd(
 #pragma unroll
     for (int s = 0; s < M::kKS; ++s) {
       if (s + 2 < M::kKS) kf[(s + 2) % 3] = kfrag(s + 2);
-      if (kLd && s < M::kLPW) load_rows(true, s, kb, buf_of(kb));
+      if (kLd && s < M::kLPW) load_rows(true, s, kb, kb & 1);
       sacc = __builtin_amdgcn_mfma_f32_32x32x16_bf16(kf[s % 3], qf[s], sacc, 0, 0, 0);
     }
     __builtin_amdgcn_sched_group_barrier(0x100, M::kKS > 1 ? 2 : 1, 0);  // steps 0, 1
@@ -314,8 +226,7 @@ __global__ __launch_bounds__(Mqa<DH>::kThreads, 1) void local_mqa_fwd(
     }
     // mask where some pair is out of the window, the causal order or the sequence
     const int Ks0 = kb * M::kKB + 32 * side;
-    const bool full =
-        Ks0 + 31 <= qw && (Ks0 > qw + 31 - W || Ks0 + 31 < sinks) && Ks0 + 31 < len;
+    const bool full = Ks0 + 31 <= qw && Ks0 > qw + 31 - W && Ks0 + 31 < T;
     if (!full) {
       // lane terms re-derived from the thread index here (this path is rare; kept live, they
       // would be spilled, and a reload waits for the loads in flight)
@@ -324,8 +235,7 @@ __global__ __launch_bounds__(Mqa<DH>::kThreads, 1) void local_mqa_fwd(
 #pragma unroll
       for (int j = 0; j < 16; ++j) {
         const int dk = 8 * (j >> 2) + (j & 3);  // key - (key of j = 0)
-        const int key = Ks0 + 4 * ((tx >> 5) & 1) + dk;
-        const bool ok = dk <= rel && (dk > rel - W || (EXT && key < sinks)) && key < len;
+        const bool ok = dk <= rel && dk > rel - W && Ks0 + 4 * ((tx >> 5) & 1) + dk < T;
         sacc[j] = ok ? sacc[j] : -__builtin_inff();
       }
     }
@@ -336,7 +246,7 @@ __global__ __launch_bounds__(Mqa<DH>::kThreads, 1) void local_mqa_fwd(
 #pragma unroll
       for (int j = 2; j < 8; ++j) mq[i] = fmaxf(mq[i], sacc[8 * i + j]);
     }
-    mx = fmaxf(fmaxf(mq[0], mq[1]), floor_m);
+    mx = fmaxf(fmaxf(mq[0], mq[1]), -1e30f);
     mx = fmaxf(mx, __shfl_xor(mx, 32, 64));
     if (half == 0) mx_out[lrow] = mx;
   };
@@ -365,16 +275,9 @@ __global__ __launch_bounds__(Mqa<DH>::kThreads, 1) void local_mqa_fwd(
     }
     const float mc = m_run * c;
     float pq[2] = {0.0f, 0.0f};
-    if (EXT && __any(fabsf(mc) > kBigScore)) {  // wave-uniform
-#pragma unroll
-      for (int j = 0; j < 16; ++j) sacc[j] = (sacc[j] - m_run) * c;
-    } else {
-#pragma unroll
-      for (int j = 0; j < 16; ++j) sacc[j] = fmaf(sacc[j], c, -mc);
-    }
 #pragma unroll
     for (int j = 0; j < 16; ++j) {
-      const float p = __builtin_amdgcn_exp2f(sacc[j]);
+      const float p = __builtin_amdgcn_exp2f(fmaf(sacc[j], c, -mc));
       sacc[j] = p;
       pq[j >> 3] += p;
     }
@@ -407,9 +310,9 @@ __global__ __launch_bounds__(Mqa<DH>::kThreads, 1) void local_mqa_fwd(
   // first, then the partner's (read back with the lane's own layout). V^T operand of tile
   // j: row i = d (side) DH/2 + 32 j + i, k = the step's 8 keys of this half (kc..kc+3,
   // kc+8..kc+11), two transposing reads of 4 keys each. Loads of block kn's K rows sit between.
-  auto block_pv = [&](int vbuf, auto with_loads, int kn) {
+  auto block_pv = [&](int kb, auto with_loads, int kn) {
     constexpr bool kLd = decltype(with_loads)::value;
-    const bf16_t *Vs = Vbuf + vbuf * M::kKElems;
+    const bf16_t *Vs = Vbuf + (kb & 1) * M::kKElems;
     auto vfrag = [&](int s4, int j) {
       const bf16_t *p = Vs + (vbase + (vx ^ (32 * j))) + s4 * 16 * DH;
       const i16x4_t a = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_i16x4_t *)p);
@@ -448,28 +351,27 @@ __global__ __launch_bounds__(Mqa<DH>::kThreads, 1) void local_mqa_fwd(
   // (lag) are read in the next segment, before the reader writes its P over them; P written in
   // segment B (lead) or A (lag) is read in the next segment.
 #pragma unroll
-  for (int ii = 0; ii < M::kLPW; ++ii) load_rows(false, ii, kb_first, buf_of(kb_first));
+  for (int ii = 0; ii < M::kLPW; ++ii) load_rows(false, ii, kb_first, kb_first & 1);
   __builtin_amdgcn_s_waitcnt(0x0F70);  // vmcnt(0): this wave's K rows of the first block landed
   lds_barrier();
   bool pending = false;  // lag: the previous block's softmax and P.V are still to do
   const std::true_type loads;
   const std::false_type no_loads;
-  for (int kb = kb_first; kb <= kb_last; kb = next_block(kb)) {
+  for (int kb = kb_first; kb <= kb_last; ++kb) {
     const bool vis = visible(kb);
-    const int cur = buf_of(kb);
-    kn = kb < kb_last ? next_block(kb) : -1;  // block whose K rows load during segment B
-    kn_buf = cur ^ 1;
+    kn = kb < kb_last ? kb + 1 : -1;  // block whose K rows load during segment B
+    kn_buf = (kb + 1) & 1;
     // segment A
     if (lead) {
       if (vis) {
         block_s(kb, loads);
       } else {
 #pragma unroll
-        for (int ii = 0; ii < M::kLPW; ++ii) load_rows(true, ii, kb, cur);
+        for (int ii = 0; ii < M::kLPW; ++ii) load_rows(true, ii, kb, kb & 1);
       }
     } else {
 #pragma unroll
-      for (int ii = 0; ii < M::kLPW; ++ii) load_rows(true, ii, kb, cur);
+      for (int ii = 0; ii < M::kLPW; ++ii) load_rows(true, ii, kb, kb & 1);
       if (pending) block_softmax(no_loads, kn);
     }
     lds_barrier();
@@ -483,7 +385,7 @@ __global__ __launch_bounds__(Mqa<DH>::kThreads, 1) void local_mqa_fwd(
       }
     } else {
       if (pending) {
-        block_pv(cur ^ 1, loads, kn);
+        block_pv(kb - 1, loads, kn);
       } else {
 #pragma unroll
         for (int ii = 0; ii < M::kLPW; ++ii) load_rows(false, ii, kn, kn_buf);
@@ -494,7 +396,7 @@ __global__ __launch_bounds__(Mqa<DH>::kThreads, 1) void local_mqa_fwd(
     lds_barrier();
     // segment C
     if (lead) {
-      if (vis) block_pv(cur, no_loads, kn);
+      if (vis) block_pv(kb, no_loads, kn);
     } else {
       if (vis) block_s(kb, no_loads);
       pending = vis;
@@ -505,7 +407,7 @@ __global__ __launch_bounds__(Mqa<DH>::kThreads, 1) void local_mqa_fwd(
   // the lag's last block
   if (!lead && pending) block_softmax(no_loads, kn);
   lds_barrier();
-  if (!lead && pending) block_pv(buf_of(kb_last), no_loads, kn);
+  if (!lead && pending) block_pv(kb_last, no_loads, kn);
   lds_barrier();
   // ---- l over the whole window: my keys plus the partner's
   if (half == 0) mx_out[lrow] = l_run;
@@ -513,15 +415,10 @@ __global__ __launch_bounds__(Mqa<DH>::kThreads, 1) void local_mqa_fwd(
   l_run += mx_in[lrow];
   // ---- normalise and store. Lane = row qr; accumulator e of tile j is d = (side) DH/2 +
   // 32 j + 8 (e / 4) + 4 half + (e % 4): runs of 4 consecutive d.
-  const bool row_in = qr < len;
   if (qr < T) {
-    const float inv = row_in ? 1.0f / l_run : 0.0f;
-    bf16_t *op = o + (static_cast<size_t>(b) * T + qr) * ostride + static_cast<size_t>(h) * DH +
+    const float inv = 1.0f / l_run;
+    bf16_t *op = o + (static_cast<size_t>(b) * T + qr) * qstride + static_cast<size_t>(h) * DH +
                  side * M::kDH2 + 4 * half;
-    if (EXT && !row_in) {  // a row past the sequence, in a block with rows of it
-#pragma unroll
-      for (int j = 0; j < M::kDT; ++j) oacc[j] = f32x16_t{};
-    }
 #pragma unroll
     for (int j = 0; j < M::kDT; ++j)
 #pragma unroll
@@ -530,40 +427,13 @@ __global__ __launch_bounds__(Mqa<DH>::kThreads, 1) void local_mqa_fwd(
                                     pack_bf16x2(oacc[j][4 * g + 2] * inv, oacc[j][4 * g + 3] * inv));
         *reinterpret_cast<uint2 *>(op + 32 * j + 8 * g) = pk;
       }
-    // ln of the denominator sum_u exp(scale s_u) = scale m + ln l
-    if (EXT && x.lse && side == 0 && half == 0)
-      x.lse[(static_cast<size_t>(b) * Hq + h) * T + qr] =
-          row_in ? (m_run * c + __builtin_amdgcn_logf(l_run)) * 0.6931471805599453f
-                 : -__builtin_inff();
-  }
-  if constexpr (EXT) {
-    // rows with finite scores and a non-finite o: again, key by key
-    float worst = 0.0f;
-#pragma unroll
-    for (int j = 0; j < M::kDT; ++j)
-#pragma unroll
-      for (int e = 0; e < 16; ++e) worst = fmaf(0.0f, oacc[j][e], worst);  // NaN if any is not finite
-    const bool odd = row_in && !(worst == 0.0f) && l_run < __builtin_inff();
-    unsigned long long rows = __ballot(odd);
-    rows = (rows | (rows >> 32)) & 0xFFFFFFFFull;
-    while (rows) {
-      const int r = __builtin_ctzll(rows);
-      rows &= rows - 1;
-      const int t = qw + r;
-      exact_row<DH>(q + (static_cast<size_t>(b) * T + t) * qstride + static_cast<size_t>(h) * DH, kb_,
-                    vb_, o + (static_cast<size_t>(b) * T + t) * ostride + static_cast<size_t>(h) * DH,
-                    x, t, W, c, side * M::kDH2, lane);
-    }
   }
 }
 
 bool local_mqa_supported(int dh) { return dh == 64 || dh == 128 || dh == 256; }
 
-namespace {
-
-template <bool EXT>
-hipError_t launch(const void *q, const void *k, const void *v, void *o, int B, int T, int Hq, int dh,
-                  int window, float scale, const MqaExt &x, hipStream_t s) {
+hipError_t launch_local_mqa(const void *q, const void *k, const void *v, void *o, int B, int T,
+                            int Hq, int dh, int window, float scale, hipStream_t s) {
   const float c = scale * 1.4426950408889634f;
   const dim3 grid((T + Mqa<64>::kQB - 1) / Mqa<64>::kQB, Hq, B);
   const bf16_t *qq = static_cast<const bf16_t *>(q);
@@ -571,32 +441,12 @@ hipError_t launch(const void *q, const void *k, const void *v, void *o, int B, i
   const bf16_t *vv = static_cast<const bf16_t *>(v);
   bf16_t *oo = static_cast<bf16_t *>(o);
   switch (dh) {
-    case 64: local_mqa_fwd<64, EXT><<<grid, Mqa<64>::kThreads, 0, s>>>(qq, kk, vv, oo, T, Hq, window, c, x); break;
-    case 128: local_mqa_fwd<128, EXT><<<grid, Mqa<128>::kThreads, 0, s>>>(qq, kk, vv, oo, T, Hq, window, c, x); break;
-    case 256: local_mqa_fwd<256, EXT><<<grid, Mqa<256>::kThreads, 0, s>>>(qq, kk, vv, oo, T, Hq, window, c, x); break;
+    case 64: local_mqa_fwd<64><<<grid, Mqa<64>::kThreads, 0, s>>>(qq, kk, vv, oo, T, Hq, window, c); break;
+    case 128: local_mqa_fwd<128><<<grid, Mqa<128>::kThreads, 0, s>>>(qq, kk, vv, oo, T, Hq, window, c); break;
+    case 256: local_mqa_fwd<256><<<grid, Mqa<256>::kThreads, 0, s>>>(qq, kk, vv, oo, T, Hq, window, c); break;
     default: return hipErrorInvalidValue;
   }
   return hipGetLastError();
-}
-
-}  // namespace
-
-hipError_t launch_local_mqa(const void *q, const void *k, const void *v, void *o, int B, int T,
-                            int Hq, int dh, int window, float scale, hipStream_t s) {
-  return launch<false>(q, k, v, o, B, T, Hq, dh, window, scale, MqaExt{}, s);
-}
-
-hipError_t launch_local_attention(const AttnArgs &a, hipStream_t s) {
-  MqaExt x;
-  x.lens = a.lens;
-  x.lse = a.lse;
-  x.q_stride = static_cast<size_t>(a.q_stride);
-  x.k_stride = static_cast<unsigned>(a.k_stride);
-  x.v_stride = static_cast<unsigned>(a.v_stride);
-  x.group = a.Hq / a.Hkv;
-  x.sinks = std::min(a.sinks, a.T);
-  x.floor = a.floor;
-  return launch<true>(a.q, a.k, a.v, a.o, a.B, a.T, a.Hq, a.dh, std::min(a.window, a.T), a.scale, x, s);
 }
 
 }  // namespace rglru

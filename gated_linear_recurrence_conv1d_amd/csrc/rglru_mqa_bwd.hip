@@ -14,121 +14,58 @@
 // In both, the accumulator layout of S and dP (one column per lane, 16 rows) is already the B
 // operand's of the products that follow, if these take their k index in the accumulator's order:
 // P and dS never leave the registers. The other operand of those products is a transpose of a block
-// in LDS, read by ds_read_b64_tr_b16. Blocks arrive by direct buffer-to-LDS loads, two buffers, one
-// barrier per block. The 16-byte chunk c of row r lies at c ^ f(r), with f chosen so that both the
+// in LDS, read by ds_read_b64_tr_b16. Blocks of 32 rows arrive by direct buffer-to-LDS loads, two ahead,
+// in a ring of four: the products with a transposed operand lag by one block, so that they run on the
+// matrix cores beside the next block's exponentials (one wave per SIMD at dh 256: nothing else would
+// fill them). One barrier per block. The 16-byte chunk c of row r lies at c ^ f(r), with f chosen so that both the
 // row reads (16 consecutive rows at one chunk) and the transposing reads (4 consecutive rows at 4
 // consecutive chunks) of a pass fall on different banks.
 //
 // Key blocks that many rows see (all heads of a group; sinks: all rows after them) are split over
 // several workgroups, whose fp32 partial dK and dV attn_dkv_sum adds in order.
+#include "rglru_attn.h"
 #include "rglru_launch.h"
-#include "rglru_mfma.h"
 
 #include <algorithm>
 #include <type_traits>
 
 namespace rglru {
 
+using namespace attn;
+
 namespace {
 
-constexpr int kRawWord3 = 0x00020000;  // buffer descriptor word 3: raw 32-bit data, no swizzle
-constexpr float kLn2Inv = 1.4426950408889634f;
-
-typedef short i16x4_t __attribute__((ext_vector_type(4)));
-typedef __attribute__((address_space(3))) i16x4_t lds_i16x4_t;
-typedef float f32x4_t __attribute__((ext_vector_type(4)));
-
-constexpr int kWg = 4;         // waves per workgroup
-constexpr int kOwn = 32 * kWg; // rows (attn_dq) or keys (attn_dkv) per workgroup
-constexpr int kBlk = 64;       // rows per LDS block
+constexpr int kRing = 4;       // attn_dq's blocks in LDS: the last one, this one and two on their way
 constexpr int kFewKeys = 256;  // rows with fewer keys: delta from the sums, not from o
-
-// A block of kBlk rows of DH bf16 in LDS, and the ways it is filled and read.
-template <int DH> struct Blk {
-  static constexpr int kElems = kBlk * DH;
-  static constexpr int kCPR = DH / 8;                 // 16-byte chunks per row
-  static constexpr int kRPI = 64 / kCPR;              // rows per wave-wide 16-byte load
-  static constexpr int kLPW = kBlk / kRPI / kWg;      // loads per wave
-  static constexpr int kKS = DH / 16;                 // k-steps over d
-  static constexpr int kDT = DH / 32;                 // 32-wide d tiles
-  // chunk swizzle: rows of 128 bytes (DH 64) share a 256-byte bank line in pairs
-  __device__ __forceinline__ static int swz(int r) {
-    return DH == 64 ? 4 * ((r >> 1) & 1) + ((r >> 2) & 3) : 4 * (r & 3) + ((r >> 2) & 3);
-  }
-  // the buffer of a block's rows: those of the sequence from `base` on, at most kBlk (rows past its
-  // end then read zero, whatever lies there)
-  __device__ __forceinline__ static __amdgpu_buffer_rsrc_t rsrc(const bf16_t *base,
-                                                                unsigned row_bytes, int rows) {
-    return __builtin_amdgcn_make_buffer_rsrc(
-        const_cast<bf16_t *>(wave_uniform(base)), static_cast<short>(0),
-        static_cast<int>(row_bytes * static_cast<unsigned>(min(rows, kBlk) - 1)) + DH * 2, kRawWord3);
-  }
-  // this wave's ii-th load of the block's rows to dst
-  __device__ __forceinline__ static void load(__amdgpu_buffer_rsrc_t src, unsigned row_bytes,
-                                              int ii, int w, int lane, const bf16_t *dst) {
-    const int i = w + kWg * ii;
-    const int row = i * kRPI + lane / kCPR;
-    const unsigned off = static_cast<unsigned>(row) * row_bytes +
-                         static_cast<unsigned>(((lane % kCPR) ^ swz(row)) * 16);
-    dma_16b(src, off, lds_addr(dst + i * 512));
-  }
-  // A operand, rows 32 hf.., k = d of step s: 8 values of row lane % 32
-  __device__ __forceinline__ static bf16x8_t rows(const bf16_t *b, int hf, int s, int lane) {
-    const int r = lane & 31;
-    return load_bf16x8(b + (32 * hf + r) * DH + (((2 * s + (lane >> 5)) ^ swz(r)) * 8));
-  }
-  // A operand, rows d = 32 j + lane % 32, k = block rows 32 hf + 16 st + (4 h.., 8 + 4 h..), h =
-  // lane / 32: the accumulator's row order
-  __device__ __forceinline__ static bf16x8_t cols(const bf16_t *b, int hf, int st, int j, int lane) {
-    const int half = lane >> 5, r4 = (lane & 15) >> 2;
-    const int cl = 2 * ((lane >> 4) & 1) + ((lane & 3) >> 1);
-    const int rj = DH == 64 ? r4 >> 1 : r4;
-    const bf16_t *p = b + (32 * hf + 16 * st + 4 * half + r4) * DH + 32 * (j ^ rj) + 4 * (lane & 1);
-    const i16x4_t x = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_i16x4_t *)(p + 8 * (cl ^ half)));
-    const i16x4_t y = __builtin_amdgcn_ds_read_tr16_b64_v4i16(
-        (lds_i16x4_t *)(p + 8 * DH + 8 * (cl ^ half ^ 2)));
-    const uint2 ux = __builtin_bit_cast(uint2, x), uy = __builtin_bit_cast(uint2, y);
-    const u32x4_t u = {ux.x, ux.y, uy.x, uy.y};
-    return __builtin_bit_cast(bf16x8_t, u);
-  }
-};
-
-// Key row kr sees query row t (t, kr < len checked apart).
-__device__ __forceinline__ bool sees(int t, int u, int W, int sinks) {
-  return u <= t && (u > t - W || u < sinks);
-}
-
-__device__ __forceinline__ int clamp_len(const int *lens, int b, int T) {
-  return lens ? min(max(lens[b], 0), T) : T;
-}
 
 }  // namespace
 
 template <int DH>
 __global__ __launch_bounds__(64 * kWg, DH == 256 ? 1 : 2) void attn_dq(AttnBwdArgs a) {
   typedef Blk<DH> K;
-  __shared__ __attribute__((aligned(16))) bf16_t smem[4 * K::kElems];  // K[2], V[2]
-  bf16_t *const Kb = smem, *const Vb = smem + 2 * K::kElems;
+  __shared__ __attribute__((aligned(1024))) unsigned char smem[kRing * K::kSlot];
+  const unsigned lds = lds_addr(smem);
+  auto slot_of = [&](int i) { return lds + (i & (kRing - 1)) * K::kSlot; };
   const int tid = threadIdx.x, w = __builtin_amdgcn_readfirstlane(tid >> 6), lane = tid & 63;
   const int lrow = lane & 31, half = lane >> 5;
   const int T = a.T, Hq = a.Hq, W = a.window, sinks = a.sinks;
   // heavy first: query blocks from the last one down, all (sequence, head) pairs of one together
   const int nbh = a.B * Hq;
   const int nqb = (T + kOwn - 1) / kOwn;
-  const int qi = blockIdx.x / nbh, bh = blockIdx.x - qi * nbh;
+  const int qi = uni(blockIdx.x / nbh), bh = blockIdx.x - qi * nbh;
   const int q0 = (nqb - 1 - qi) * kOwn;
-  const int h = bh % Hq, b = bh / Hq;
+  const int b = uni(bh / Hq), h = bh - b * Hq;
   const int len = clamp_len(a.lens, b, T);
   const int qw = q0 + 32 * w, qr = qw + lrow;
   const size_t tok = static_cast<size_t>(b) * T;
   const int qc = min(qr, T - 1);
-  float *const delta = a.delta + (static_cast<size_t>(b) * Hq + h) * T;
+  float2 *const stat = a.stat + (static_cast<size_t>(b) * Hq + h) * T;
   bf16_t *const dq = static_cast<bf16_t *>(a.dq) + (tok + qc) * a.dq_stride + static_cast<size_t>(h) * DH;
   if (q0 >= len) {
     if (qr < T) {
 #pragma unroll
       for (int s = 0; s < K::kKS; ++s) *reinterpret_cast<u32x4_t *>(dq + 16 * s + 8 * half) = u32x4_t{};
-      if (half == 0) delta[qr] = 0.0f;
+      if (half == 0) stat[qr] = make_float2(__builtin_inff(), 0.0f);
     }
     return;
   }
@@ -159,7 +96,7 @@ __global__ __launch_bounds__(64 * kWg, DH == 256 ? 1 : 2) void attn_dq(AttnBwdAr
 #pragma unroll
   for (int s = 0; s < K::kKS; ++s) asm volatile("" ::"v"(qf[s]), "v"(gf[s]));
 
-  const int kvh = h / a.group;
+  const int kvh = uni(h / a.group);
   const bf16_t *kb_ = static_cast<const bf16_t *>(a.k) + tok * a.k_stride + static_cast<size_t>(kvh) * DH;
   const bf16_t *vb_ = static_cast<const bf16_t *>(a.v) + tok * a.v_stride + static_cast<size_t>(kvh) * DH;
   const unsigned krb = static_cast<unsigned>(a.k_stride) * 2, vrb = static_cast<unsigned>(a.v_stride) * 2;
@@ -169,16 +106,27 @@ __global__ __launch_bounds__(64 * kWg, DH == 256 ? 1 : 2) void attn_dq(AttnBwdAr
   const int ns = min((sinks + kBlk - 1) / kBlk, win);
   const int n = ns + end - win;
   auto first_row = [&](int i) { return (i < ns ? i : i - ns + win) * kBlk; };
-  auto load_block = [&](int i) {
-    const int u0 = first_row(i), buf = (i & 1) * K::kElems;
-    const __amdgpu_buffer_rsrc_t ks = K::rsrc(kb_ + static_cast<size_t>(u0) * a.k_stride, krb, len - u0);
-    const __amdgpu_buffer_rsrc_t vs = K::rsrc(vb_ + static_cast<size_t>(u0) * a.v_stride, vrb, len - u0);
-#pragma unroll
-    for (int ii = 0; ii < K::kLPW; ++ii) {
-      K::load(ks, krb, ii, w, lane, Kb + buf);
-      K::load(vs, vrb, ii, w, lane, Vb + buf);
-    }
+  // the loads of block i (past the last one: zeros, without touching memory, so that every step
+  // issues the same number)
+  struct Src {
+    __amdgpu_buffer_rsrc_t k, v;
   };
+  auto src_of = [&](int i) {
+    const int u0 = first_row(min(i, n - 1)), rows = i < n ? len - u0 : 0;
+    return Src{K::rsrc(kb_ + static_cast<size_t>(u0) * a.k_stride, krb, rows),
+               K::rsrc(vb_ + static_cast<size_t>(u0) * a.v_stride, vrb, rows)};
+  };
+  auto load_part = [&](const Src &src, int i, int ii) {
+    const unsigned dst = slot_of(i);
+    K::load(src.k, krb, ii, w, lane, dst);
+    K::load(src.v, vrb, ii, w, lane, dst + K::kBytes);
+  };
+  auto load_block = [&](int i) {
+    const Src src = src_of(i);
+#pragma unroll
+    for (int ii = 0; ii < K::kLPW; ++ii) load_part(src, i, ii);
+  };
+  const unsigned row_lane = K::row_lane(lane), col_lane = K::col_lane(lane);
   f32x16_t acc[K::kDT];
 #pragma unroll
   for (int j = 0; j < K::kDT; ++j) acc[j] = f32x16_t{};
@@ -188,56 +136,69 @@ __global__ __launch_bounds__(64 * kWg, DH == 256 ? 1 : 2) void attn_dq(AttnBwdAr
   auto walk = [&](auto delta_only) {
     constexpr bool kDelta = decltype(delta_only)::value;
     load_block(0);
+    load_block(1);
+    u32x4_t ds[2] = {};  // the last block's dS
     for (int i = 0; i < n; ++i) {
-      __builtin_amdgcn_s_waitcnt(0x0F70);  // vmcnt(0): this wave's rows of block i landed
-      lds_barrier();                        // everyone's landed; everyone is done with block i - 1
-      if (i + 1 < n) load_block(i + 1);
-      const bf16_t *Kc = Kb + (i & 1) * K::kElems, *Vc = Vb + (i & 1) * K::kElems;
-      const int u0 = first_row(i);
+      // this wave's rows of block i have landed (those of i + 1 may be on their way); then everyone's
+      // have, and everyone is done with block i - 2
+      __builtin_amdgcn_s_waitcnt(0x0F70 | (2 * K::kLPW));
+      lds_barrier();
+      const unsigned at = slot_of(i) + row_lane;
+      const int U = first_row(i);
+      f32x16_t s = f32x16_t{}, dp = f32x16_t{};
+      const Src src = src_of(i + 2);
 #pragma unroll
-      for (int hf = 0; hf < 2; ++hf) {
-        const int U = u0 + 32 * hf;
-        // some pair of (my rows, these keys) visible?
-        if (U > qw + 31 || (U + 31 <= qw - W && U >= sinks) || qw >= len) continue;
-        f32x16_t s = f32x16_t{}, dp = f32x16_t{};
+      for (int d = 0; d < K::kKS; ++d) {
+        if (d % 4 == 0) load_part(src, i + 2, d / 4);
+        s = __builtin_amdgcn_mfma_f32_32x32x16_bf16(K::rows(at, d), qf[d], s, 0, 0, 0);
+        dp = __builtin_amdgcn_mfma_f32_32x32x16_bf16(K::rows(at + K::kBytes, d), gf[d], dp, 0, 0, 0);
+      }
+      read_ahead<K::kKS, 2, 2, 3>();
+      const bool full = U + 31 <= qw && (U > qw + 31 - W || U + 31 < sinks);  // U + 31 < len follows
+      if (!full) {
 #pragma unroll
-        for (int d = 0; d < K::kKS; ++d)
-          s = __builtin_amdgcn_mfma_f32_32x32x16_bf16(K::rows(Kc, hf, d, lane), qf[d], s, 0, 0, 0);
-#pragma unroll
-        for (int d = 0; d < K::kKS; ++d)
-          dp = __builtin_amdgcn_mfma_f32_32x32x16_bf16(K::rows(Vc, hf, d, lane), gf[d], dp, 0, 0, 0);
-        const bool full = U + 31 <= qw && (U > qw + 31 - W || U + 31 < sinks);  // U + 31 < len follows
-        if (!full) {
-#pragma unroll
-          for (int e = 0; e < 16; ++e) {
-            const int u = U + 8 * (e >> 2) + 4 * half + (e & 3);
-            s[e] = sees(qr, u, W, sinks) && u < len ? s[e] : -__builtin_inff();
-            dp[e] = one || qr == 0 ? dl : dp[e];  // a row with one key has no gradient
-          }
-        }
-        if constexpr (kDelta) {
-#pragma unroll
-          for (int e = 0; e < 16; ++e) {
-            const float p = __builtin_amdgcn_exp2f(fmaf(s[e], a.c, -l2));
-            sp += p;
-            spd = fmaf(p, dp[e], spd);
-          }
-        } else {
-          u32x4_t ds[2];
-#pragma unroll
-          for (int e = 0; e < 16; e += 2) {
-            const float p0 = __builtin_amdgcn_exp2f(fmaf(s[e], a.c, -l2));
-            const float p1 = __builtin_amdgcn_exp2f(fmaf(s[e + 1], a.c, -l2));
-            ds[e >> 3][(e >> 1) & 3] = pack_bf16x2(p0 * (dp[e] - dl), p1 * (dp[e + 1] - dl));
-          }
-#pragma unroll
-          for (int st = 0; st < 2; ++st)
-#pragma unroll
-            for (int j = 0; j < K::kDT; ++j)
-              acc[j] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(
-                  K::cols(Kc, hf, st, j, lane), __builtin_bit_cast(bf16x8_t, ds[st]), acc[j], 0, 0, 0);
+        for (int e = 0; e < 16; ++e) {
+          const int u = U + 8 * (e >> 2) + 4 * half + (e & 3);
+          s[e] = sees(qr, u, W, sinks) && u < len ? s[e] : -__builtin_inff();
+          dp[e] = one || qr == 0 ? dl : dp[e];  // a row with one key has no gradient
         }
       }
+      if constexpr (kDelta) {
+#pragma unroll
+        for (int e = 0; e < 16; ++e) {
+          const float p = __builtin_amdgcn_exp2f(fmaf(s[e], a.c, -l2));
+          sp += p;
+          spd = fmaf(p, dp[e], spd);
+        }
+      } else {
+        // the last block's dS^T into dQ^T beside this block's exponentials (block 0: zero into it)
+        const unsigned pt = slot_of(i > 0 ? i - 1 : 0) + col_lane;
+        u32x4_t dn[2];
+#pragma unroll
+        for (int st = 0; st < 2; ++st)
+#pragma unroll
+          for (int j = 0; j < K::kDT; ++j)
+            acc[j] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(
+                K::cols(pt, st, j), __builtin_bit_cast(bf16x8_t, ds[st]), acc[j], 0, 0, 0);
+#pragma unroll
+        for (int e = 0; e < 16; e += 2) {
+          const float p0 = __builtin_amdgcn_exp2f(fmaf(s[e], a.c, -l2));
+          const float p1 = __builtin_amdgcn_exp2f(fmaf(s[e + 1], a.c, -l2));
+          dn[e >> 3][(e >> 1) & 3] = pack_bf16x2(p0 * (dp[e] - dl), p1 * (dp[e + 1] - dl));
+        }
+        ds[0] = dn[0];
+        ds[1] = dn[1];
+      }
+    }
+    __builtin_amdgcn_s_waitcnt(0x0F70);  // the zeros have landed too
+    if constexpr (!kDelta) {
+      const unsigned pt = slot_of(n - 1) + col_lane;
+#pragma unroll
+      for (int st = 0; st < 2; ++st)
+#pragma unroll
+        for (int j = 0; j < K::kDT; ++j)
+          acc[j] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(
+              K::cols(pt, st, j), __builtin_bit_cast(bf16x8_t, ds[st]), acc[j], 0, 0, 0);
     }
   };
   // delta from the rounded o is off by a 2^-9th of its terms, which averages out over many keys but
@@ -250,7 +211,7 @@ __global__ __launch_bounds__(64 * kWg, DH == 256 ? 1 : 2) void attn_dq(AttnBwdAr
     dl = spd / sp;
     lds_barrier();  // the buffers are filled again
   }
-  if (half == 0 && qr < T) delta[qr] = in ? dl : 0.0f;
+  if (half == 0 && qr < T) stat[qr] = make_float2(l2, in ? dl : 0.0f);
   walk(std::false_type{});
   if (qr >= T) return;
   const float f = in ? a.scale : 0.0f;
@@ -265,187 +226,214 @@ __global__ __launch_bounds__(64 * kWg, DH == 256 ? 1 : 2) void attn_dq(AttnBwdAr
     }
 }
 
-// Key block kb of a sequence: [64-row query blocks that see it], for the static length T; the
-// splits of blocks with sinks and of the others are a.s_sink and a.s_win.
-template <int DH>
-__global__ __launch_bounds__(64 * kWg, DH == 256 ? 1 : 2) void attn_dkv(AttnBwdArgs a) {
+// Workgroup = 128 keys, 8 waves: wave (kt, side) has keys 32 kt.. . Side 0 holds k (B operands) and
+// accumulates dV, side 1 holds v and accumulates dK, so that each fits in 256 registers and two waves,
+// one of each side, share a SIMD:
+//   step i, side 0: S(i) = Q K^T, P(i) = exp2(c S - lse), handed over through LDS; dV^T += dO^T P(i - 1)
+//   step i, side 1: dP(i) = dO V^T; dS(i - 1) = P(i - 1) (dP(i - 1) - delta); dK^T += Q^T dS(i - 1)
+// Both hold the same elements of S and dP in a lane, so the exchange is 16 values per lane, written and
+// read in the lane's own order, and the one-step lag makes one barrier per step enough.
+constexpr int kSlots = 3;  // blocks in LDS: the last one, this one, the next on its way
+template <int DH> struct DkvLds {
+  __attribute__((aligned(1024))) unsigned char blocks[kSlots * Blk<DH>::kSlot];
+  f32x4_t px[2][kWg][4][64];       // P on its way to side 1
+  float2 rowv[kSlots][kBlk];       // (lse in exp2 units, delta)
+};
+
+template <int DH, int SIDE>
+__device__ __forceinline__ void dkv_side(const AttnBwdArgs &a, DkvLds<DH> &sh, int kt, int lane) {
   typedef Blk<DH> K;
-  __shared__ __attribute__((aligned(16))) bf16_t smem[4 * K::kElems];  // Q[2], dO[2]
-  __shared__ __attribute__((aligned(16))) float rowv[2][2][kBlk];      // [buffer][lse, delta][row]
-  bf16_t *const Qb = smem, *const Gb = smem + 2 * K::kElems;
-  const int tid = threadIdx.x, w = __builtin_amdgcn_readfirstlane(tid >> 6), lane = tid & 63;
+  const unsigned lds = lds_addr(sh.blocks);
   const int lrow = lane & 31, half = lane >> 5;
   const int T = a.T, Hq = a.Hq, W = a.window, sinks = a.sinks;
-  const int bk = blockIdx.x / a.slots, slot = blockIdx.x - bk * a.slots;
-  const int kvh = bk % a.Hkv, b = bk / a.Hkv;
+  const int bk = uni(blockIdx.x / a.slots), wg_slot = blockIdx.x - bk * a.slots;
+  const int b = uni(bk / a.Hkv), kvh = bk - b * a.Hkv;
   const int head_slots = a.nsb * a.s_sink;
   int kb, sp, S;
-  if (slot < head_slots) {
+  if (wg_slot < head_slots) {
     S = a.s_sink;
-    kb = slot / S;
-    sp = slot - kb * S;
+    kb = uni(wg_slot / S);
+    sp = wg_slot - kb * S;
   } else {
     S = a.s_win;
-    kb = (slot - head_slots) / S;
-    sp = slot - head_slots - kb * S;
+    kb = uni((wg_slot - head_slots) / S);
+    sp = wg_slot - head_slots - kb * S;
     kb += a.nsb;
   }
   const int K0 = kb * kOwn;
   const int len = clamp_len(a.lens, b, T);
-  const int kw = K0 + 32 * w, kr = kw + lrow;
+  const int kw = K0 + 32 * kt, kr = kw + lrow;
   const size_t tok = static_cast<size_t>(b) * T;
-  // this lane's key: k and v as B operands (rows past the sequence: zero)
-  bf16x8_t kf[K::kKS], vf[K::kKS];
+  // this lane's key: k or v as B operands (rows past the sequence: zero)
+  bf16x8_t kf[K::kKS];
   {
-    const size_t row = tok + min(kr, T - 1);
-    const bf16_t *kp = static_cast<const bf16_t *>(a.k) + row * a.k_stride + static_cast<size_t>(kvh) * DH + 8 * half;
-    const bf16_t *vp = static_cast<const bf16_t *>(a.v) + row * a.v_stride + static_cast<size_t>(kvh) * DH + 8 * half;
+    const bf16_t *kp = static_cast<const bf16_t *>(SIDE ? a.v : a.k) +
+                       (tok + min(kr, T - 1)) * (SIDE ? a.v_stride : a.k_stride) +
+                       static_cast<size_t>(kvh) * DH + 8 * half;
     const bool in = kr < len;
 #pragma unroll
     for (int s = 0; s < K::kKS; ++s) {
       u32x4_t x = *reinterpret_cast<const u32x4_t *>(kp + 16 * s);
-      u32x4_t y = *reinterpret_cast<const u32x4_t *>(vp + 16 * s);
-      if (!in) x = y = u32x4_t{};
+      if (!in) x = u32x4_t{};
       kf[s] = __builtin_bit_cast(bf16x8_t, x);
-      vf[s] = __builtin_bit_cast(bf16x8_t, y);
     }
 #pragma unroll
-    for (int s = 0; s < K::kKS; ++s) asm volatile("" ::"v"(kf[s]), "v"(vf[s]));
+    for (int s = 0; s < K::kKS; ++s) asm volatile("" ::"v"(kf[s]));
   }
-  f32x16_t dk[K::kDT], dv[K::kDT];
+  f32x16_t acc[K::kDT];  // dV^T or dK^T
 #pragma unroll
-  for (int j = 0; j < K::kDT; ++j) dk[j] = dv[j] = f32x16_t{};
-  // items: (head of the group, 64-row block); this workgroup's share
+  for (int j = 0; j < K::kDT; ++j) acc[j] = f32x16_t{};
+  // items: (head of the group, 32-row block); this workgroup's share
   const int qfirst = K0 / kBlk;
   const int qlast_row = K0 < sinks ? len - 1
                                    : static_cast<int>(min(static_cast<long long>(len) - 1,
                                                           static_cast<long long>(K0) + kOwn - 2 + W));
   const int nq = K0 < len ? qlast_row / kBlk - qfirst + 1 : 0;
   const int items = nq * a.group;
-  const int share = (items + S - 1) / S;
+  const int share = uni((items + S - 1) / S);
   const int i0 = min(items, sp * share), i1 = min(items, i0 + share);
-  const unsigned qrb = static_cast<unsigned>(a.q_stride) * 2, grb = static_cast<unsigned>(Hq) * DH * 2;
-  const bf16_t *qb_ = static_cast<const bf16_t *>(a.q) + tok * a.q_stride;
-  const bf16_t *gb_ = static_cast<const bf16_t *>(a.do_) + tok * Hq * DH;
   const bool one = W == 1 && sinks == 0;
-  float pre = 0.0f;  // threads 0..127: the next block's lse or delta
-  auto load_item = [&](int i) {
-    const int hh = i / nq, q0 = (qfirst + i - hh * nq) * kBlk, buf = (i & 1) * K::kElems;
-    const int h = kvh * a.group + hh;
-    const __amdgpu_buffer_rsrc_t qs =
-        K::rsrc(qb_ + static_cast<size_t>(q0) * a.q_stride + static_cast<size_t>(h) * DH, qrb, len - q0);
-    const __amdgpu_buffer_rsrc_t gs =
-        K::rsrc(gb_ + (static_cast<size_t>(q0) * Hq + h) * DH, grb, len - q0);
-#pragma unroll
-    for (int ii = 0; ii < K::kLPW; ++ii) {
-      K::load(qs, qrb, ii, w, lane, Qb + buf);
-      K::load(gs, grb, ii, w, lane, Gb + buf);
-    }
-    if (tid < 2 * kBlk) {
-      const int t = q0 + (tid & (kBlk - 1));
-      const size_t at = (static_cast<size_t>(b) * Hq + h) * T + min(t, T - 1);
-      if (tid < kBlk)
-        pre = t < len ? a.lse[at] * kLn2Inv : __builtin_inff();
-      else
-        pre = t < len ? a.delta[at] : 0.0f;
+  struct At {  // an item's head of the group and block
+    int hh, qb;
+  };
+  auto next = [&](At &at) {
+    if (++at.qb == nq) {
+      at.qb = 0;
+      ++at.hh;
     }
   };
-  auto put_rows = [&](int i) {
-    if (tid < 2 * kBlk) rowv[i & 1][tid / kBlk][tid & (kBlk - 1)] = pre;
+  // side 0 brings the Q rows, side 1 the dO rows, and every wave the rows' stat
+  const unsigned rb = SIDE ? static_cast<unsigned>(Hq) * DH * 2 : static_cast<unsigned>(a.q_stride) * 2;
+  const bf16_t *const rows_ = static_cast<const bf16_t *>(SIDE ? a.do_ : a.q) + tok * (rb / 2);
+  auto load_item = [&](At at, int sl) {
+    const int q0 = (qfirst + at.qb) * kBlk, h = kvh * a.group + at.hh;
+    const __amdgpu_buffer_rsrc_t src =
+        K::rsrc(rows_ + static_cast<size_t>(q0) * (rb / 2) + static_cast<size_t>(h) * DH, rb, len - q0);
+    const __amdgpu_buffer_rsrc_t st = __builtin_amdgcn_make_buffer_rsrc(
+        wave_uniform(a.stat + (static_cast<size_t>(b) * Hq + h) * T + q0), static_cast<short>(0),
+        uni(min(len - q0, kBlk) * 8), kRawWord3);
+#pragma unroll
+    for (int ii = 0; ii < K::kLPW; ++ii)
+      K::load(src, rb, ii, kt, lane, lds + sl * K::kSlot + (SIDE ? K::kBytes : 0u));
+    dma_4b(st, lane * 4, lds_addr(sh.rowv[sl]));
+  };
+  const unsigned row_lane = K::row_lane(lane) + (SIDE ? K::kBytes : 0u);  // side 0 reads Q, 1 dO
+  const unsigned col_lane = K::col_lane(lane) + (SIDE ? 0u : K::kBytes);  // side 0 reads dO, 1 Q
+  auto products = [&](int sl, const u32x4_t (&pd)[2]) {
+    const unsigned pt = lds + sl * K::kSlot + col_lane;
+#pragma unroll
+    for (int st = 0; st < 2; ++st)
+#pragma unroll
+      for (int j = 0; j < K::kDT; ++j)
+        acc[j] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(
+            K::cols(pt, st, j), __builtin_bit_cast(bf16x8_t, pd[st]), acc[j], 0, 0, 0);
+  };
+  u32x4_t pd[2] = {};         // P (side 0) or dS (side 1) of the last item
+  f32x16_t dpl = f32x16_t{};  // side 1: dP of the last item
+  // side 1: dS of the last item (first row Ql) from its P, dP and delta
+  auto make_ds = [&](int buf, int sl, int Ql) {
+#pragma unroll
+    for (int e4 = 0; e4 < 4; ++e4) {
+      const f32x4_t p = sh.px[buf][kt][e4][lane];
+      const f32x4_t va = *reinterpret_cast<const f32x4_t *>(&sh.rowv[sl][8 * e4 + 4 * half]);
+      const f32x4_t vb = *reinterpret_cast<const f32x4_t *>(&sh.rowv[sl][8 * e4 + 4 * half + 2]);
+      float d[4] = {p[0] * (dpl[4 * e4] - va[1]), p[1] * (dpl[4 * e4 + 1] - va[3]),
+                    p[2] * (dpl[4 * e4 + 2] - vb[1]), p[3] * (dpl[4 * e4 + 3] - vb[3])};
+      if (one) d[0] = d[1] = d[2] = d[3] = 0.0f;  // a row with one key has no gradient
+      if (Ql + 8 * e4 + 4 * half == 0) d[0] = 0.0f;
+      pd[e4 >> 1][2 * (e4 & 1)] = pack_bf16x2(d[0], d[1]);
+      pd[e4 >> 1][2 * (e4 & 1) + 1] = pack_bf16x2(d[2], d[3]);
+    }
   };
   if (i0 < i1) {
-    load_item(i0);
-    put_rows(i0);
-  }
-  for (int i = i0; i < i1; ++i) {
-    __builtin_amdgcn_s_waitcnt(0x0F70);  // vmcnt(0): this wave's rows of item i landed
-    lds_barrier();
-    if (i + 1 < i1) load_item(i + 1);
-    const bf16_t *Qc = Qb + (i & 1) * K::kElems, *Gc = Gb + (i & 1) * K::kElems;
-    const int hh = i / nq, q0 = (qfirst + i - hh * nq) * kBlk;
-#pragma unroll
-    for (int hf = 0; hf < 2; ++hf) {
-      const int Q = q0 + 32 * hf;
-      if (kw > Q + 31 || (kw + 31 <= Q - W && kw >= sinks) || Q >= len || kw >= len) continue;
-      f32x16_t s = f32x16_t{}, dp = f32x16_t{};
+    At cur = {uni(i0 / nq), 0};
+    cur.qb = i0 - cur.hh * nq;
+    At head = cur;
+    int sl = 0, slp = 0;  // slots of this item and the last (the first one: its own, with P = 0)
+    int Ql = 0;
+    load_item(head, 0);
+    for (int i = i0; i < i1; ++i) {
+      __builtin_amdgcn_s_waitcnt(0x0F70);  // vmcnt(0): this wave's rows of item i landed
+      lds_barrier();  // everyone's landed, everyone is done with item i - 2 and P(i - 1) is written
+      const int sln = sl == kSlots - 1 ? 0 : sl + 1;
+      next(head);
+      if (i + 1 < i1) load_item(head, sln);
+      const int Q = (qfirst + cur.qb) * kBlk;
+      next(cur);
+      f32x16_t s = f32x16_t{};
+      const unsigned at = lds + sl * K::kSlot + row_lane;
 #pragma unroll
       for (int d = 0; d < K::kKS; ++d)
-        s = __builtin_amdgcn_mfma_f32_32x32x16_bf16(K::rows(Qc, hf, d, lane), kf[d], s, 0, 0, 0);
+        s = __builtin_amdgcn_mfma_f32_32x32x16_bf16(K::rows(at, d), kf[d], s, 0, 0, 0);
+      if constexpr (SIDE == 0) {
+        products(slp, pd);
+        const bool full = kw + 31 <= Q && (kw > Q + 31 - W || kw + 31 < sinks);
+        if (!full) {
 #pragma unroll
-      for (int d = 0; d < K::kKS; ++d)
-        dp = __builtin_amdgcn_mfma_f32_32x32x16_bf16(K::rows(Gc, hf, d, lane), vf[d], dp, 0, 0, 0);
-      const bool full = kw + 31 <= Q && (kw > Q + 31 - W || kw + 31 < sinks);
-      if (!full) {
-#pragma unroll
-        for (int e = 0; e < 16; ++e) {
-          const int t = Q + 8 * (e >> 2) + 4 * half + (e & 3);
-          s[e] = sees(t, kr, W, sinks) ? s[e] : -__builtin_inff();
-          // a row with one key has no gradient
-          if (one || t == 0) dp[e] = rowv[i & 1][1][32 * hf + 8 * (e >> 2) + 4 * half + (e & 3)];
+          for (int e = 0; e < 16; ++e) {
+            const int t = Q + 8 * (e >> 2) + 4 * half + (e & 3);
+            s[e] = sees(t, kr, W, sinks) ? s[e] : -__builtin_inff();
+          }
         }
+#pragma unroll
+        for (int e4 = 0; e4 < 4; ++e4) {
+          const f32x4_t va = *reinterpret_cast<const f32x4_t *>(&sh.rowv[sl][8 * e4 + 4 * half]);
+          const f32x4_t vb = *reinterpret_cast<const f32x4_t *>(&sh.rowv[sl][8 * e4 + 4 * half + 2]);
+          const f32x4_t p = {__builtin_amdgcn_exp2f(fmaf(s[4 * e4], a.c, -va[0])),
+                             __builtin_amdgcn_exp2f(fmaf(s[4 * e4 + 1], a.c, -va[2])),
+                             __builtin_amdgcn_exp2f(fmaf(s[4 * e4 + 2], a.c, -vb[0])),
+                             __builtin_amdgcn_exp2f(fmaf(s[4 * e4 + 3], a.c, -vb[2]))};
+          sh.px[i & 1][kt][e4][lane] = p;
+          pd[e4 >> 1][2 * (e4 & 1)] = pack_bf16x2(p[0], p[1]);
+          pd[e4 >> 1][2 * (e4 & 1) + 1] = pack_bf16x2(p[2], p[3]);
+        }
+      } else {
+        if (i > i0) make_ds((i - 1) & 1, slp, Ql);
+        products(slp, pd);
+        dpl = s;
       }
-      u32x4_t pp[2], ds[2];
-#pragma unroll
-      for (int e4 = 0; e4 < 4; ++e4) {
-        const f32x4_t l2 = *reinterpret_cast<const f32x4_t *>(&rowv[i & 1][0][32 * hf + 8 * e4 + 4 * half]);
-        const f32x4_t dl = *reinterpret_cast<const f32x4_t *>(&rowv[i & 1][1][32 * hf + 8 * e4 + 4 * half]);
-        float p[4], d[4];
-#pragma unroll
-        for (int e = 0; e < 4; ++e) {
-          p[e] = __builtin_amdgcn_exp2f(fmaf(s[4 * e4 + e], a.c, -l2[e]));
-          d[e] = p[e] * (dp[4 * e4 + e] - dl[e]);
-        }
-#pragma unroll
-        for (int e = 0; e < 2; ++e) {
-          pp[e4 >> 1][2 * (e4 & 1) + e] = pack_bf16x2(p[2 * e], p[2 * e + 1]);
-          ds[e4 >> 1][2 * (e4 & 1) + e] = pack_bf16x2(d[2 * e], d[2 * e + 1]);
-        }
-      }
-#pragma unroll
-      for (int st = 0; st < 2; ++st)
-#pragma unroll
-        for (int j = 0; j < K::kDT; ++j)
-          dv[j] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(
-              K::cols(Gc, hf, st, j, lane), __builtin_bit_cast(bf16x8_t, pp[st]), dv[j], 0, 0, 0);
-#pragma unroll
-      for (int st = 0; st < 2; ++st)
-#pragma unroll
-        for (int j = 0; j < K::kDT; ++j)
-          dk[j] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(
-              K::cols(Qc, hf, st, j, lane), __builtin_bit_cast(bf16x8_t, ds[st]), dk[j], 0, 0, 0);
+      Ql = Q;
+      slp = sl;
+      sl = sln;
     }
-    if (i + 1 < i1) put_rows(i + 1);
+    lds_barrier();  // P of the last item
+    if constexpr (SIDE == 1) make_ds((i1 - 1) & 1, slp, Ql);
+    products(slp, pd);
   }
   // lane = key kr; accumulator e of tile j is d = 32 j + 8 (e / 4) + 4 half + e % 4
   if (S > 1) {
-    float *pk = a.part + (static_cast<size_t>(blockIdx.x) * 2 * kOwn + (32 * w + lrow)) * DH + 4 * half;
-    float *pv = pk + static_cast<size_t>(kOwn) * DH;
+    float *pk = a.part + ((static_cast<size_t>(blockIdx.x) * 2 + (SIDE ? 0 : 1)) * kOwn + (32 * kt + lrow)) * DH + 4 * half;
 #pragma unroll
     for (int j = 0; j < K::kDT; ++j)
 #pragma unroll
       for (int g = 0; g < 4; ++g) {
-        const f32x4_t x = {dk[j][4 * g], dk[j][4 * g + 1], dk[j][4 * g + 2], dk[j][4 * g + 3]};
-        const f32x4_t y = {dv[j][4 * g], dv[j][4 * g + 1], dv[j][4 * g + 2], dv[j][4 * g + 3]};
+        const f32x4_t x = {acc[j][4 * g], acc[j][4 * g + 1], acc[j][4 * g + 2], acc[j][4 * g + 3]};
         *reinterpret_cast<f32x4_t *>(pk + 32 * j + 8 * g) = x;
-        *reinterpret_cast<f32x4_t *>(pv + 32 * j + 8 * g) = y;
       }
     return;
   }
   if (kr >= T) return;
-  bf16_t *ok = static_cast<bf16_t *>(a.dk) + (tok + kr) * a.dk_stride + static_cast<size_t>(kvh) * DH + 4 * half;
-  bf16_t *ov = static_cast<bf16_t *>(a.dv) + (tok + kr) * a.dv_stride + static_cast<size_t>(kvh) * DH + 4 * half;
+  bf16_t *out = static_cast<bf16_t *>(SIDE ? a.dk : a.dv) +
+                (tok + kr) * (SIDE ? a.dk_stride : a.dv_stride) + static_cast<size_t>(kvh) * DH + 4 * half;
+  const float f = SIDE ? a.scale : 1.0f;
 #pragma unroll
   for (int j = 0; j < K::kDT; ++j)
 #pragma unroll
-    for (int g = 0; g < 4; ++g) {
-      const float f = a.scale;
-      *reinterpret_cast<uint2 *>(ok + 32 * j + 8 * g) =
-          make_uint2(pack_bf16x2(dk[j][4 * g] * f, dk[j][4 * g + 1] * f),
-                     pack_bf16x2(dk[j][4 * g + 2] * f, dk[j][4 * g + 3] * f));
-      *reinterpret_cast<uint2 *>(ov + 32 * j + 8 * g) =
-          make_uint2(pack_bf16x2(dv[j][4 * g], dv[j][4 * g + 1]),
-                     pack_bf16x2(dv[j][4 * g + 2], dv[j][4 * g + 3]));
-    }
+    for (int g = 0; g < 4; ++g)
+      *reinterpret_cast<uint2 *>(out + 32 * j + 8 * g) =
+          make_uint2(pack_bf16x2(acc[j][4 * g] * f, acc[j][4 * g + 1] * f),
+                     pack_bf16x2(acc[j][4 * g + 2] * f, acc[j][4 * g + 3] * f));
+}
+
+template <int DH>
+__global__ __launch_bounds__(64 * 2 * kWg, 2) void attn_dkv(AttnBwdArgs a) {
+  __shared__ DkvLds<DH> sh;
+  const int w = uni(threadIdx.x >> 6), lane = threadIdx.x & 63;
+  // both sides pass the same number of barriers
+  if (w < kWg)
+    dkv_side<DH, 0>(a, sh, w, lane);
+  else
+    dkv_side<DH, 1>(a, sh, w - kWg, lane);
 }
 
 // dk, dv of the split key blocks: the partial sums in order, 8 values per lane.
@@ -501,7 +489,7 @@ AttnBwdPlan attn_bwd_plan(int B, int T, int Hq, int Hkv, int window, int sinks) 
   p.slots = p.nsb * p.s_sink + (nkb - p.nsb) * p.s_win;
   return p;
 }
-size_t attn_bwd_delta_floats(int B, int T, int Hq) { return static_cast<size_t>(B) * T * Hq; }
+size_t attn_bwd_stat_bytes(int B, int T, int Hq) { return static_cast<size_t>(B) * T * Hq * sizeof(float2); }
 size_t attn_bwd_part_floats(const AttnBwdPlan &p, int B, int Hkv, int dh) {
   if (p.s_sink == 1 && p.s_win == 1) return 0;
   return static_cast<size_t>(B) * Hkv * p.slots * 2 * kOwn * dh;
@@ -514,7 +502,7 @@ template <int DH> hipError_t launch(const AttnBwdArgs &a, hipStream_t s) {
   attn_dq<DH><<<nq * a.B * a.Hq, 64 * kWg, 0, s>>>(a);
   hipError_t e = hipGetLastError();
   if (e != hipSuccess) return e;
-  attn_dkv<DH><<<static_cast<unsigned>(a.slots) * a.B * a.Hkv, 64 * kWg, 0, s>>>(a);
+  attn_dkv<DH><<<static_cast<unsigned>(a.slots) * a.B * a.Hkv, 64 * 2 * kWg, 0, s>>>(a);
   e = hipGetLastError();
   if (e != hipSuccess || (a.s_sink == 1 && a.s_win == 1)) return e;
   const size_t n = static_cast<size_t>(a.T) * (DH / 8) * a.B * a.Hkv * 2;

@@ -283,9 +283,11 @@ def test_attention_backward_against_differences():
 
 
 def test_sinkless_single_head_is_local_mqa():
+    """One key/value head and no sinks: the multi-query kernel computes the same, each within the bound."""
     rng = np.random.default_rng(2)
     q, k, v = normal(rng, 2, 300, 4, 128), normal(rng, 2, 300, 1, 128), normal(rng, 2, 300, 1, 128)
-    assert torch.equal(rg.local_attention(q, k, v, 77), rg.local_mqa(q, k[:, :, 0], v[:, :, 0], 77))
+    bound = ab.attention_bounds(num(q), num(k), num(v), None, 77)[1]
+    check(rg.local_attention(q, k, v, 77), num(rg.local_mqa(q, k[:, :, 0], v[:, :, 0], 77)), 2 * bound, "o")
 
 
 @pytest.mark.parametrize("bad", [float("nan"), float("inf"), -float("inf")])

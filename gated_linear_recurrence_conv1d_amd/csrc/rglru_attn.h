@@ -23,14 +23,18 @@ constexpr int kWg = 4;         // waves per workgroup
 constexpr int kOwn = 32 * kWg; // rows (attn_dq) or keys (attn_dkv) per workgroup
 constexpr int kBlk = 32;       // rows per LDS block
 
+// An integer that is the same in every lane, kept in a scalar register (quotients and some minima run on
+// the vector unit; branches on such values, and descriptors made from them, then cost registers).
+__device__ __forceinline__ int uni(int v) { return __builtin_amdgcn_readfirstlane(v); }
+
 // A block of kBlk rows of DH bf16 in LDS, and the ways it is filled and read.
-template <int DH> struct Blk {
+template <int DH, int WAVES = kWg> struct Blk {  // WAVES: how many share the loads
   static constexpr unsigned kRowBytes = DH * 2;
   static constexpr unsigned kBytes = kBlk * kRowBytes;  // one block
   static constexpr unsigned kSlot = 2 * kBytes;         // a ring slot: a block of K (Q), one of V (dO)
   static constexpr int kCPR = DH / 8;                 // 16-byte chunks per row
   static constexpr int kRPI = 64 / kCPR;              // rows per wave-wide 16-byte load
-  static constexpr int kLPW = kBlk / kRPI / kWg;      // loads per wave and block
+  static constexpr int kLPW = kBlk / kRPI / WAVES;    // loads per wave and block
   static constexpr int kKS = DH / 16;                 // k-steps over d
   static constexpr int kDT = DH / 32;                 // 32-wide d tiles
   // chunk swizzle: rows of 128 bytes (DH 64) share a 256-byte bank line in pairs
@@ -46,14 +50,29 @@ template <int DH> struct Blk {
         rows > 0 ? static_cast<int>(row_bytes * static_cast<unsigned>(min(rows, kBlk) - 1)) + DH * 2 : 0,
         kRawWord3);
   }
-  // this wave's ii-th load of the block's rows to LDS byte address dst
-  __device__ __forceinline__ static void load(__amdgpu_buffer_rsrc_t src, unsigned row_bytes,
-                                              int ii, int w, int lane, unsigned dst) {
-    const int i = w + kWg * ii;
-    const int row = i * kRPI + lane / kCPR;
-    const unsigned off = static_cast<unsigned>(row) * row_bytes +
-                         static_cast<unsigned>(((lane % kCPR) ^ swz(row)) * 16);
-    dma_16b(src, off, static_cast<unsigned>(__builtin_amdgcn_readfirstlane(dst + i * 1024)));
+  // A wave's ii-th load of a block covers rows kPart ii + (its first) ..; the lane's byte offset in it
+  // depends on ii only through the chunk swizzle, whose bits repeat after kPar loads.
+  static constexpr int kPart = WAVES * kRPI;
+  static constexpr int kPar = kPart < 16 ? 16 / kPart : 1;
+  struct Lane {
+    unsigned off[kPar];
+  };
+  __device__ __forceinline__ static Lane load_lane(int w, int lane, unsigned row_bytes) {
+    const int row = w * kRPI + lane / kCPR;
+    Lane l;
+#pragma unroll
+    for (int p = 0; p < kPar; ++p)
+      l.off[p] = static_cast<unsigned>(row) * row_bytes +
+                 static_cast<unsigned>(((lane % kCPR) ^ swz(row + kPart * p)) * 16);
+    return l;
+  }
+  // that load: base is the block's first row, rows those of the sequence from there on, dst the block's
+  // LDS byte address
+  __device__ __forceinline__ static void load(const bf16_t *base, unsigned row_bytes, int rows, int ii,
+                                              int w, const Lane &l, unsigned dst) {
+    const __amdgpu_buffer_rsrc_t src =
+        rsrc(base + static_cast<size_t>(ii * kPart) * (row_bytes / 2), row_bytes, rows - ii * kPart);
+    dma_16b(src, l.off[ii % kPar], static_cast<unsigned>(uni(dst + (w + WAVES * ii) * 1024)));
   }
   // A block's two reads, from byte addresses that depend on the lane only through one register: the
   // row length and every block start are multiples of the bits that the steps change by XOR.
@@ -97,17 +116,13 @@ template <int N, int R, int M, int D> __device__ __forceinline__ void read_ahead
   }
 }
 
-// An integer that is the same in every lane, kept in a scalar register (quotients run on the vector
-// unit).
-__device__ __forceinline__ int uni(int v) { return __builtin_amdgcn_readfirstlane(v); }
-
 // Key row kr sees query row t (t, kr < len checked apart).
 __device__ __forceinline__ bool sees(int t, int u, int W, int sinks) {
   return u <= t && (u > t - W || u < sinks);
 }
 
 __device__ __forceinline__ int clamp_len(const int *lens, int b, int T) {
-  return lens ? min(max(uniform_load(lens, b), 0), T) : T;
+  return uni(lens ? min(max(uniform_load(lens, b), 0), T) : T);
 }
 
 // The key blocks that query rows q0 .. q0 + rows - 1 of a sequence of len tokens need, in order: those
@@ -115,9 +130,9 @@ __device__ __forceinline__ int clamp_len(const int *lens, int b, int T) {
 struct BlockWalk {
   int win, ns, n;  // the window's first block; sink blocks; blocks in all
   __device__ __forceinline__ BlockWalk(int q0, int rows, int len, int W, int sinks) {
-    win = max(0, q0 - W + 1) / kBlk;
-    ns = min((sinks + kBlk - 1) / kBlk, win);
-    n = ns + (min(len, q0 + rows) - 1) / kBlk + 1 - win;
+    win = uni(max(0, q0 - W + 1) / kBlk);
+    ns = uni(min((sinks + kBlk - 1) / kBlk, win));
+    n = uni(ns + (min(len, q0 + rows) - 1) / kBlk + 1 - win);
   }
   __device__ __forceinline__ int first_row(int i) const { return (i < ns ? i : i - ns + win) * kBlk; }
 };

@@ -7,13 +7,10 @@
 // One pass over the visible keys with a running maximum m and sum l per row. Both contractions put a
 // query row in each lane: S^T = K Q^T (A = K rows from LDS, B = q in registers for the kernel's life) and
 // O^T += V^T P^T (A = V^T from LDS by transposing reads, B = P). The accumulator layout of S^T is already the
-// B operand's of the second, so P never leaves its lane. A wave owns 32 RT rows and all of dh; four
-// waves are a workgroup, two workgroups share a CU, and each wave works alone between the barriers
-// (one per 32-key block), so that one wave's matrix work runs beside another's exponentials. Within a
-// wave the product with V lags by one block, beside the block's softmax (not where P is split: its lo
-// half would not fit in the registers over that time). Per block the LDS serves, for
-// four waves, dh / 16 row reads and as many transposing ones (half the rate), which is what bounds RT =
-// 1; with RT = 2 (dh <= 128) every read feeds two MFMAs.
+// B operand's of the second, so P never leaves its lane. A wave owns 32 rows and all of dh (64 registers of q
+// and 128 of O at dh 256: two waves per SIMD); four waves are a workgroup, at least two workgroups share a
+// CU, and each wave works alone between the barriers (one per 32-key block), so that one wave's matrix
+// work runs beside another's exponentials.
 #include "rglru_attn.h"
 #include "rglru_launch.h"
 
@@ -33,6 +30,7 @@ constexpr int kSplitKeys = 256;
 // s c - m c in one FMA is off by the rounding of m c, 2^-24 of it: for scores beyond this (in exp2
 // units) the difference s - m is formed first
 constexpr float kBigScore = 16384.0f;
+constexpr int kAhead = 3;  // MFMA steps that LDS operands are read ahead
 
 }  // namespace
 
@@ -63,6 +61,10 @@ __device__ __forceinline__ void exact_row(const bf16_t *q, const bf16_t *k, cons
 #pragma unroll
     for (int i = 0; i < kPer; ++i)
       a[i] = a[i] * corr + p * bf16_to_f32(v[static_cast<size_t>(u) * x.v_stride + lane * kPer + i]);
+    bool done = true;  // all of o is NaN already
+#pragma unroll
+    for (int i = 0; i < kPer; ++i) done = done && a[i] != a[i];
+    if (__all(done)) break;
     ++u;
     if (u == x.sinks && u < lo) u = lo;
   }
@@ -70,11 +72,11 @@ __device__ __forceinline__ void exact_row(const bf16_t *q, const bf16_t *k, cons
   for (int i = 0; i < kPer; ++i) o[lane * kPer + i] = f32_to_bf16(a[i] / l);
 }
 
-template <int DH, int RT>
+template <int DH>
 __global__ __launch_bounds__(64 * kWg, 2) void attn_fwd(AttnArgs x) {
   typedef Blk<DH> K;
-  constexpr int kRows = 32 * RT * kWg;  // per workgroup
-  __shared__ __attribute__((aligned(1024))) unsigned char smem[5 * K::kBytes];  // K[2], V[3]
+  constexpr int kRows = kOwn;  // per workgroup
+  __shared__ __attribute__((aligned(1024))) unsigned char smem[2 * K::kSlot];  // two slots of K, V
   const unsigned lds = lds_addr(smem);
   const int tid = threadIdx.x, w = uni(tid >> 6), lane = tid & 63;
   const int lrow = lane & 31, half = lane >> 5;
@@ -100,205 +102,193 @@ __global__ __launch_bounds__(64 * kWg, 2) void attn_fwd(AttnArgs x) {
       if (q0 + i < T) lse_[q0 + i] = -__builtin_inff();
     return;
   }
-  const int qw = q0 + 32 * RT * w;  // this wave's first row; its rows: qw + 32 r + lrow
+  const int qw = q0 + 32 * w, qr = qw + lrow;  // this wave's first row, this lane's row
   const bf16_t *const q_ = static_cast<const bf16_t *>(x.q) + tok * x.q_stride + static_cast<size_t>(h) * DH;
   const bf16_t *const k_ = static_cast<const bf16_t *>(x.k) + tok * x.k_stride + static_cast<size_t>(kvh) * DH;
   const bf16_t *const v_ = static_cast<const bf16_t *>(x.v) + tok * x.v_stride + static_cast<size_t>(kvh) * DH;
-  bf16x8_t qf[RT][K::kKS];
+  bf16x8_t qf[K::kKS];
+  {
+    const bf16_t *qp = q_ + static_cast<size_t>(min(qr, T - 1)) * x.q_stride + 8 * half;
 #pragma unroll
-  for (int r = 0; r < RT; ++r) {
-    const bf16_t *qp = q_ + static_cast<size_t>(min(qw + 32 * r + lrow, T - 1)) * x.q_stride + 8 * half;
+    for (int s = 0; s < K::kKS; ++s) qf[s] = load_bf16x8(qp + 16 * s);
+    // complete these loads here: the compiler does not see the LDS loads that share their counter
 #pragma unroll
-    for (int s = 0; s < K::kKS; ++s) qf[r][s] = load_bf16x8(qp + 16 * s);
+    for (int s = 0; s < K::kKS; ++s) asm volatile("" ::"v"(qf[s]));
   }
-  // complete these loads here: the compiler does not see the LDS loads that share their counter
-#pragma unroll
-  for (int r = 0; r < RT; ++r)
-#pragma unroll
-    for (int s = 0; s < K::kKS; ++s) asm volatile("" ::"v"(qf[r][s]));
   const BlockWalk walk(q0, kRows, len, W, sinks);
   const unsigned krb = static_cast<unsigned>(x.k_stride) * 2, vrb = static_cast<unsigned>(x.v_stride) * 2;
-  auto load_block = [&](int i, int vslot) {
-    const int u0 = walk.first_row(i);
-    const __amdgpu_buffer_rsrc_t ks = K::rsrc(k_ + static_cast<size_t>(u0) * x.k_stride, krb, len - u0);
-    const __amdgpu_buffer_rsrc_t vs = K::rsrc(v_ + static_cast<size_t>(u0) * x.v_stride, vrb, len - u0);
+  const typename K::Lane kl = K::load_lane(w, lane, krb), vl = K::load_lane(w, lane, vrb);
+  // the n-th of this wave's 2 kLPW loads of block i, of K and V in turn (past the last block: zeros,
+  // without touching memory)
+  auto load_part = [&](int i, int n) {
+    const int u0 = walk.first_row(min(i, walk.n - 1)), ii = n / 2, rows = i < walk.n ? len - u0 : 0;
+    const unsigned dst = lds + (i & 1) * K::kSlot;
+    if (n % 2 == 0)
+      K::load(k_ + static_cast<size_t>(u0) * x.k_stride, krb, rows, ii, w, kl, dst);
+    else
+      K::load(v_ + static_cast<size_t>(u0) * x.v_stride, vrb, rows, ii, w, vl, dst + K::kBytes);
+  };
+  auto load_block = [&](int i) {
 #pragma unroll
-    for (int ii = 0; ii < K::kLPW; ++ii) {
-      K::load(ks, krb, ii, w, lane, lds + (i & 1) * K::kBytes);
-      K::load(vs, vrb, ii, w, lane, lds + (2 + vslot) * K::kBytes);
-    }
+    for (int n = 0; n < 2 * K::kLPW; ++n) load_part(i, n);
   };
   const unsigned row_lane = K::row_lane(lane), col_lane = K::col_lane(lane);
 
-  unsigned odd[RT];  // rows to do again
+  unsigned odd = 0;  // rows to do again
   // the whole walk and the stores, P as bf16 (kSplit: as bf16 hi + lo)
   auto run = [&](auto split_c) {
     constexpr bool kSplit = decltype(split_c)::value;
-    f32x16_t acc[RT][K::kDT];  // O^T
-    float m[RT], l[RT];        // running maximum (of raw scores), and this half's sum
-    u32x4_t p[RT][2], pl[RT][2];  // the last block's P: two 16-key steps, hi (and lo)
+    f32x16_t acc[K::kDT];  // O^T
 #pragma unroll
-    for (int r = 0; r < RT; ++r) {
-#pragma unroll
-      for (int j = 0; j < K::kDT; ++j) acc[r][j] = f32x16_t{};
-      m[r] = x.floor;
-      l[r] = 0.0f;
-      p[r][0] = p[r][1] = u32x4_t{};
-    }
-    auto products = [&](int vslot) {
-      const unsigned at = lds + (2 + vslot) * K::kBytes + col_lane;
-#pragma unroll
-      for (int st = 0; st < 2; ++st)
-#pragma unroll
-        for (int j = 0; j < K::kDT; ++j) {
-          const bf16x8_t vt = K::cols(at, st, j);
-#pragma unroll
-          for (int r = 0; r < RT; ++r) {
-            acc[r][j] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(
-                vt, __builtin_bit_cast(bf16x8_t, p[r][st]), acc[r][j], 0, 0, 0);
-            if constexpr (kSplit)
-              acc[r][j] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(
-                  vt, __builtin_bit_cast(bf16x8_t, pl[r][st]), acc[r][j], 0, 0, 0);
-          }
-        }
-    };
-    bool ran = false;            // the last block was visible: its P is still to go into O
-    int vs = 0, vsp = 0;         // V slots of this block and the last
-    load_block(0, 0);
+    for (int j = 0; j < K::kDT; ++j) acc[j] = f32x16_t{};
+    float m = x.floor, l = 0.0f;  // running maximum (of raw scores), and this half's sum
+    load_block(0);
     for (int i = 0; i < walk.n; ++i) {
       __builtin_amdgcn_s_waitcnt(0x0F70);  // vmcnt(0): this wave's rows of block i landed
-      lds_barrier();                        // everyone's landed; everyone is done with block i - 2's V
-      const int vsn = vs == 2 ? 0 : vs + 1;
-      if (i + 1 < walk.n) load_block(i + 1, vsn);
+      lds_barrier();                        // everyone's landed; everyone is done with block i - 1
       const int U = walk.first_row(i);
-      const bool vis = U <= qw + 32 * RT - 1 && (U + 31 > qw - W || U < sinks) && qw < len;
-      // (after the last visible block once more, all masked: its P into O, then P = 0)
-      if (vis || (ran && !kSplit)) {
-        f32x16_t s[RT];
+      const bool vis = U <= qw + 31 && (U + 31 > qw - W || U < sinks) && qw < len;
+      // the next block's loads: between the MFMAs, or at once in a wave that sees nothing of this block
+      // (that branch kept apart from the next one: as its else, it costs registers)
+      int burst = vis ? 0 : 1;
+      asm volatile("" : "+v"(burst));
+      if (uni(burst)) load_block(i + 1);
+      if (!vis) continue;
+      const unsigned slot = lds + (i & 1) * K::kSlot;
+      // S^T: K rows read kAhead steps ahead, pinned by the scheduling barriers (the compiler else reads each
+      // right before its use)
+      f32x16_t s = f32x16_t{};
+      {
+        bf16x8_t kr[kAhead + 1];
 #pragma unroll
-        for (int r = 0; r < RT; ++r) s[r] = f32x16_t{};
-        const unsigned at = lds + (i & 1) * K::kBytes + row_lane;
+        for (int d = 0; d < kAhead; ++d) kr[d] = K::rows(slot + row_lane, d);
+        __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
         for (int d = 0; d < K::kKS; ++d) {
-          const bf16x8_t kr = K::rows(at, d);
-#pragma unroll
-          for (int r = 0; r < RT; ++r)
-            s[r] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(kr, qf[r][d], s[r], 0, 0, 0);
+          if (d + kAhead < K::kKS) kr[(d + kAhead) % (kAhead + 1)] = K::rows(slot + row_lane, d + kAhead);
+          if (d % 2 == 0) load_part(i + 1, d / 2);
+          s = __builtin_amdgcn_mfma_f32_32x32x16_bf16(kr[d % (kAhead + 1)], qf[d], s, 0, 0, 0);
+          __builtin_amdgcn_sched_barrier(0);
         }
-        if constexpr (!kSplit) products(vsp);  // the last block's (the first: P = 0)
-        const bool full = U + 31 <= qw && (U > qw + 32 * RT - 1 - W || U + 31 < sinks) && U + 31 < len;
-        if (!full) {
-#pragma unroll
-          for (int r = 0; r < RT; ++r)
-#pragma unroll
-            for (int e = 0; e < 16; ++e) {
-              const int u = U + 8 * (e >> 2) + 4 * half + (e & 3);
-              s[r][e] = sees(qw + 32 * r + lrow, u, W, sinks) && u < len ? s[r][e] : -__builtin_inff();
-            }
-        }
-#pragma unroll
-        for (int r = 0; r < RT; ++r) {
-          float mx = fmaxf(s[r][0], s[r][1]), my = fmaxf(s[r][2], s[r][3]);
-#pragma unroll
-          for (int e = 4; e < 16; e += 2) {
-            mx = fmaxf(mx, s[r][e]);
-            my = fmaxf(my, s[r][e + 1]);
-          }
-          float lo, hi;
-          halves(fmaxf(mx, my), lo, hi);
-          mx = fmaxf(fmaxf(lo, hi), x.floor);
-          // O and l are kept relative to a maximum that is raised only when a row's grows by more than
-          // 2^8: they share it, so the result does not change, and the rescale is rare
-          const bool raise = (mx - m[r]) * c > 8.0f;
-          if (__any(raise)) {
-            const float mn = raise ? mx : m[r];
-            const float corr = __builtin_amdgcn_exp2f((m[r] - mn) * c);
-            l[r] *= corr;
-            m[r] = mn;
-#pragma unroll
-            for (int j = 0; j < K::kDT; ++j) acc[r][j] *= corr;
-          }
-          const float mc = m[r] * c;
-          if (__any(fabsf(mc) > kBigScore)) {
-#pragma unroll
-            for (int e = 0; e < 16; ++e) s[r][e] = (s[r][e] - m[r]) * c;
-          } else {
-#pragma unroll
-            for (int e = 0; e < 16; ++e) s[r][e] = fmaf(s[r][e], c, -mc);
-          }
-          float l0 = 0.0f, l1 = 0.0f;
-#pragma unroll
-          for (int e = 0; e < 16; e += 2) {
-            const float a = __builtin_amdgcn_exp2f(s[r][e]), bb = __builtin_amdgcn_exp2f(s[r][e + 1]);
-            l0 += a;
-            l1 += bb;
-            const uint32_t hw = pack_bf16x2(a, bb);
-            p[r][e >> 3][(e >> 1) & 3] = hw;
-            if constexpr (kSplit) pl[r][e >> 3][(e >> 1) & 3] = pack_bf16x2(a - bf16lo(hw), bb - bf16hi(hw));
-          }
-          l[r] += l0 + l1;
-        }
-        if constexpr (kSplit) products(vs);
       }
-      ran = vis;
-      vsp = vs;
-      vs = vsn;
-    }
-    if constexpr (!kSplit) products(vsp);
-    // normalise and store; lane = row, accumulator e of tile j is d = 32 j + 8 (e / 4) + 4 half + e % 4
+      const bool full = U + 31 <= qw && (U > qw + 31 - W || U + 31 < sinks) && U + 31 < len;
+      if (!full) {
+        // (lane terms from the thread index here: kept, they would take registers from the whole walk)
+        const int tx = static_cast<int>(__builtin_amdgcn_workitem_id_x());
 #pragma unroll
-    for (int r = 0; r < RT; ++r) {
+        for (int e = 0; e < 16; ++e) {
+          const int u = U + 8 * (e >> 2) + 4 * ((tx >> 5) & 1) + (e & 3);
+          s[e] = sees(qw + (tx & 31), u, W, sinks) && u < len ? s[e] : -__builtin_inff();
+        }
+      }
+      float mx = fmaxf(s[0], s[1]), my = fmaxf(s[2], s[3]);
+#pragma unroll
+      for (int e = 4; e < 16; e += 2) {
+        mx = fmaxf(mx, s[e]);
+        my = fmaxf(my, s[e + 1]);
+      }
       float lo, hi;
-      halves(l[r], lo, hi);
-      const float lt = lo + hi;
-      const int t = qw + 32 * r + lrow;
-      const bool in = t < len;
-      const float inv = 1.0f / lt;
-      float worst = 0.0f;
+      halves(fmaxf(mx, my), lo, hi);
+      mx = fmaxf(fmaxf(lo, hi), x.floor);
+      // O and l are kept relative to a maximum that is raised only when a row's grows by more than 2^8:
+      // they share it, so the result does not change, and the rescale is rare
+      const bool raise = (mx - m) * c > 8.0f;
+      if (__any(raise)) {
+        const float mn = raise ? mx : m;
+        const float corr = __builtin_amdgcn_exp2f((m - mn) * c);
+        l *= corr;
+        m = mn;
+#pragma unroll
+        for (int j = 0; j < K::kDT; ++j) acc[j] *= corr;
+      }
+      const float mc = m * c;
+      if (__any(fabsf(mc) > kBigScore)) {
+#pragma unroll
+        for (int e = 0; e < 16; ++e) s[e] = (s[e] - m) * c;
+      } else {
+#pragma unroll
+        for (int e = 0; e < 16; ++e) s[e] = fmaf(s[e], c, -mc);
+      }
+      u32x4_t p[2], pl[2];  // P of two 16-key steps, hi (and lo)
+      float l0 = 0.0f, l1 = 0.0f;
+#pragma unroll
+      for (int e = 0; e < 16; e += 2) {
+        const float a = __builtin_amdgcn_exp2f(s[e]), bb = __builtin_amdgcn_exp2f(s[e + 1]);
+        l0 += a;
+        l1 += bb;
+        const uint32_t hw = pack_bf16x2(a, bb);
+        p[e >> 3][(e >> 1) & 3] = hw;
+        if constexpr (kSplit) pl[e >> 3][(e >> 1) & 3] = pack_bf16x2(a - bf16lo(hw), bb - bf16hi(hw));
+      }
+      l += l0 + l1;
+      // O^T += V^T P^T: step n is key step n / kDT, d tile n % kDT
+      {
+        auto v_of = [&](int n) { return K::cols(slot + K::kBytes + col_lane, n / K::kDT, n % K::kDT); };
+        bf16x8_t vt[kAhead + 1];
+#pragma unroll
+        for (int n = 0; n < kAhead; ++n) vt[n] = v_of(n);
+#pragma unroll
+        for (int n = 0; n < 2 * K::kDT; ++n) {
+          if (n + kAhead < 2 * K::kDT) vt[(n + kAhead) % (kAhead + 1)] = v_of(n + kAhead);
+          f32x16_t &o = acc[n % K::kDT];
+          o = __builtin_amdgcn_mfma_f32_32x32x16_bf16(
+              vt[n % (kAhead + 1)], __builtin_bit_cast(bf16x8_t, p[n / K::kDT]), o, 0, 0, 0);
+          if constexpr (kSplit)
+            o = __builtin_amdgcn_mfma_f32_32x32x16_bf16(
+                vt[n % (kAhead + 1)], __builtin_bit_cast(bf16x8_t, pl[n / K::kDT]), o, 0, 0, 0);
+          __builtin_amdgcn_sched_barrier(0);
+        }
+      }
+    }
+    __builtin_amdgcn_s_waitcnt(0x0F70);  // the zeros past the last block have landed too
+    // normalise and store; lane = row, accumulator e of tile j is d = 32 j + 8 (e / 4) + 4 half + e % 4
+    float lo, hi;
+    halves(l, lo, hi);
+    const float lt = lo + hi;
+    const bool in = qr < len;
+    const float inv = 1.0f / lt;
+    float worst = 0.0f;
+#pragma unroll
+    for (int j = 0; j < K::kDT; ++j)
+#pragma unroll
+      for (int e = 0; e < 16; ++e) {
+        acc[j][e] = in ? acc[j][e] * inv : 0.0f;
+        worst = fmaf(0.0f, acc[j][e], worst);  // NaN if any is not finite
+      }
+    if (qr < T) {
+      bf16_t *op = o_ + static_cast<size_t>(qr) * ostride + 4 * half;
 #pragma unroll
       for (int j = 0; j < K::kDT; ++j)
 #pragma unroll
-        for (int e = 0; e < 16; ++e) {
-          acc[r][j][e] = in ? acc[r][j][e] * inv : 0.0f;
-          worst = fmaf(0.0f, acc[r][j][e], worst);  // NaN if any is not finite
-        }
-      if (t < T) {
-        bf16_t *op = o_ + static_cast<size_t>(t) * ostride + 4 * half;
-#pragma unroll
-        for (int j = 0; j < K::kDT; ++j)
-#pragma unroll
-          for (int g = 0; g < 4; ++g)
-            *reinterpret_cast<uint2 *>(op + 32 * j + 8 * g) =
-                make_uint2(pack_bf16x2(acc[r][j][4 * g], acc[r][j][4 * g + 1]),
-                           pack_bf16x2(acc[r][j][4 * g + 2], acc[r][j][4 * g + 3]));
-        // ln of the denominator sum_u exp(scale s_u) = scale m + ln l
-        if (lse_ && half == 0)
-          lse_[t] = in ? (m[r] * c + __builtin_amdgcn_logf(lt)) * 0.6931471805599453f : -__builtin_inff();
-      }
-      const unsigned long long rows = __ballot(in && !(worst == 0.0f) && lt < __builtin_inff());
-      odd[r] = static_cast<unsigned>(rows | (rows >> 32));
+        for (int g = 0; g < 4; ++g)
+          *reinterpret_cast<uint2 *>(op + 32 * j + 8 * g) =
+              make_uint2(pack_bf16x2(acc[j][4 * g], acc[j][4 * g + 1]),
+                         pack_bf16x2(acc[j][4 * g + 2], acc[j][4 * g + 3]));
+      // ln of the denominator sum_u exp(scale s_u) = scale m + ln l
+      if (lse_ && half == 0)
+        lse_[qr] = in ? (m * c + __builtin_amdgcn_logf(lt)) * 0.6931471805599453f : -__builtin_inff();
     }
+    const unsigned long long rows = __ballot(in && !(worst == 0.0f) && lt < __builtin_inff());
+    odd = static_cast<unsigned>(rows | (rows >> 32));
   };
   if (min(q0 + 1, W) < kSplitKeys)
     run(std::true_type{});
   else
     run(std::false_type{});
   // rows with finite scores and a non-finite o: again, key by key
-#pragma unroll
-  for (int r = 0; r < RT; ++r)
-    while (odd[r]) {
-      const int t = qw + 32 * r + __builtin_ctz(odd[r]);
-      odd[r] &= odd[r] - 1;
-      exact_row<DH>(q_ + static_cast<size_t>(t) * x.q_stride, k_, v_, o_ + static_cast<size_t>(t) * ostride,
-                    x, c, t, lane);
-    }
+  while (odd) {
+    const int t = qw + __builtin_ctz(odd);
+    odd &= odd - 1;
+    exact_row<DH>(q_ + static_cast<size_t>(t) * x.q_stride, k_, v_, o_ + static_cast<size_t>(t) * ostride, x, c,
+                  t, lane);
+  }
 }
 
 namespace {
 
-template <int DH, int RT> hipError_t launch(const AttnArgs &a, hipStream_t s) {
-  const unsigned nq = static_cast<unsigned>((a.T + 32 * RT * kWg - 1) / (32 * RT * kWg));
-  attn_fwd<DH, RT><<<nq * a.B * a.Hq, 64 * kWg, 0, s>>>(a);
+template <int DH> hipError_t launch(const AttnArgs &a, hipStream_t s) {
+  const unsigned nq = static_cast<unsigned>((a.T + kOwn - 1) / kOwn);
+  attn_fwd<DH><<<nq * a.B * a.Hq, 64 * kWg, 0, s>>>(a);
   return hipGetLastError();
 }
 
@@ -309,9 +299,9 @@ hipError_t launch_local_attention(const AttnArgs &args, hipStream_t s) {
   a.window = std::min(a.window, a.T);
   a.sinks = std::min(a.sinks, a.T);
   switch (a.dh) {
-    case 64: return launch<64, 1>(a, s);
-    case 128: return launch<128, 1>(a, s);
-    case 256: return launch<256, 1>(a, s);
+    case 64: return launch<64>(a, s);
+    case 128: return launch<128>(a, s);
+    case 256: return launch<256>(a, s);
   }
   return hipErrorInvalidValue;
 }

@@ -108,18 +108,20 @@ __global__ __launch_bounds__(64 * kWg, DH == 256 ? 1 : 2) void attn_dq(AttnBwdAr
   auto first_row = [&](int i) { return (i < ns ? i : i - ns + win) * kBlk; };
   // the loads of block i (past the last one: zeros, without touching memory, so that every step
   // issues the same number)
+  const typename K::Lane kl = K::load_lane(w, lane, krb), vl = K::load_lane(w, lane, vrb);
   struct Src {
-    __amdgpu_buffer_rsrc_t k, v;
+    const bf16_t *k, *v;
+    int rows;
   };
   auto src_of = [&](int i) {
-    const int u0 = first_row(min(i, n - 1)), rows = i < n ? len - u0 : 0;
-    return Src{K::rsrc(kb_ + static_cast<size_t>(u0) * a.k_stride, krb, rows),
-               K::rsrc(vb_ + static_cast<size_t>(u0) * a.v_stride, vrb, rows)};
+    const int u0 = first_row(min(i, n - 1));
+    return Src{kb_ + static_cast<size_t>(u0) * a.k_stride, vb_ + static_cast<size_t>(u0) * a.v_stride,
+               i < n ? len - u0 : 0};
   };
   auto load_part = [&](const Src &src, int i, int ii) {
     const unsigned dst = slot_of(i);
-    K::load(src.k, krb, ii, w, lane, dst);
-    K::load(src.v, vrb, ii, w, lane, dst + K::kBytes);
+    K::load(src.k, krb, src.rows, ii, w, kl, dst);
+    K::load(src.v, vrb, src.rows, ii, w, vl, dst + K::kBytes);
   };
   auto load_block = [&](int i) {
     const Src src = src_of(i);
@@ -305,30 +307,28 @@ __device__ __forceinline__ void dkv_side(const AttnBwdArgs &a, DkvLds<DH> &sh, i
   // side 0 brings the Q rows, side 1 the dO rows, and every wave the rows' stat
   const unsigned rb = SIDE ? static_cast<unsigned>(Hq) * DH * 2 : static_cast<unsigned>(a.q_stride) * 2;
   const bf16_t *const rows_ = static_cast<const bf16_t *>(SIDE ? a.do_ : a.q) + tok * (rb / 2);
+  const typename K::Lane ll = K::load_lane(kt, lane, rb);
   auto load_item = [&](At at, int sl) {
     const int q0 = (qfirst + at.qb) * kBlk, h = kvh * a.group + at.hh;
-    const __amdgpu_buffer_rsrc_t src =
-        K::rsrc(rows_ + static_cast<size_t>(q0) * (rb / 2) + static_cast<size_t>(h) * DH, rb, len - q0);
     const __amdgpu_buffer_rsrc_t st = __builtin_amdgcn_make_buffer_rsrc(
         wave_uniform(a.stat + (static_cast<size_t>(b) * Hq + h) * T + q0), static_cast<short>(0),
         uni(min(len - q0, kBlk) * 8), kRawWord3);
 #pragma unroll
     for (int ii = 0; ii < K::kLPW; ++ii)
-      K::load(src, rb, ii, kt, lane, lds + sl * K::kSlot + (SIDE ? K::kBytes : 0u));
+      K::load(rows_ + static_cast<size_t>(q0) * (rb / 2) + static_cast<size_t>(h) * DH, rb, len - q0, ii, kt, ll,
+              lds + sl * K::kSlot + (SIDE ? K::kBytes : 0u));
     dma_4b(st, lane * 4, lds_addr(sh.rowv[sl]));
   };
   const unsigned row_lane = K::row_lane(lane) + (SIDE ? K::kBytes : 0u);  // side 0 reads Q, 1 dO
   const unsigned col_lane = K::col_lane(lane) + (SIDE ? 0u : K::kBytes);  // side 0 reads dO, 1 Q
-  auto products = [&](int sl, const u32x4_t (&pd)[2]) {
-    const unsigned pt = lds + sl * K::kSlot + col_lane;
-#pragma unroll
-    for (int st = 0; st < 2; ++st)
-#pragma unroll
-      for (int j = 0; j < K::kDT; ++j)
-        acc[j] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(
-            K::cols(pt, st, j), __builtin_bit_cast(bf16x8_t, pd[st]), acc[j], 0, 0, 0);
-  };
   u32x4_t pd[2] = {};         // P (side 0) or dS (side 1) of the last item
+  // step i of the product into acc (row step i / kDT, d tile i % kDT; as many as S has k-steps)
+  static_assert(2 * K::kDT == K::kKS, "one product step per k-step");
+  auto product = [&](int sl, int i) {
+    const int st = i / K::kDT, j = i % K::kDT;
+    acc[j] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(K::cols(lds + sl * K::kSlot + col_lane, st, j),
+                                                     __builtin_bit_cast(bf16x8_t, pd[st]), acc[j], 0, 0, 0);
+  };
   f32x16_t dpl = f32x16_t{};  // side 1: dP of the last item
   // side 1: dS of the last item (first row Ql) from its P, dP and delta
   auto make_ds = [&](int buf, int sl, int Ql) {
@@ -360,13 +360,16 @@ __device__ __forceinline__ void dkv_side(const AttnBwdArgs &a, DkvLds<DH> &sh, i
       if (i + 1 < i1) load_item(head, sln);
       const int Q = (qfirst + cur.qb) * kBlk;
       next(cur);
+      if constexpr (SIDE == 1)
+        if (i > i0) make_ds((i - 1) & 1, slp, Ql);
       f32x16_t s = f32x16_t{};
       const unsigned at = lds + sl * K::kSlot + row_lane;
 #pragma unroll
-      for (int d = 0; d < K::kKS; ++d)
+      for (int d = 0; d < K::kKS; ++d) {
         s = __builtin_amdgcn_mfma_f32_32x32x16_bf16(K::rows(at, d), kf[d], s, 0, 0, 0);
+        product(slp, d);  // between the steps of S, which wait for each other
+      }
       if constexpr (SIDE == 0) {
-        products(slp, pd);
         const bool full = kw + 31 <= Q && (kw > Q + 31 - W || kw + 31 < sinks);
         if (!full) {
 #pragma unroll
@@ -388,8 +391,6 @@ __device__ __forceinline__ void dkv_side(const AttnBwdArgs &a, DkvLds<DH> &sh, i
           pd[e4 >> 1][2 * (e4 & 1) + 1] = pack_bf16x2(p[2], p[3]);
         }
       } else {
-        if (i > i0) make_ds((i - 1) & 1, slp, Ql);
-        products(slp, pd);
         dpl = s;
       }
       Ql = Q;
@@ -398,7 +399,8 @@ __device__ __forceinline__ void dkv_side(const AttnBwdArgs &a, DkvLds<DH> &sh, i
     }
     lds_barrier();  // P of the last item
     if constexpr (SIDE == 1) make_ds((i1 - 1) & 1, slp, Ql);
-    products(slp, pd);
+#pragma unroll
+    for (int d = 0; d < K::kKS; ++d) product(slp, d);
   }
   // lane = key kr; accumulator e of tile j is d = 32 j + 8 (e / 4) + 4 half + e % 4
   if (S > 1) {

@@ -20,6 +20,11 @@ if not os.path.exists(LIB_PATH):
     raise ImportError(f"{LIB_PATH} is not built; run gated_linear_recurrence_conv1d_amd/build.py "
                       "(or __graft_entry__.build())")
 _lib = ctypes.CDLL(LIB_PATH)
+try:
+    from . import _rglru_torch as _ext  # checks and calls of the attention block's operators
+except ImportError as e:
+    raise ImportError("_rglru_torch.so is not built; run gated_linear_recurrence_conv1d_amd/build.py "
+                      "(or __graft_entry__.build())") from e
 
 RGLRU_OK = 0
 RGLRU_ERR_INVALID_ARG = 1
@@ -391,99 +396,32 @@ _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (
     lambda index: torch.cuda.current_stream(index).cuda_stream)
 
 
-class _Call:
-    """The device, type and stream of one call; checks tensors against them. The checks of tensors
-    that fit take a few attribute reads each: with calls of a few microseconds on the GPU, the
-    host's share is what counts."""
-
-    __slots__ = ("index", "io", "stream")
-
-    def __init__(self, t, name, stream):
-        if not isinstance(t, torch.Tensor):
-            raise TypeError(f"{name}: expected a torch.Tensor")
-        if isinstance(stream, torch.cuda.Stream) and stream.device != t.device:
-            raise ValueError(f"stream: on {stream.device}, {name} on {t.device}")
-        self.index, self.io, self.stream = t.get_device(), t.dtype, stream
-
-    def flat(self, t, dtype, shape, name):
-        """Pointer of a contiguous tensor of this type and shape (None: any); None for None."""
-        if t is None:
-            return None
-        if (isinstance(t, torch.Tensor) and (dtype is None or t.dtype is dtype) and
-                (shape is None or t.shape == shape) and t.get_device() == self.index >= 0 and
-                t.is_contiguous()):
-            return t.data_ptr()
-        if shape is not None and isinstance(t, torch.Tensor):
-            _shape(t, shape, name)
-        p = _ptr(t, dtype, name)
-        if t.get_device() != self.index:
-            raise ValueError(f"{name}: on device {t.get_device()}, expected {self.index}")
-        return p
-
-    def heads(self, t, shape, name):
-        """(pointer, elements from token to token) of a tensor of this shape, (..., H, dh); (None, 0)
-        for None."""
-        if t is None:
-            return None, 0
-        H, dh = shape[-2:]
-        if (isinstance(t, torch.Tensor) and t.dtype is self.io and t.shape == shape and
-                t.get_device() == self.index >= 0):
-            if t.is_contiguous():
-                return t.data_ptr(), H * dh
-            st = t.stride()  # part of the columns of one tensor
-            if (st[-1] == 1 and st[-2] == dh and st[-3] >= H * dh and
-                    (len(shape) == 3 or len(shape) == 4 and st[0] == st[1] * shape[1])):
-                return t.data_ptr(), st[-3]
-        if not isinstance(t, torch.Tensor):
-            raise TypeError(f"{name}: expected a torch.Tensor")
-        _shape(t, shape, name)
-        if t.dtype != self.io:
-            raise ValueError(f"{name}: expected {self.io}, got {t.dtype}")
-        if not t.is_cuda or t.get_device() != self.index:
-            raise ValueError(f"{name}: must be a device tensor on device {self.index}, is on {t.device}")
-        st = t.stride()
-        if (dh > 1 and st[-1] != 1) or (H > 1 and st[-2] != dh):
-            raise ValueError(f"{name}: the heads of a token must be contiguous")
-        step, reach = H * dh, None  # the innermost leading dimension longer than 1 gives the stride
-        for n, d in zip(shape[-3::-1], st[-3::-1]):
-            if n == 1:
-                continue
-            if reach is None:
-                step = d
-            elif d != reach:
-                raise ValueError(f"{name}: tokens must be one stride apart")
-            reach = d * n
-        if step < H * dh:
-            raise ValueError(f"{name}: tokens overlap")
-        return t.data_ptr(), step
-
-    def run(self, where, fn, *args, keep=()):
-        """fn(*args, stream) on the call's device; `keep`: tensors allocated for it here."""
-        s = self.stream
-        if s is None:
-            s = _raw_stream(self.index)
+def _call(where, fn, q, stream, keep, *args):
+    """fn(*args, stream), which checks its tensors (csrc/rglru_torch.cpp), on q's device; `keep`: tensors
+    allocated for it here."""
+    if not isinstance(q, torch.Tensor):
+        raise TypeError("q: expected a torch.Tensor")
+    index = q.get_device()
+    if index < 0:
+        status = fn(*args, 0)  # refused there, by what is wrong with the tensors
+    else:
+        if stream is None:
+            s = _raw_stream(index)
         else:
-            if not isinstance(s, torch.cuda.Stream):
-                s = torch.cuda.ExternalStream(int(s), device=self.index)
+            if not isinstance(stream, torch.cuda.Stream):
+                stream = torch.cuda.ExternalStream(int(stream), device=index)
+            elif stream.device_index != index:
+                raise ValueError(f"stream: on {stream.device}, q on {q.device}")
             for t in keep:  # from the current stream's pool: not reused before this stream is done
-                t.record_stream(s)
-            s = s.cuda_stream
-        if self.index == torch.cuda.current_device():
+                t.record_stream(stream)
+            s = stream.cuda_stream
+        if index == torch.cuda.current_device():
             status = fn(*args, s)
         else:
-            with torch.cuda.device(self.index):
+            with torch.cuda.device(index):
                 status = fn(*args, s)
-        if status != RGLRU_OK:
-            raise RglruError(status, where)
-
-
-def _heads_of(t, name):
-    if not isinstance(t, torch.Tensor):
-        raise TypeError(f"{name}: expected a torch.Tensor")
-    if t.dim() < 3:
-        raise ValueError(f"{name}: expected [..., heads, dh], got shape {tuple(t.shape)}")
-    shape = tuple(t.shape)
-    return shape, shape[:-2], shape[-2], shape[-1]
+    if status != RGLRU_OK:
+        raise RglruError(status, where)
 
 
 def _int32(n):
@@ -491,45 +429,12 @@ def _int32(n):
     return n if n < 0x7FFFFFFF else 0x7FFFFFFF
 
 
-def _bytes(t):
-    return 0 if t is None else t.numel() * t.element_size()
-
-
 def rglru_qk_norm_rope(q, k, positions, inv_freq, q_out, k_out, q_w=None, k_w=None, eps=1e-6,
                        v=None, k_pages=None, v_pages=None, slots=None, stream=None, _keep=()):
     """q [..., Hq, dh], k, v [..., Hkv, dh]; positions int32 and slots int64 [...]; inv_freq f32
     [rot / 2]; k_pages, v_pages [pages, page, Hkv, dh]. k_out may be None with slots."""
-    c = _Call(q, "q", stream)
-    qshape, lead, Hq, dh = _heads_of(q, "q")
-    Hkv = _heads_of(k, "k")[2]
-    kshape = lead + (Hkv, dh)
-    f32 = torch.float32
-    rows = positions.numel()
-    rot = 0 if inv_freq is None else 2 * inv_freq.numel()
-    qp, qs = c.heads(q, qshape, "q")
-    kp, ks = c.heads(k, kshape, "k")
-    qop, qos = c.heads(q_out, qshape, "q_out")
-    kop, kos = c.heads(k_out, kshape, "k_out")
-    n_slots = vs = 0
-    vp = kpp = vpp = sp = None
-    if slots is not None:
-        if k_pages is None or v_pages is None or v is None:
-            raise ValueError("slots: needs v, k_pages and v_pages")
-        if k_pages.dim() != 4:
-            raise ValueError(f"k_pages: expected [pages, page, Hkv, dh], got {tuple(k_pages.shape)}")
-        pool = (k_pages.shape[0], k_pages.shape[1], Hkv, dh)
-        n_slots = pool[0] * pool[1]
-        vp, vs = c.heads(v, kshape, "v")
-        kpp = c.flat(k_pages, c.io, pool, "k_pages")
-        vpp = c.flat(v_pages, c.io, pool, "v_pages")
-        sp = c.flat(slots, torch.int64, lead, "slots")
-    elif k_pages is not None or v_pages is not None:
-        raise ValueError("k_pages, v_pages: need slots")
-    c.run("rglru_qk_norm_rope", _lib.rglru_qk_norm_rope, qp, kp, vp,
-          c.flat(q_w, f32, (dh,), "q_w"), c.flat(k_w, f32, (dh,), "k_w"),
-          c.flat(inv_freq, f32, (rot // 2,), "inv_freq"),
-          c.flat(positions, torch.int32, lead, "positions"), sp, qop, kop, kpp, vpp, rows, Hq, Hkv,
-          dh, rot, qs, ks, vs, qos, kos, n_slots, eps, _dt(c.io), keep=_keep)
+    _call("rglru_qk_norm_rope", _ext.qk_norm_rope, q, stream, _keep, q, k, v, q_w, k_w, inv_freq,
+          positions, slots, q_out, k_out, k_pages, v_pages, eps)
 
 
 def qk_norm_rope(q, k, positions, inv_freq, q_w=None, k_w=None, eps=1e-6, v=None, k_pages=None,
@@ -554,27 +459,8 @@ def rglru_qk_norm_rope_backward_workspace_size(rows, dh) -> int:
 def rglru_qk_norm_rope_backward(q, k, positions, inv_freq, dq_out, dk_out, dq, dk, q_w=None,
                                 k_w=None, dq_w=None, dk_w=None, eps=1e-6, workspace=None,
                                 stream=None, _keep=()):
-    c = _Call(q, "q", stream)
-    qshape, lead, Hq, dh = _heads_of(q, "q")
-    Hkv = _heads_of(k, "k")[2]
-    kshape = lead + (Hkv, dh)
-    f32 = torch.float32
-    rot = 0 if inv_freq is None else 2 * inv_freq.numel()
-    ptrs, strides = [], []
-    for t, shape, name in ((q, qshape, "q"), (k, kshape, "k"), (dq_out, qshape, "dq_out"),
-                           (dk_out, kshape, "dk_out"), (dq, qshape, "dq"), (dk, kshape, "dk")):
-        p, st = c.heads(t, shape, name)
-        ptrs.append(p)
-        strides.append(st)
-    wsb = _bytes(workspace)
-    c.run("rglru_qk_norm_rope_backward", _lib.rglru_qk_norm_rope_backward, ptrs[0], ptrs[1],
-          c.flat(q_w, f32, (dh,), "q_w"), c.flat(k_w, f32, (dh,), "k_w"),
-          c.flat(inv_freq, f32, (rot // 2,), "inv_freq"),
-          c.flat(positions, torch.int32, lead, "positions"), *ptrs[2:],
-          c.flat(dq_w, f32, (dh,), "dq_w"), c.flat(dk_w, f32, (dh,), "dk_w"), positions.numel(), Hq,
-          Hkv, dh, rot, *strides, eps, _dt(c.io),
-          c.flat(workspace, None, None, "workspace"), wsb,
-          keep=_keep)
+    _call("rglru_qk_norm_rope_backward", _ext.qk_norm_rope_backward, q, stream, _keep, q, k, q_w, k_w,
+          inv_freq, positions, dq_out, dk_out, dq, dk, dq_w, dk_w, eps, workspace)
 
 
 def qk_norm_rope_backward(q, k, positions, inv_freq, dq_out, dk_out, q_w=None, k_w=None, eps=1e-6,
@@ -605,21 +491,8 @@ def rglru_local_attention(q, k, v, o, window, sinks=0, lens=None, scale=0.0, lse
                           _keep=()):
     """q [B,T,Hq,dh], k, v [B,T,Hkv,dh], o as q and contiguous, bf16; lens int32 [B]; lse f32
     [B,Hq,T]."""
-    c = _Call(q, "q", stream)
-    qshape, lead, Hq, dh = _heads_of(q, "q")
-    if len(lead) != 2:
-        raise ValueError(f"q: expected [B, T, Hq, dh], got shape {qshape}")
-    B, T = lead
-    Hkv = _heads_of(k, "k")[2]
-    kshape = (B, T, Hkv, dh)
-    qp, qs = c.heads(q, qshape, "q")
-    kp, ks = c.heads(k, kshape, "k")
-    vp, vs = c.heads(v, kshape, "v")
-    c.run("rglru_local_attention", _lib.rglru_local_attention, qp, kp, vp,
-          c.flat(lens, torch.int32, (B,), "lens"), c.flat(o, c.io, qshape, "o"),
-          c.flat(lse, torch.float32, (B, Hq, T), "lse"), B, T, Hq, Hkv, dh, qs, ks, vs,
-          _int32(window), _int32(sinks), float(scale), _dt(c.io),
-          keep=_keep)
+    _call("rglru_local_attention", _ext.local_attention, q, stream, _keep, q, k, v, lens, o, lse,
+          window, sinks, scale)
 
 
 def local_attention(q, k, v, window, sinks=0, lens=None, scale=0.0, want_lse=False, stream=None):
@@ -641,23 +514,8 @@ def rglru_local_attention_backward_workspace_size(B, T, Hq, Hkv, dh, window, sin
 def rglru_local_attention_backward(q, k, v, o, lse, do, dq, dk, dv, window, sinks=0, lens=None,
                                    scale=0.0, workspace=None, stream=None, _keep=()):
     """o, do as q and contiguous; dq as q, dk and dv as k (slices of a packed gradient are fine)."""
-    c = _Call(q, "q", stream)
-    qshape, lead, Hq, dh = _heads_of(q, "q")
-    if len(lead) != 2:
-        raise ValueError(f"q: expected [B, T, Hq, dh], got shape {qshape}")
-    B, T = lead
-    Hkv = _heads_of(k, "k")[2]
-    kshape = (B, T, Hkv, dh)
-    (qp, qs), (dqp, dqs) = c.heads(q, qshape, "q"), c.heads(dq, qshape, "dq")
-    (kp, ks), (vp, vs), (dkp, dks), (dvp, dvs) = (
-        c.heads(t, kshape, n) for t, n in ((k, "k"), (v, "v"), (dk, "dk"), (dv, "dv")))
-    c.run("rglru_local_attention_backward", _lib.rglru_local_attention_backward, qp, kp, vp,
-          c.flat(lens, torch.int32, (B,), "lens"), c.flat(o, c.io, qshape, "o"),
-          c.flat(lse, torch.float32, (B, Hq, T), "lse"), c.flat(do, c.io, qshape, "do"), dqp, dkp, dvp,
-          B, T, Hq, Hkv, dh, qs, ks, vs, dqs, dks, dvs, _int32(window),
-          _int32(sinks), float(scale), _dt(c.io),
-          c.flat(workspace, None, None, "workspace"),
-          _bytes(workspace), keep=_keep)
+    _call("rglru_local_attention_backward", _ext.local_attention_backward, q, stream, _keep, q, k, v,
+          lens, o, lse, do, dq, dk, dv, window, sinks, scale, workspace)
 
 
 def local_attention_backward(q, k, v, o, lse, do, window, sinks=0, lens=None, scale=0.0, dq=None,
@@ -694,23 +552,8 @@ def rglru_paged_attention(q, k_pages, v_pages, block_table, lens, o, window, sin
                           workspace=None, stream=None, _keep=()):
     """q [N,Hq,dh], k_pages, v_pages [pages,page,Hkv,dh] of one type (bf16 or f32); block_table
     int32 [N,max_pages], lens int32 [N]; o as q and contiguous."""
-    c = _Call(q, "q", stream)
-    qshape, lead, Hq, dh = _heads_of(q, "q")
-    if len(lead) != 1:
-        raise ValueError(f"q: expected [N, Hq, dh], got shape {qshape}")
-    if k_pages.dim() != 4 or block_table.dim() != 2:
-        raise ValueError("k_pages: expected [pages, page, Hkv, dh]; block_table: [N, max_pages]")
-    pages, page, Hkv, _ = k_pages.shape
-    N, pool = lead[0], (pages, page, Hkv, dh)
-    qp, qs = c.heads(q, qshape, "q")
-    c.run("rglru_paged_attention", _lib.rglru_paged_attention, qp,
-          c.flat(k_pages, c.io, pool, "k_pages"), c.flat(v_pages, c.io, pool, "v_pages"),
-          c.flat(block_table, torch.int32, (N, block_table.shape[1]), "block_table"),
-          c.flat(lens, torch.int32, (N,), "lens"), c.flat(o, c.io, qshape, "o"), N, Hq, Hkv, dh,
-          qs, pages, page, block_table.shape[1], _int32(window),
-          _int32(sinks), float(scale), _dt(c.io),
-          c.flat(workspace, None, None, "workspace"),
-          _bytes(workspace), keep=_keep)
+    _call("rglru_paged_attention", _ext.paged_attention, q, stream, _keep, q, k_pages, v_pages,
+          block_table, lens, o, window, sinks, scale, workspace)
 
 
 def paged_attention(q, k_pages, v_pages, block_table, lens, window, sinks=0, scale=0.0,
@@ -718,9 +561,10 @@ def paged_attention(q, k_pages, v_pages, block_table, lens, window, sinks=0, sca
     """Returns o [N,Hq,dh] of q's type."""
     new = [torch.empty_like(q, memory_format=torch.contiguous_format)]
     if workspace is None and q.dim() == 3 and k_pages.dim() == 4 and block_table.dim() == 2:
-        n = rglru_paged_attention_workspace_size(q.shape[0], q.shape[1], k_pages.shape[2],
-                                                 q.shape[2], k_pages.shape[1],
-                                                 block_table.shape[1], window, sinks, q.dtype)
+        N, Hq, dh = q.shape
+        _, page, Hkv, _ = k_pages.shape
+        n = rglru_paged_attention_workspace_size(N, Hq, Hkv, dh, page, block_table.shape[1], window,
+                                                 sinks, q.dtype)
         if n:
             workspace = torch.empty(n, dtype=torch.uint8, device=q.device)
             new.append(workspace)

@@ -239,3 +239,38 @@ def test_binding_refuses_what_does_not_fit():
     with pytest.raises(ValueError, match="block_table"):
         rg.rglru_paged_attention(f(3, 4, 64), f(9, 16, 2, 64), f(9, 16, 2, 64), f(2, 4, dtype=torch.int32),
                                  f(3, dtype=torch.int32), f(3, 4, 64), 10)
+
+
+def test_binding_refuses_by_argument():
+    """Host tensors whose first fault is not their device: each message names its tensor."""
+    bf, i32 = torch.bfloat16, torch.int32
+    q, k = torch.zeros(2, 5, 4, 64, dtype=bf), torch.zeros(2, 5, 2, 64, dtype=bf)
+    pos, freq = torch.zeros(2, 5, dtype=i32), torch.zeros(16)
+    with pytest.raises(ValueError, match="q: unsupported dtype torch.float64"):
+        rg.rglru_qk_norm_rope(q.double(), k, pos, freq, q, k)
+    with pytest.raises(ValueError, match="q: expected .*heads"):
+        rg.rglru_qk_norm_rope(q[0, 0], k, pos, freq, q, k)
+    with pytest.raises(TypeError, match="k: expected a torch.Tensor"):
+        rg.rglru_qk_norm_rope(q, [1], pos, freq, q, k)
+    with pytest.raises(TypeError, match="lens: expected a torch.Tensor"):
+        rg.rglru_local_attention(q, k, k, q, 4, lens=[1, 2])
+    with pytest.raises(ValueError, match=r"q_w: expected shape \(64,\), got \(32,\)"):
+        rg.rglru_qk_norm_rope(q, k, pos, freq, q, k, q_w=torch.zeros(32), k_w=torch.zeros(64))
+    with pytest.raises(ValueError, match="inv_freq: expected torch.float32"):
+        rg.rglru_qk_norm_rope(q, k, pos, freq.double(), q, k)
+    with pytest.raises(ValueError, match="slots: expected torch.int64"):
+        rg.rglru_qk_norm_rope(q, k, pos, freq, q, k, v=k, k_pages=torch.zeros(2, 4, 2, 64, dtype=bf),
+                              v_pages=torch.zeros(2, 4, 2, 64, dtype=bf), slots=pos)
+    with pytest.raises(ValueError, match="workspace: must be contiguous"):
+        rg.rglru_local_attention_backward(q, k, k, q, torch.zeros(2, 4, 5), q, q, k, k, 4,
+                                          workspace=torch.zeros(4, 8)[:, ::2])
+    with pytest.raises(ValueError, match="q: expected .*N, Hq, dh"):
+        rg.rglru_paged_attention(q, torch.zeros(9, 16, 2, 64, dtype=bf), torch.zeros(9, 16, 2, 64, dtype=bf),
+                                 torch.zeros(3, 4, dtype=i32), torch.zeros(3, dtype=i32), q, 10)
+    with pytest.raises(TypeError):
+        rg.rglru_local_attention(q, k, k, q, "4")
+    with pytest.raises(TypeError):
+        rg.rglru_local_attention(q, k, k, q, 4, scale="a")
+    # a window that no integer of the entry point holds is the widest one; here the device is what is wrong
+    with pytest.raises(ValueError, match="device"):
+        rg.rglru_local_attention(q, k, k, q, 1 << 70)

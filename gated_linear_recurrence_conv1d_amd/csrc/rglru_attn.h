@@ -17,6 +17,8 @@ constexpr float kLn2Inv = 1.4426950408889634f;
 typedef short i16x4_t __attribute__((ext_vector_type(4)));
 typedef __attribute__((address_space(3))) i16x4_t lds_i16x4_t;
 typedef __attribute__((address_space(3))) u32x4_t lds_u32x4_t;
+typedef unsigned u32x2_t __attribute__((ext_vector_type(2)));
+typedef __attribute__((address_space(3))) u32x2_t lds_u32x2_t;
 typedef float f32x4_t __attribute__((ext_vector_type(4)));
 
 constexpr int kWg = 4;         // waves per workgroup
@@ -26,6 +28,11 @@ constexpr int kBlk = 32;       // rows per LDS block
 // An integer that is the same in every lane, kept in a scalar register (quotients and some minima run on
 // the vector unit; branches on such values, and descriptors made from them, then cost registers).
 __device__ __forceinline__ int uni(int v) { return __builtin_amdgcn_readfirstlane(v); }
+__device__ __forceinline__ long long uni64(long long v) {
+  const unsigned lo = __builtin_amdgcn_readfirstlane(static_cast<unsigned>(v));
+  const unsigned hi = __builtin_amdgcn_readfirstlane(static_cast<unsigned>(static_cast<unsigned long long>(v) >> 32));
+  return static_cast<long long>(static_cast<unsigned long long>(hi) << 32 | lo);
+}
 
 // A block of kBlk rows of DH bf16 in LDS, and the ways it is filled and read.
 template <int DH, int WAVES = kWg> struct Blk {  // WAVES: how many share the loads
@@ -101,6 +108,53 @@ template <int DH, int WAVES = kWg> struct Blk {  // WAVES: how many share the lo
     const uint2 ux = __builtin_bit_cast(uint2, x), uy = __builtin_bit_cast(uint2, y);
     const u32x4_t u = {ux.x, ux.y, uy.x, uy.y};
     return __builtin_bit_cast(bf16x8_t, u);
+  }
+};
+
+// A wave's 32 rows of DH bf16, one row per lane pair (l, l + 32), on their way to and from registers. Lane
+// by lane, each access would touch 32 rows 16 bytes at a time; through a block of LDS that is the wave's own
+// (`tile`), whole rows are read and written.
+template <int DH> struct Tile {
+  typedef Blk<DH, 1> K;
+  static constexpr int kPasses = K::kKS;  // wave-wide 16-byte accesses of 32 rows
+  // the lane's row and chunk in pass p, and their place in the tile
+  __device__ __forceinline__ static int row(int p, int lane) { return p * K::kRPI + lane / K::kCPR; }
+  __device__ __forceinline__ static unsigned at(unsigned tile, int p, int lane) {
+    const int r = row(p, lane);
+    return tile + r * K::kRowBytes + (((lane % K::kCPR) ^ K::swz(r)) * 16);
+  }
+  // starts the loads of the rows of the sequence from `base` on (rows >= `rows`: zero)
+  __device__ __forceinline__ static void start(const bf16_t *base, unsigned row_bytes, int rows, int lane,
+                                               unsigned tile) {
+    asm volatile("" : "+v"(lane));  // (as in store)
+    const typename K::Lane l = K::load_lane(0, lane, row_bytes);
+#pragma unroll
+    for (int ii = 0; ii < K::kLPW; ++ii) K::load(base, row_bytes, rows, ii, 0, l, tile);
+  }
+  __device__ __forceinline__ static void landed() { asm volatile("s_waitcnt vmcnt(0)" ::: "memory"); }
+  // this lane's row as a B operand, k-step s: its values 16 s + 8 (lane / 32) ..
+  __device__ __forceinline__ static bf16x8_t operand(unsigned tile, int lane, int s) {
+    return K::rows(tile + K::row_lane(lane), s);
+  }
+  // stores an accumulator of DH / 32 tiles (value(j, g): its elements 4 g .. 4 g + 3 of tile j, which are
+  // d = 32 j + 8 g + 4 (lane / 32) .., as bf16) to the rows below `rows`
+  template <typename F>
+  __device__ __forceinline__ static void store(unsigned tile, int lane, F value, bf16_t *base, size_t stride,
+                                               int rows) {
+    asm volatile("" : "+v"(lane));  // the lane's terms are formed here: kept from the start, they take registers
+    const int r = lane & 31, half = lane >> 5;
+#pragma unroll
+    for (int j = 0; j < K::kDT; ++j)
+#pragma unroll
+      for (int g = 0; g < 4; ++g)
+        *(lds_u32x2_t *)static_cast<uintptr_t>(tile + r * K::kRowBytes + (((4 * j + g) ^ K::swz(r)) * 16) +
+                                               8 * half) = value(j, g);
+    asm volatile("" ::: "memory");
+#pragma unroll
+    for (int p = 0; p < kPasses; ++p)
+      if (row(p, lane) < rows)
+        *reinterpret_cast<u32x4_t *>(base + row(p, lane) * stride + 8 * (lane % K::kCPR)) =
+            *(lds_u32x4_t *)static_cast<uintptr_t>(at(tile, p, lane));
   }
 };
 

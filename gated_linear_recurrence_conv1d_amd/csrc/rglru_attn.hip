@@ -107,14 +107,13 @@ __global__ __launch_bounds__(64 * kWg, 2) void attn_fwd(AttnArgs x) {
   const bf16_t *const k_ = static_cast<const bf16_t *>(x.k) + tok * x.k_stride + static_cast<size_t>(kvh) * DH;
   const bf16_t *const v_ = static_cast<const bf16_t *>(x.v) + tok * x.v_stride + static_cast<size_t>(kvh) * DH;
   bf16x8_t qf[K::kKS];
-  {
-    const bf16_t *qp = q_ + static_cast<size_t>(min(qr, T - 1)) * x.q_stride + 8 * half;
+  const unsigned tile = lds + w * K::kBytes;  // this wave's, before and after the walk
+  Tile<DH>::start(q_ + static_cast<size_t>(qw) * x.q_stride, static_cast<unsigned>(x.q_stride) * 2, len - qw, lane,
+                  tile);
+  Tile<DH>::landed();
 #pragma unroll
-    for (int s = 0; s < K::kKS; ++s) qf[s] = load_bf16x8(qp + 16 * s);
-    // complete these loads here: the compiler does not see the LDS loads that share their counter
-#pragma unroll
-    for (int s = 0; s < K::kKS; ++s) asm volatile("" ::"v"(qf[s]));
-  }
+  for (int s = 0; s < K::kKS; ++s) qf[s] = Tile<DH>::operand(tile, lane, s);
+  lds_barrier();  // everyone has its rows: the slots may be filled
   const BlockWalk walk(q0, kRows, len, W, sinks);
   const unsigned krb = static_cast<unsigned>(x.k_stride) * 2, vrb = static_cast<unsigned>(x.v_stride) * 2;
   const typename K::Lane kl = K::load_lane(w, lane, krb), vl = K::load_lane(w, lane, vrb);
@@ -159,13 +158,15 @@ __global__ __launch_bounds__(64 * kWg, 2) void attn_fwd(AttnArgs x) {
       // right before its use)
       f32x16_t s = f32x16_t{};
       {
+        unsigned ks = slot + row_lane;
+        asm volatile("" : "+v"(ks));
         bf16x8_t kr[kAhead + 1];
 #pragma unroll
-        for (int d = 0; d < kAhead; ++d) kr[d] = K::rows(slot + row_lane, d);
+        for (int d = 0; d < kAhead; ++d) kr[d] = K::rows(ks, d);
         __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
         for (int d = 0; d < K::kKS; ++d) {
-          if (d + kAhead < K::kKS) kr[(d + kAhead) % (kAhead + 1)] = K::rows(slot + row_lane, d + kAhead);
+          if (d + kAhead < K::kKS) kr[(d + kAhead) % (kAhead + 1)] = K::rows(ks, d + kAhead);
           if (d % 2 == 0) load_part(i + 1, d / 2);
           s = __builtin_amdgcn_mfma_f32_32x32x16_bf16(kr[d % (kAhead + 1)], qf[d], s, 0, 0, 0);
           __builtin_amdgcn_sched_barrier(0);
@@ -223,19 +224,21 @@ __global__ __launch_bounds__(64 * kWg, 2) void attn_fwd(AttnArgs x) {
       l += l0 + l1;
       // O^T += V^T P^T: step n is key step n / kDT, d tile n % kDT
       {
-        auto v_of = [&](int n) { return K::cols(slot + K::kBytes + col_lane, n / K::kDT, n % K::kDT); };
+        unsigned vs = slot + K::kBytes + col_lane;
+        asm volatile("" : "+v"(vs));  // one register; the steps' XORs are then with literals
+        auto v_of = [&](int n) { return K::cols(vs, n & 1, n >> 1); };
         bf16x8_t vt[kAhead + 1];
 #pragma unroll
         for (int n = 0; n < kAhead; ++n) vt[n] = v_of(n);
 #pragma unroll
         for (int n = 0; n < 2 * K::kDT; ++n) {
           if (n + kAhead < 2 * K::kDT) vt[(n + kAhead) % (kAhead + 1)] = v_of(n + kAhead);
-          f32x16_t &o = acc[n % K::kDT];
+          f32x16_t &o = acc[n >> 1];
           o = __builtin_amdgcn_mfma_f32_32x32x16_bf16(
-              vt[n % (kAhead + 1)], __builtin_bit_cast(bf16x8_t, p[n / K::kDT]), o, 0, 0, 0);
+              vt[n % (kAhead + 1)], __builtin_bit_cast(bf16x8_t, p[n & 1]), o, 0, 0, 0);
           if constexpr (kSplit)
             o = __builtin_amdgcn_mfma_f32_32x32x16_bf16(
-                vt[n % (kAhead + 1)], __builtin_bit_cast(bf16x8_t, pl[n / K::kDT]), o, 0, 0, 0);
+                vt[n % (kAhead + 1)], __builtin_bit_cast(bf16x8_t, pl[n & 1]), o, 0, 0, 0);
           __builtin_amdgcn_sched_barrier(0);
         }
       }
@@ -255,19 +258,17 @@ __global__ __launch_bounds__(64 * kWg, 2) void attn_fwd(AttnArgs x) {
         acc[j][e] = in ? acc[j][e] * inv : 0.0f;
         worst = fmaf(0.0f, acc[j][e], worst);  // NaN if any is not finite
       }
-    if (qr < T) {
-      bf16_t *op = o_ + static_cast<size_t>(qr) * ostride + 4 * half;
-#pragma unroll
-      for (int j = 0; j < K::kDT; ++j)
-#pragma unroll
-        for (int g = 0; g < 4; ++g)
-          *reinterpret_cast<uint2 *>(op + 32 * j + 8 * g) =
-              make_uint2(pack_bf16x2(acc[j][4 * g], acc[j][4 * g + 1]),
-                         pack_bf16x2(acc[j][4 * g + 2], acc[j][4 * g + 3]));
-      // ln of the denominator sum_u exp(scale s_u) = scale m + ln l
-      if (lse_ && half == 0)
-        lse_[qr] = in ? (m * c + __builtin_amdgcn_logf(lt)) * 0.6931471805599453f : -__builtin_inff();
-    }
+    lds_barrier();  // everyone is done with the slots
+    Tile<DH>::store(
+        tile, lane,
+        [&](int j, int g) {
+          return u32x2_t{pack_bf16x2(acc[j][4 * g], acc[j][4 * g + 1]),
+                         pack_bf16x2(acc[j][4 * g + 2], acc[j][4 * g + 3])};
+        },
+        o_ + static_cast<size_t>(qw) * ostride, ostride, T - qw);
+    // ln of the denominator sum_u exp(scale s_u) = scale m + ln l
+    if (lse_ && half == 0 && qr < T)
+      lse_[qr] = in ? (m * c + __builtin_amdgcn_logf(lt)) * 0.6931471805599453f : -__builtin_inff();
     const unsigned long long rows = __ballot(in && !(worst == 0.0f) && lt < __builtin_inff());
     odd = static_cast<unsigned>(rows | (rows >> 32));
   };

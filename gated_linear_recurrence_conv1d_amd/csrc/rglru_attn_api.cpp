@@ -81,6 +81,22 @@ rglru_status check_attn(int B, int T, int Hq, int Hkv, int dh, long long q_strid
 // units.
 float max_floor(float c) { return -2.9e38f / (c > 1.0f ? c : 1.0f); }
 
+// Where the parts of the attention backward's workspace begin (lse2 first), and its size.
+struct AttnBwdLayout {
+  size_t delta, part, first, span, total;
+};
+AttnBwdLayout attn_bwd_layout(const rglru::AttnBwdPlan &p, int B, int T, int Hq, int Hkv, int dh) {
+  using rglru::align_up;
+  AttnBwdLayout l;
+  l.delta = align_up(static_cast<size_t>(B) * T * Hq * sizeof(float));
+  l.part = 2 * l.delta;
+  // per workgroup: a block begun before its share and one that goes on behind it, dV and dK of 128 keys
+  l.first = l.part + align_up(static_cast<size_t>(p.groups) * 2 * 2 * 128 * dh * sizeof(float));
+  l.span = l.first + align_up((p.entries + 1) * sizeof(long long));
+  l.total = l.span + align_up(p.entries * Hkv * sizeof(int2));
+  return l;
+}
+
 rglru_status check_paged(int N, int Hq, int Hkv, int dh, int page_size, int max_pages, int window,
                          int sinks, rglru_dtype dt) {
   if (page_size < 1 || max_pages < 1 || window < 1 || sinks < 0) return RGLRU_ERR_INVALID_ARG;
@@ -265,9 +281,7 @@ size_t rglru_local_attention_backward_workspace_size(int B, int T, int Hq, int H
   if (check_attn(B, T, Hq, Hkv, dh, static_cast<long long>(Hq) * dh, static_cast<long long>(Hkv) * dh,
                  static_cast<long long>(Hkv) * dh, window, sinks, 0.0f, RGLRU_BF16) != RGLRU_OK)
     return 0;
-  const rglru::AttnBwdPlan p = rglru::attn_bwd_plan(B, T, Hq, Hkv, std::min(window, T), sinks);
-  return rglru::align_up(rglru::attn_bwd_stat_bytes(B, T, Hq)) +
-         rglru::align_up(rglru::attn_bwd_part_floats(p, B, Hkv, dh) * sizeof(float));
+  return attn_bwd_layout(rglru::attn_bwd_plan(B, T, Hq, Hkv, std::min(window, T), sinks), B, T, Hq, Hkv, dh).total;
 }
 
 rglru_status rglru_local_attention_backward(
@@ -308,18 +322,21 @@ rglru_status rglru_local_attention_backward(
   window = std::min(window, T);
   sinks = std::min(sinks, T);
   const rglru::AttnBwdPlan p = rglru::attn_bwd_plan(B, T, Hq, Hkv, window, sinks);
+  const AttnBwdLayout at = attn_bwd_layout(p, B, T, Hq, Hkv, dh);
   char *ws = static_cast<char *>(workspace);
   rglru::AttnBwdArgs a = {};
   a.q = q, a.k = k, a.v = v, a.o = o, a.do_ = d_o, a.lse = lse, a.lens = lens;
   a.dq = dq, a.dk = dk, a.dv = dv;
-  a.stat = reinterpret_cast<float2 *>(ws);
-  a.part = reinterpret_cast<float *>(
-      ws + rglru::align_up(rglru::attn_bwd_stat_bytes(B, T, Hq)));
+  a.lse2 = reinterpret_cast<float *>(ws);
+  a.delta = reinterpret_cast<float *>(ws + at.delta);
+  a.part = reinterpret_cast<float *>(ws + at.part);
+  a.first = reinterpret_cast<long long *>(ws + at.first);
+  a.span = reinterpret_cast<int2 *>(ws + at.span);
   a.B = B, a.T = T, a.Hq = Hq, a.Hkv = Hkv, a.group = Hq / Hkv;
   a.q_stride = q_stride, a.k_stride = k_stride, a.v_stride = v_stride;
   a.dq_stride = dq_stride, a.dk_stride = dk_stride, a.dv_stride = dv_stride;
   a.window = window, a.sinks = sinks, a.scale = scale, a.c = scale * 1.4426950408889634f;
-  a.nsb = p.nsb, a.s_sink = p.s_sink, a.s_win = p.s_win, a.slots = p.slots;
+  a.groups = p.groups;
   (void)hipGetLastError();
   return hip_status(
       rglru::launch_local_attention_backward(a, dh, static_cast<hipStream_t>(stream)));

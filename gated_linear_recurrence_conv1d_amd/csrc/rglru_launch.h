@@ -121,28 +121,27 @@ struct AttnArgs {
 };
 hipError_t launch_local_attention(const AttnArgs &a, hipStream_t s);
 
-// Its backward. stat [B][Hq][T] (lse in exp2 units, delta) and part (dK, dV partial sums of the key
-// blocks that are split) lie in the workspace; key blocks with sinks have s_sink splits, the others s_win.
+// Its backward. In the workspace: lse2 (lse in exp2 units) and delta [B][Hq][T], part (the dK, dV of key
+// blocks that several workgroups share), and who has which (first, span).
 struct AttnBwdPlan {
-  int nsb, s_sink, s_win;  // key blocks with sinks; splits of those and of the others
-  int slots;               // workgroups per (sequence, key/value head)
+  int groups;      // workgroups that share the key side's work
+  size_t entries;  // (sequence, key block) pairs
 };
 struct AttnBwdArgs {
   const void *q, *k, *v, *o, *do_;
   const float *lse;
   const int *lens;  // [B] or NULL
   void *dq, *dk, *dv;
-  float2 *stat;
-  float *part;
+  float *lse2, *delta, *part;
+  long long *first;  // [entries + 1]
+  int2 *span;        // [Hkv][entries]
   int B, T, Hq, Hkv, group;
   long long q_stride, k_stride, v_stride, dq_stride, dk_stride, dv_stride;
   int window, sinks;
   float scale, c;  // c = scale * log2(e)
-  int nsb, s_sink, s_win, slots;
+  int groups;
 };
 AttnBwdPlan attn_bwd_plan(int B, int T, int Hq, int Hkv, int window, int sinks);
-size_t attn_bwd_stat_bytes(int B, int T, int Hq);
-size_t attn_bwd_part_floats(const AttnBwdPlan &p, int B, int Hkv, int dh);
 hipError_t launch_local_attention_backward(const AttnBwdArgs &a, int dh, hipStream_t s);
 
 // Attention of one token per sequence over a paged cache; part and stat hold the chunks' O and

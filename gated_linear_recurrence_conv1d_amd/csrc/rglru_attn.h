@@ -73,13 +73,12 @@ template <int DH, int WAVES = kWg> struct Blk {  // WAVES: how many share the lo
                  static_cast<unsigned>(((lane % kCPR) ^ swz(row + kPart * p)) * 16);
     return l;
   }
-  // that load: base is the block's first row, rows those of the sequence from there on, dst the block's
-  // LDS byte address
-  __device__ __forceinline__ static void load(const bf16_t *base, unsigned row_bytes, int rows, int ii,
-                                              int w, const Lane &l, unsigned dst) {
-    const __amdgpu_buffer_rsrc_t src =
-        rsrc(base + static_cast<size_t>(ii * kPart) * (row_bytes / 2), row_bytes, rows - ii * kPart);
-    dma_16b(src, l.off[ii % kPar], static_cast<unsigned>(uni(dst + (w + WAVES * ii) * 1024)));
+  // that load, from the block's buffer to its LDS byte address dst. (One buffer for all of a block's loads:
+  // one for each would cost some 25 scalar instructions a load, as many cycles as the block's MFMAs at DH 128.)
+  __device__ __forceinline__ static void load(__amdgpu_buffer_rsrc_t src, unsigned row_bytes, int ii, int w,
+                                              const Lane &l, unsigned dst) {
+    dma_16b(src, l.off[ii % kPar] + ii * kPart * row_bytes,
+            static_cast<unsigned>(uni(dst + (w + WAVES * ii) * 1024)));
   }
   // A block's two reads, from byte addresses that depend on the lane only through one register: the
   // row length and every block start are multiples of the bits that the steps change by XOR.
@@ -128,8 +127,9 @@ template <int DH> struct Tile {
                                                unsigned tile) {
     asm volatile("" : "+v"(lane));  // (as in store)
     const typename K::Lane l = K::load_lane(0, lane, row_bytes);
+    const __amdgpu_buffer_rsrc_t src = K::rsrc(base, row_bytes, rows);
 #pragma unroll
-    for (int ii = 0; ii < K::kLPW; ++ii) K::load(base, row_bytes, rows, ii, 0, l, tile);
+    for (int ii = 0; ii < K::kLPW; ++ii) K::load(src, row_bytes, ii, 0, l, tile);
   }
   __device__ __forceinline__ static void landed() { asm volatile("s_waitcnt vmcnt(0)" ::: "memory"); }
   // this lane's row as a B operand, k-step s: its values 16 s + 8 (lane / 32) ..

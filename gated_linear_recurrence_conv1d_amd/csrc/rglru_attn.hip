@@ -117,19 +117,26 @@ __global__ __launch_bounds__(64 * kWg, 2) void attn_fwd(AttnArgs x) {
   const BlockWalk walk(q0, kRows, len, W, sinks);
   const unsigned krb = static_cast<unsigned>(x.k_stride) * 2, vrb = static_cast<unsigned>(x.v_stride) * 2;
   const typename K::Lane kl = K::load_lane(w, lane, krb), vl = K::load_lane(w, lane, vrb);
-  // the n-th of this wave's 2 kLPW loads of block i, of K and V in turn (past the last block: zeros,
-  // without touching memory)
-  auto load_part = [&](int i, int n) {
-    const int u0 = walk.first_row(min(i, walk.n - 1)), ii = n / 2, rows = i < walk.n ? len - u0 : 0;
-    const unsigned dst = lds + (i & 1) * K::kSlot;
-    if (n % 2 == 0)
-      K::load(k_ + static_cast<size_t>(u0) * x.k_stride, krb, rows, ii, w, kl, dst);
-    else
-      K::load(v_ + static_cast<size_t>(u0) * x.v_stride, vrb, rows, ii, w, vl, dst + K::kBytes);
+  // block i's rows (past the last block: none, which reads zeros without touching memory)
+  struct Src {
+    __amdgpu_buffer_rsrc_t k, v;
+    unsigned dst;
   };
-  auto load_block = [&](int i) {
+  auto src_of = [&](int i) {
+    const int u0 = walk.first_row(min(i, walk.n - 1)), rows = i < walk.n ? len - u0 : 0;
+    return Src{K::rsrc(k_ + static_cast<size_t>(u0) * x.k_stride, krb, rows),
+               K::rsrc(v_ + static_cast<size_t>(u0) * x.v_stride, vrb, rows), lds + (i & 1) * K::kSlot};
+  };
+  // the n-th of this wave's 2 kLPW loads of a block, of K and V in turn
+  auto load_part = [&](const Src &src, int n) {
+    if (n % 2 == 0)
+      K::load(src.k, krb, n / 2, w, kl, src.dst);
+    else
+      K::load(src.v, vrb, n / 2, w, vl, src.dst + K::kBytes);
+  };
+  auto load_block = [&](const Src &src) {
 #pragma unroll
-    for (int n = 0; n < 2 * K::kLPW; ++n) load_part(i, n);
+    for (int n = 0; n < 2 * K::kLPW; ++n) load_part(src, n);
   };
   const unsigned row_lane = K::row_lane(lane), col_lane = K::col_lane(lane);
 
@@ -141,7 +148,7 @@ __global__ __launch_bounds__(64 * kWg, 2) void attn_fwd(AttnArgs x) {
 #pragma unroll
     for (int j = 0; j < K::kDT; ++j) acc[j] = f32x16_t{};
     float m = x.floor, l = 0.0f;  // running maximum (of raw scores), and this half's sum
-    load_block(0);
+    load_block(src_of(0));
     for (int i = 0; i < walk.n; ++i) {
       __builtin_amdgcn_s_waitcnt(0x0F70);  // vmcnt(0): this wave's rows of block i landed
       lds_barrier();                        // everyone's landed; everyone is done with block i - 1
@@ -151,7 +158,8 @@ __global__ __launch_bounds__(64 * kWg, 2) void attn_fwd(AttnArgs x) {
       // (that branch kept apart from the next one: as its else, it costs registers)
       int burst = vis ? 0 : 1;
       asm volatile("" : "+v"(burst));
-      if (uni(burst)) load_block(i + 1);
+      const Src src = src_of(i + 1);
+      if (uni(burst)) load_block(src);
       if (!vis) continue;
       const unsigned slot = lds + (i & 1) * K::kSlot;
       // S^T: K rows read kAhead steps ahead, pinned by the scheduling barriers (the compiler else reads each
@@ -167,7 +175,7 @@ __global__ __launch_bounds__(64 * kWg, 2) void attn_fwd(AttnArgs x) {
 #pragma unroll
         for (int d = 0; d < K::kKS; ++d) {
           if (d + kAhead < K::kKS) kr[(d + kAhead) % (kAhead + 1)] = K::rows(ks, d + kAhead);
-          if (d % 2 == 0) load_part(i + 1, d / 2);
+          if (d % 2 == 0) load_part(src, d / 2);
           s = __builtin_amdgcn_mfma_f32_32x32x16_bf16(kr[d % (kAhead + 1)], qf[d], s, 0, 0, 0);
           __builtin_amdgcn_sched_barrier(0);
         }

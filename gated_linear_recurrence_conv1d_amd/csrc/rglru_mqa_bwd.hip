@@ -167,10 +167,10 @@ __device__ __forceinline__ void dq_side(const AttnBwdArgs &a, DqLds<DH> &sh, int
   const typename K::Lane ll = K::load_lane(rt, lane, rb);
   auto load_block = [&](int i, int sl) {
     const int u0 = walk_.first_row(i);
+    const __amdgpu_buffer_rsrc_t src = K::rsrc(rows_ + static_cast<size_t>(u0) * stride, rb, len - u0);
 #pragma unroll
     for (int ii = 0; ii < K::kLPW; ++ii)
-      K::load(rows_ + static_cast<size_t>(u0) * stride, rb, len - u0, ii, rt, ll,
-              lds + sl * K::kSlot + (SIDE ? K::kBytes : 0u));
+      K::load(src, rb, ii, rt, ll, lds + sl * K::kSlot + (SIDE ? K::kBytes : 0u));
   };
   const unsigned row_lane = K::row_lane(lane) + (SIDE ? K::kBytes : 0u), col_lane = K::col_lane(lane);
   f32x16_t acc[K::kDT];  // side 1: dQ^T
@@ -413,10 +413,11 @@ __device__ __forceinline__ void dkv_side(const AttnBwdArgs &a, DkvLds<DH> &sh, i
       const __amdgpu_buffer_rsrc_t st = __builtin_amdgcn_make_buffer_rsrc(
           wave_uniform((SIDE ? a.delta : a.lse2) + (static_cast<size_t>(b) * Hq + h) * T + q0),
           static_cast<short>(0), uni(min(len - q0, kBlk) * 4), kRawWord3);
+      const __amdgpu_buffer_rsrc_t src =
+          K::rsrc(rows_ + static_cast<size_t>(q0) * (rb / 2) + static_cast<size_t>(h) * DH, rb, len - q0);
 #pragma unroll
       for (int ii = 0; ii < K::kLPW; ++ii)
-        K::load(rows_ + static_cast<size_t>(q0) * (rb / 2) + static_cast<size_t>(h) * DH, rb, len - q0, ii, kt, ll,
-                lds + sl * K::kSlot + (SIDE ? K::kBytes : 0u));
+        K::load(src, rb, ii, kt, ll, lds + sl * K::kSlot + (SIDE ? K::kBytes : 0u));
       dma_4b(st, lane * 4, lds_addr(sh.rowv[SIDE][sl]));
     };
     const unsigned row_lane = K::row_lane(lane) + (SIDE ? K::kBytes : 0u);  // side 0 reads Q, 1 dO

@@ -533,8 +533,18 @@ template <int DH> __global__ __launch_bounds__(256) void attn_dkv_sum(AttnBwdArg
   f32x4_t acc = {};
   if (span.x >= 0) {
     const float *const part = a.part + static_cast<size_t>(side) * kOwn * DH + 4 * unit;
-    for (int w = span.x; w <= span.y; ++w)
-      acc += *reinterpret_cast<const f32x4_t *>(part + (2 * static_cast<size_t>(w) + (w == span.x)) * 2 * kOwn * DH);
+    constexpr int kAt = 4;  // parts whose loads are under way at a time
+    for (int w0 = span.x; w0 <= span.y; w0 += kAt) {
+      f32x4_t x[kAt];
+#pragma unroll
+      for (int j = 0; j < kAt; ++j) {
+        const int w = min(w0 + j, span.y);
+        x[j] = *reinterpret_cast<const f32x4_t *>(part + (2 * static_cast<size_t>(w) + (w == span.x)) * 2 * kOwn * DH);
+      }
+#pragma unroll
+      for (int j = 0; j < kAt; ++j)
+        if (w0 + j <= span.y) acc += x[j];
+    }
   }
   const int nkb = (a.T + kOwn - 1) / kOwn, n = a.B * nkb;
   const int kvh = uni(i / n), e = i - kvh * n, b = uni(e / nkb), kb = e - b * nkb;

@@ -394,6 +394,7 @@ def rglru_backward(x, conv_w, W_a, b_a, W_x, b_x, Lambda, h0, y, dy, dh_T, dx, d
 # `stream`, else on that device's current stream.
 _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (
     lambda index: torch.cuda.current_stream(index).cuda_stream)
+_current_device = getattr(torch._C, "_cuda_getDevice", None) or torch.cuda.current_device
 
 
 def _call(where, fn, q, stream, keep, *args):
@@ -415,7 +416,7 @@ def _call(where, fn, q, stream, keep, *args):
             for t in keep:  # from the current stream's pool: not reused before this stream is done
                 t.record_stream(stream)
             s = stream.cuda_stream
-        if index == torch.cuda.current_device():
+        if index == _current_device():  # a tensor lives there: the runtime is up
             status = fn(*args, s)
         else:
             with torch.cuda.device(index):
@@ -442,10 +443,10 @@ def qk_norm_rope(q, k, positions, inv_freq, q_w=None, k_w=None, eps=1e-6, v=None
     """Returns (q_out, k_out), new contiguous tensors unless given (q and k themselves: in place)."""
     new = []
     if q_out is None:
-        q_out = torch.empty_like(q, memory_format=torch.contiguous_format)
+        q_out = _ext.empty_as(q)
         new.append(q_out)
     if k_out is None:
-        k_out = torch.empty_like(k, memory_format=torch.contiguous_format)
+        k_out = _ext.empty_as(k)
         new.append(k_out)
     rglru_qk_norm_rope(q, k, positions, inv_freq, q_out, k_out, q_w, k_w, eps, v, k_pages, v_pages,
                        slots, stream, _keep=new)
@@ -497,7 +498,7 @@ def rglru_local_attention(q, k, v, o, window, sinks=0, lens=None, scale=0.0, lse
 
 def local_attention(q, k, v, window, sinks=0, lens=None, scale=0.0, want_lse=False, stream=None):
     """Returns o [B,T,Hq,dh] (bf16), or (o, lse) with lse f32 [B,Hq,T], which the backward needs."""
-    new = [torch.empty_like(q, memory_format=torch.contiguous_format)]
+    new = [_ext.empty_as(q)]
     if want_lse:
         B, T, Hq, _ = q.shape
         new.append(torch.empty((B, Hq, T), dtype=torch.float32, device=q.device))
@@ -559,14 +560,14 @@ def rglru_paged_attention(q, k_pages, v_pages, block_table, lens, o, window, sin
 def paged_attention(q, k_pages, v_pages, block_table, lens, window, sinks=0, scale=0.0,
                     workspace=None, stream=None):
     """Returns o [N,Hq,dh] of q's type."""
-    new = [torch.empty_like(q, memory_format=torch.contiguous_format)]
+    new = [_ext.empty_as(q)]
     if workspace is None and q.dim() == 3 and k_pages.dim() == 4 and block_table.dim() == 2:
         N, Hq, dh = q.shape
         _, page, Hkv, _ = k_pages.shape
         n = rglru_paged_attention_workspace_size(N, Hq, Hkv, dh, page, block_table.shape[1], window,
                                                  sinks, q.dtype)
         if n:
-            workspace = torch.empty(n, dtype=torch.uint8, device=q.device)
+            workspace = _ext.empty_bytes(q, n)
             new.append(workspace)
     rglru_paged_attention(q, k_pages, v_pages, block_table, lens, new[0], window, sinks, scale,
                           workspace, stream, _keep=new)

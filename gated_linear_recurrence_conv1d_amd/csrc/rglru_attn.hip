@@ -8,9 +8,13 @@
 // query row in each lane: S^T = K Q^T (A = K rows from LDS, B = q in registers for the kernel's life) and
 // O^T += V^T P^T (A = V^T from LDS by transposing reads, B = P). The accumulator layout of S^T is already the
 // B operand's of the second, so P never leaves its lane. A wave owns 32 rows and all of dh (64 registers of q
-// and 128 of O at dh 256: two waves per SIMD); four waves are a workgroup, at least two workgroups share a
+// and 128 of O at dh 256: two waves per SIMD); four waves are a workgroup, two or three workgroups share a
 // CU, and each wave works alone between the barriers (one per 32-key block), so that one wave's matrix
 // work runs beside another's exponentials.
+//
+// Bound by the matrix and vector units in turn: they overlap only across the two or three waves of a SIMD. 98 us
+// at B8 T2048 (ragged) Hq10 dh256 W1024, 345 us at T16384 Hq8 Hkv2 dh128 W4096 (700 TFLOP/s). Without its loads
+// the first takes a quarter less, without LDS reads or without exponentials a tenth.
 #include "rglru_attn.h"
 #include "rglru_launch.h"
 
@@ -72,13 +76,17 @@ __device__ __forceinline__ void exact_row(const bf16_t *q, const bf16_t *k, cons
   for (int i = 0; i < kPer; ++i) o[lane * kPer + i] = f32_to_bf16(a[i] / l);
 }
 
-template <int DH>
-__global__ __launch_bounds__(64 * kWg, 2) void attn_fwd(AttnArgs x) {
+// KS: groups of four waves that share the rows, each with every KS-th key block, joined at the end.
+template <int DH, int KS>
+__global__ __launch_bounds__(64 * kWg * KS, 2) void attn_fwd(AttnArgs x) {
   typedef Blk<DH> K;
   constexpr int kRows = kOwn;  // per workgroup
-  __shared__ __attribute__((aligned(1024))) unsigned char smem[2 * K::kSlot];  // two slots of K, V
-  const unsigned lds = lds_addr(smem);
-  const int tid = threadIdx.x, w = uni(tid >> 6), lane = tid & 63;
+  __shared__ __attribute__((aligned(1024))) unsigned char smem[KS * 2 * K::kSlot];  // two slots of K, V a group
+  __shared__ float joined[KS > 1 ? 2 : 1][KS > 1 ? 64 * kWg : 1];                   // group 1's m and l
+  static_assert(KS <= 2 && (KS == 1 || sizeof(smem) >= kRows * DH * sizeof(float)), "room for group 1's O");
+  const int tid = threadIdx.x, lane = tid & 63;
+  const int grp = KS > 1 ? uni(tid >> 6) / kWg : 0, w = uni(tid >> 6) - grp * kWg;
+  const unsigned lds = lds_addr(smem) + grp * 2 * K::kSlot;
   const int lrow = lane & 31, half = lane >> 5;
   const int T = x.T, Hq = x.Hq, W = x.window, sinks = x.sinks;
   const float c = x.scale * kLn2Inv;
@@ -94,11 +102,11 @@ __global__ __launch_bounds__(64 * kWg, 2) void attn_fwd(AttnArgs x) {
   bf16_t *const o_ = static_cast<bf16_t *>(x.o) + tok * ostride + static_cast<size_t>(h) * DH;
   float *const lse_ = x.lse ? x.lse + (static_cast<size_t>(b) * Hq + h) * T : nullptr;
   if (q0 >= len) {  // no row of the block belongs to the sequence
-    for (int i = tid; i < kRows * (DH / 8); i += 64 * kWg) {
+    for (int i = tid; i < kRows * (DH / 8); i += 64 * kWg * KS) {
       const int t = q0 + i / (DH / 8);
       if (t < T) *reinterpret_cast<u32x4_t *>(o_ + static_cast<size_t>(t) * ostride + (i % (DH / 8)) * 8) = u32x4_t{};
     }
-    for (int i = tid; lse_ && i < kRows; i += 64 * kWg)
+    for (int i = tid; lse_ && i < kRows; i += 64 * kWg * KS)
       if (q0 + i < T) lse_[q0 + i] = -__builtin_inff();
     return;
   }
@@ -117,13 +125,13 @@ __global__ __launch_bounds__(64 * kWg, 2) void attn_fwd(AttnArgs x) {
   const BlockWalk walk(q0, kRows, len, W, sinks);
   const unsigned krb = static_cast<unsigned>(x.k_stride) * 2, vrb = static_cast<unsigned>(x.v_stride) * 2;
   const typename K::Lane kl = K::load_lane(w, lane, krb), vl = K::load_lane(w, lane, vrb);
-  // block i's rows (past the last block: none, which reads zeros without touching memory)
+  // the rows of the group's i-th block (past the last one: none, which reads zeros without touching memory)
   struct Src {
     __amdgpu_buffer_rsrc_t k, v;
     unsigned dst;
   };
   auto src_of = [&](int i) {
-    const int u0 = walk.first_row(min(i, walk.n - 1)), rows = i < walk.n ? len - u0 : 0;
+    const int n = KS * i + grp, u0 = walk.first_row(min(n, walk.n - 1)), rows = n < walk.n ? len - u0 : 0;
     return Src{K::rsrc(k_ + static_cast<size_t>(u0) * x.k_stride, krb, rows),
                K::rsrc(v_ + static_cast<size_t>(u0) * x.v_stride, vrb, rows), lds + (i & 1) * K::kSlot};
   };
@@ -149,11 +157,11 @@ __global__ __launch_bounds__(64 * kWg, 2) void attn_fwd(AttnArgs x) {
     for (int j = 0; j < K::kDT; ++j) acc[j] = f32x16_t{};
     float m = x.floor, l = 0.0f;  // running maximum (of raw scores), and this half's sum
     load_block(src_of(0));
-    for (int i = 0; i < walk.n; ++i) {
+    for (int i = 0; i < (walk.n + KS - 1) / KS; ++i) {
       __builtin_amdgcn_s_waitcnt(0x0F70);  // vmcnt(0): this wave's rows of block i landed
       lds_barrier();                        // everyone's landed; everyone is done with block i - 1
-      const int U = walk.first_row(i);
-      const bool vis = U <= qw + 31 && (U + 31 > qw - W || U < sinks) && qw < len;
+      const int U = walk.first_row(KS * i + grp);
+      const bool vis = (KS == 1 || KS * i + grp < walk.n) && U <= qw + 31 && (U + 31 > qw - W || U < sinks) && qw < len;
       // the next block's loads: between the MFMAs, or at once in a wave that sees nothing of this block
       // (that branch kept apart from the next one: as its else, it costs registers)
       int burst = vis ? 0 : 1;
@@ -258,6 +266,36 @@ __global__ __launch_bounds__(64 * kWg, 2) void attn_fwd(AttnArgs x) {
       __builtin_amdgcn_s_setprio(0);
     }
     __builtin_amdgcn_s_waitcnt(0x0F70);  // the zeros past the last block have landed too
+    lds_barrier();                        // everyone is done with the slots
+    if constexpr (KS > 1) {
+      f32x4_t *const o1 = reinterpret_cast<f32x4_t *>(smem) + w * 64 + lane;  // in the accumulators' order
+      if (grp == 1) {
+#pragma unroll
+        for (int j = 0; j < K::kDT; ++j)
+#pragma unroll
+          for (int g = 0; g < 4; ++g)
+            o1[(4 * j + g) * 64 * kWg] = f32x4_t{acc[j][4 * g], acc[j][4 * g + 1], acc[j][4 * g + 2], acc[j][4 * g + 3]};
+        joined[0][w * 64 + lane] = m;
+        joined[1][w * 64 + lane] = l;
+      }
+      lds_barrier();
+      if (grp == 0) {
+        const float m1 = joined[0][w * 64 + lane], mn = fmaxf(m, m1);
+        const float f0 = __builtin_amdgcn_exp2f((m - mn) * c), f1 = __builtin_amdgcn_exp2f((m1 - mn) * c);
+        l = l * f0 + joined[1][w * 64 + lane] * f1;
+        m = mn;
+#pragma unroll
+        for (int j = 0; j < K::kDT; ++j)
+#pragma unroll
+          for (int g = 0; g < 4; ++g) {
+            const f32x4_t y = o1[(4 * j + g) * 64 * kWg];
+#pragma unroll
+            for (int e = 0; e < 4; ++e) acc[j][4 * g + e] = acc[j][4 * g + e] * f0 + y[e] * f1;
+          }
+      }
+      lds_barrier();
+      if (grp != 0) return;
+    }
     // normalise and store; lane = row, accumulator e of tile j is d = 32 j + 8 (e / 4) + 4 half + e % 4
     float lo, hi;
     halves(l, lo, hi);
@@ -272,7 +310,6 @@ __global__ __launch_bounds__(64 * kWg, 2) void attn_fwd(AttnArgs x) {
         acc[j][e] = in ? acc[j][e] * inv : 0.0f;
         worst = fmaf(0.0f, acc[j][e], worst);  // NaN if any is not finite
       }
-    lds_barrier();  // everyone is done with the slots
     Tile<DH>::store(
         tile, lane,
         [&](int j, int g) {
@@ -301,9 +338,15 @@ __global__ __launch_bounds__(64 * kWg, 2) void attn_fwd(AttnArgs x) {
 
 namespace {
 
+// With a workgroup a CU or fewer, each SIMD would have one wave, whose steps wait for each other: two share the
+// keys then (17.5 us instead of 22 at B3 T1111 Hq6 Hkv2 dh128 W300, 7.3 instead of 8.1 at B1 T101 Hq4 dh64).
 template <int DH> hipError_t launch(const AttnArgs &a, hipStream_t s) {
-  const unsigned nq = static_cast<unsigned>((a.T + kOwn - 1) / kOwn);
-  attn_fwd<DH><<<nq * a.B * a.Hq, 64 * kWg, 0, s>>>(a);
+  constexpr unsigned kCus = 256;
+  const unsigned groups = static_cast<unsigned>((a.T + kOwn - 1) / kOwn) * a.B * a.Hq;
+  if (groups <= kCus && a.T > kBlk)
+    attn_fwd<DH, 2><<<groups, 64 * kWg * 2, 0, s>>>(a);
+  else
+    attn_fwd<DH, 1><<<groups, 64 * kWg, 0, s>>>(a);
   return hipGetLastError();
 }
 

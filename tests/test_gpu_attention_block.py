@@ -265,6 +265,21 @@ def test_attention_backward(B, T, Hq, Hkv, dh, W, S, lens, scale):
         assert not dq.any() and not dk.any()
 
 
+MANY = [  # more workgroups than CUs, and more key blocks in all than 64 and than 64 * 64
+    (22, 260, 4, 2, 64, 100, 3, [260 - 11 * (i % 24) for i in range(22)], 0.0),
+    (30, 140, 5, 1, 128, 90, 0, None, 0.0),
+    (26, 270, 4, 1, 256, 200, 5, [270 if i % 3 else 17 * i % 271 for i in range(26)], 0.0),
+    (6, 700, 8, 2, 64, 300, 3, [700, 0, 333, 700, 64, 1], 0.0),
+    (4200, 20, 1, 1, 64, 7, 0, None, 0.0),
+]
+
+
+@pytest.mark.parametrize("B,T,Hq,Hkv,dh,W,S,lens,scale", MANY)
+def test_attention_of_many(B, T, Hq, Hkv, dh, W, S, lens, scale):
+    test_attention(B, T, Hq, Hkv, dh, W, S, lens, scale)
+    test_attention_backward(B, T, Hq, Hkv, dh, W, S, lens, scale)
+
+
 def test_attention_backward_against_differences():
     """The directional derivative along random steps, from fp64 central differences of the oracle's
     forward: within the gradients' own bound, summed along the step (plus 1e-6 for the differences)."""

@@ -70,11 +70,15 @@ rglru_status check_attn(int B, int T, int Hq, int Hkv, int dh, long long q_strid
   if (B > 65535 || Hq > 65535) return RGLRU_ERR_UNSUPPORTED;
   if (q_stride > kMaxStride || k_stride > kMaxStride || v_stride > kMaxStride)
     return RGLRU_ERR_UNSUPPORTED;
-  // a sequence's k and v must fit a 32-bit buffer range, with room past it for the kernel's
-  // no-op loads
+  // a sequence's k and v stay well within 32-bit byte offsets
   constexpr long long kRange = 1LL << 30;
   if (T * k_stride * 2 > kRange || T * v_stride * 2 > kRange) return RGLRU_ERR_UNSUPPORTED;
   return RGLRU_OK;
+}
+
+// The sum over workgroups' parts has dh / 4 workgroups for each key block: a launch's grid has to hold them.
+bool bwd_grid_ok(int B, int T, int Hkv, int dh) {
+  return (T + 127LL) / 128 * B * Hkv * (dh / 4) <= 0x7FFFFFFF;
 }
 
 // The kernels' running maximum starts here: below every score that matters, and finite in exp2
@@ -279,7 +283,8 @@ rglru_status rglru_local_attention(const void *q, const void *k, const void *v, 
 size_t rglru_local_attention_backward_workspace_size(int B, int T, int Hq, int Hkv, int dh,
                                                      int window, int sinks) {
   if (check_attn(B, T, Hq, Hkv, dh, static_cast<long long>(Hq) * dh, static_cast<long long>(Hkv) * dh,
-                 static_cast<long long>(Hkv) * dh, window, sinks, 0.0f, RGLRU_BF16) != RGLRU_OK)
+                 static_cast<long long>(Hkv) * dh, window, sinks, 0.0f, RGLRU_BF16) != RGLRU_OK ||
+      !bwd_grid_ok(B, T, Hkv, dh))
     return 0;
   return attn_bwd_layout(rglru::attn_bwd_plan(B, T, Hq, Hkv, std::min(window, T), sinks), B, T, Hq, Hkv, dh).total;
 }
@@ -293,6 +298,7 @@ rglru_status rglru_local_attention_backward(
   rglru_status st =
       check_attn(B, T, Hq, Hkv, dh, q_stride, k_stride, v_stride, window, sinks, scale, dt);
   if (st != RGLRU_OK) return st;
+  if (!bwd_grid_ok(B, T, Hkv, dh)) return RGLRU_ERR_UNSUPPORTED;
   if (!q || !k || !v || !o || !lse || !d_o || !dq || !dk || !dv) return RGLRU_ERR_INVALID_ARG;
   if (!stride_ok(dq_stride, Hq, dh) || !stride_ok(dk_stride, Hkv, dh) || !stride_ok(dv_stride, Hkv, dh))
     return RGLRU_ERR_INVALID_ARG;

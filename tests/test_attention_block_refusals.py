@@ -139,6 +139,17 @@ def test_attention_backward_refusals(kw, status):
     assert attn_bwd(**kw) == status
 
 
+def test_attention_backward_grid_limit():
+    """Sizes whose key blocks a launch's grid cannot count are refused, and have no workspace: 65535 blocks
+    of 1024 heads at dh / 4 workgroups each are 2147450880 at dh 128, which 2^31 - 1 holds, and twice that at
+    dh 256."""
+    wide = dict(B=65535, T=1, Hq=1024, Hkv=1024, dh=256, **{n: 1 << 18 for n in (
+        "q_stride", "k_stride", "v_stride", "dq_stride", "dk_stride", "dv_stride")})
+    assert attn_bwd(**wide) == UNSUP
+    assert rg.rglru_local_attention_backward_workspace_size(65535, 1, 1024, 1024, 256, 16) == 0
+    assert rg.rglru_local_attention_backward_workspace_size(65535, 1, 1024, 1024, 128, 16) > 0
+
+
 PG_PTRS = ["q", "k_pages", "v_pages", "block_table", "lens", "o"]
 PA = at(PG_PTRS)
 

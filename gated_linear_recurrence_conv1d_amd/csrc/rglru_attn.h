@@ -21,9 +21,9 @@ typedef unsigned u32x2_t __attribute__((ext_vector_type(2)));
 typedef __attribute__((address_space(3))) u32x2_t lds_u32x2_t;
 typedef float f32x4_t __attribute__((ext_vector_type(4)));
 
-constexpr int kWg = 4;         // waves per workgroup
-constexpr int kOwn = 32 * kWg; // rows (attn_dq) or keys (attn_dkv) per workgroup
-constexpr int kBlk = 32;       // rows per LDS block
+constexpr int kWg = 4;          // waves (or pairs of waves) of a workgroup that own 32 rows or keys each
+constexpr int kOwn = 32 * kWg;  // rows or keys per workgroup
+constexpr int kBlk = 32;        // rows per LDS block
 
 // An integer that is the same in every lane, kept in a scalar register (quotients and some minima run on
 // the vector unit; branches on such values, and descriptors made from them, then cost registers).
@@ -158,19 +158,7 @@ template <int DH> struct Tile {
   }
 };
 
-// Pins the order of a run of N steps of R LDS reads and M MFMAs each: the reads D steps ahead, no
-// further (the compiler else hoists more of them than there are registers).
-template <int N, int R, int M, int D> __device__ __forceinline__ void read_ahead() {
-#pragma unroll
-  for (int i = 0; i < D && i < N; ++i) __builtin_amdgcn_sched_group_barrier(0x100, R, 0);
-#pragma unroll
-  for (int i = 0; i < N; ++i) {
-    __builtin_amdgcn_sched_group_barrier(0x008, M, 0);
-    if (i + D < N) __builtin_amdgcn_sched_group_barrier(0x100, R, 0);
-  }
-}
-
-// Key row kr sees query row t (t, kr < len checked apart).
+// Query row t sees key row u (t, u < len checked apart).
 __device__ __forceinline__ bool sees(int t, int u, int W, int sinks) {
   return u <= t && (u > t - W || u < sinks);
 }

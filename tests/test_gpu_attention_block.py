@@ -150,6 +150,30 @@ def test_norm_rope_backward(dtype, lead, Hq, Hkv, dh, rot, norm, packed, shift, 
         assert torch.equal(got["d" + name], again["d" + name])
 
 
+@pytest.mark.parametrize("dtype,dh", [(BF, 256), (BF, 64), (F32, 128)])
+def test_norm_rope_backward_keeps_heads_apart(dtype, dh):
+    """Heads of q and of k share a wave: what is not finite in one kind stays out of the other's gradients, which
+    are the same to the bit."""
+    rng = np.random.default_rng(31)
+    q, k = normal(rng, 40, 3, dh, dtype=dtype), normal(rng, 40, 2, dh, dtype=dtype)
+    gq, gk = normal(rng, 40, 3, dh, dtype=dtype), normal(rng, 40, 2, dh, dtype=dtype)
+    pos, freq = torch.arange(40, device=DEV, dtype=torch.int32), torch.rand(dh // 4, device=DEV)
+    w = torch.rand(dh, device=DEV)
+    want = rg.qk_norm_rope_backward(q, k, pos, freq, gq, gk, w, w)
+    for bad in (float("nan"), float("inf")):
+        for mine, grads, other, o_w, hit, h_w in ((k, gk, "dq", "dq_w", "dk", "dk_w"), (q, gq, "dk", "dk_w", "dq", "dq_w")):
+            for x in (mine, grads):
+                keep = x[5].clone()
+                x[5, 1] = bad
+                got = rg.qk_norm_rope_backward(q, k, pos, freq, gq, gk, w, w)
+                x[5] = keep
+                assert torch.equal(got[other], want[other]) and torch.equal(got[o_w], want[o_w])
+                assert not torch.isfinite(got[h_w]).all() and not torch.isfinite(got[hit][5, 1].float()).all()
+                rest = torch.ones(40, dtype=torch.bool, device=DEV)
+                rest[5] = False
+                assert torch.equal(got[hit][rest], want[hit][rest])
+
+
 def test_norm_rope_backward_against_differences():
     """fp32 gradients against fp64 central differences of the oracle's forward, step 1e-4: off by the
     third derivative's h^2 / 6 (below 1e-6 of the gradient's norm) and the kernel's own bound, 1e-5 of

@@ -410,7 +410,8 @@ def _call(where, fn, q, stream, keep, *args):
             s = _raw_stream(index)
         else:
             if not isinstance(stream, torch.cuda.Stream):
-                stream = torch.cuda.ExternalStream(int(stream), device=index)
+                stream = (torch.cuda.ExternalStream(int(stream), device=index) if int(stream) else
+                          torch.cuda.default_stream(index))  # (0 would be a new one)
             elif stream.device_index != index:
                 raise ValueError(f"stream: on {stream.device}, q on {q.device}")
             for t in keep:  # from the current stream's pool: not reused before this stream is done

@@ -307,10 +307,10 @@ rglru_status rglru_local_attention(const void *q, const void *k, const void *v, 
  *    may be parts of one tensor and must not overlap the inputs or each other. Rows t >= lens[b]
  *    are zero, and nothing in those rows of the inputs is used
  *  workspace  at least rglru_local_attention_backward_workspace_size() bytes
- * P and dS enter their products as bf16, sums are fp32 and taken in a fixed order (no floating-point
- * atomics): results are bitwise reproducible. p comes from the scores and lse, both fp32: scores
- * (scale * s) beyond 2^16 in magnitude lose its digits. An infinite or NaN input may reach every gradient of
- * the tiles (128 rows by 64) it is in. */
+ * P and dS enter their products as bf16, sums are fp32 and taken in an order that the sizes, lens, window
+ * and sinks fix (no floating-point atomics): results are bitwise reproducible. p comes from the scores and
+ * lse, both fp32: scores (scale * s) beyond 2^16 in magnitude lose its digits. An infinite or NaN input may
+ * reach every gradient of the tiles (128 rows by 32 keys, 128 keys by 32 rows) it is in. */
 size_t rglru_local_attention_backward_workspace_size(int B, int T, int Hq, int Hkv, int dh,
                                                      int window, int sinks);
 rglru_status rglru_local_attention_backward(

@@ -350,6 +350,26 @@ def test_values_out_of_sight_do_not_matter(bad):
     check(got_v[0, ~sees], num(ref[0, ~sees]), 2 * bound[0, ~sees.cpu().numpy()] + 1e-6, "rows out of sight")
 
 
+@pytest.mark.parametrize("dh", [64, 256])
+@pytest.mark.parametrize("bad", [float("nan"), float("inf")])
+def test_values_out_of_sight_do_not_matter_of_many(bad, dh):
+    """The same with more workgroups than CUs, whose waves walk all of their keys: the other sequences and the
+    rows before are as they were, to the bit."""
+    rng = np.random.default_rng(4)
+    B, T, W, S, at = 90, 200, 30, 2, 140
+    q, k, v = packed_qkv(rng, B, T, 2, 1, dh)
+    ref = rg.local_attention(q, k, v, W, S)
+    v[7, at, 0, 5] = bad
+    got = rg.local_attention(q, k, v, W, S)
+    others = torch.arange(B, device=DEV) != 7
+    assert torch.equal(got[others], ref[others]) and torch.equal(got[7, :128], ref[7, :128])
+    assert not torch.isfinite(got[7, at:at + W, :, 5].float()).any()
+    sees = torch.zeros(T, dtype=torch.bool, device=DEV)
+    sees[at:at + W] = True
+    bound = ab.attention_bounds(*(np.nan_to_num(num(x[7:8]), posinf=0, neginf=0) for x in (q, k, v)), None, W, S)[1]
+    check(got[7, ~sees], num(ref[7, ~sees]), 2 * bound[0, ~sees.cpu().numpy()] + 1e-6, "rows out of sight")
+
+
 def test_large_scores():
     """Scores down to -1e28 (inputs near the top of bf16's useful range): one key takes all, no NaN, in
     both forms. p of the others is below exp(-1e25) = 0, so o is that key's value, rounded once."""
@@ -585,3 +605,25 @@ def test_other_stream_and_graph():
         graph.replay()
         torch.cuda.synchronize()
         assert all(torch.equal(a, b) for a, b in zip(out, want)), i
+
+
+def test_streams_by_number():
+    """A stream's number is that stream; 0 is the default stream, whatever stream is current."""
+    seen = []
+
+    class Ext:
+        @staticmethod
+        def local_attention(*args):
+            seen.append(args[-1])
+            return rg.RGLRU_OK
+
+    q = torch.zeros(1, 3, 1, 64, dtype=BF, device=DEV)
+    side, real = torch.cuda.Stream(), rg._ext
+    try:
+        rg._ext = Ext
+        with torch.cuda.stream(side):
+            for stream in (None, 0, side.cuda_stream, side, torch.cuda.default_stream()):
+                rg.rglru_local_attention(q, q, q, q, 2, stream=stream)
+    finally:
+        rg._ext = real
+    assert seen == [side.cuda_stream, 0, side.cuda_stream, side.cuda_stream, 0]

@@ -6,7 +6,7 @@
 // consecutive rows at 4 consecutive chunks) of a pass fall on different banks.
 #pragma once
 
-#include "rglru_mfma.h"
+#include "rglru_loads.h"
 
 namespace rglru {
 namespace attn {

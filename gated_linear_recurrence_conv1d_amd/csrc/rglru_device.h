@@ -184,21 +184,6 @@ __device__ __forceinline__ void dma_16b(__amdgpu_buffer_rsrc_t rsrc, unsigned vo
       : "v"(voff), "s"(lds_base), "s"(rsrc));
 }
 
-// The same with 4 bytes per lane (256 bytes).
-__device__ __forceinline__ void dma_4b(__amdgpu_buffer_rsrc_t rsrc, unsigned voff,
-                                       unsigned lds_base) {
-  unsigned saved;
-  asm volatile(
-      "s_mov_b32 %0, m0\n\t"
-      "s_mov_b32 m0, %2\n\t"
-      "s_nop 0\n\t"
-      "buffer_load_dword %1, %3, 0 offen lds\n\t"
-      "s_nop 0\n\t"
-      "s_mov_b32 m0, %0"
-      : "=&s"(saved)
-      : "v"(voff), "s"(lds_base), "s"(rsrc));
-}
-
 // LDS byte address of a __shared__ pointer (the low half of its generic address), wave-uniform.
 __device__ __forceinline__ unsigned lds_addr(const void *p) {
   return __builtin_amdgcn_readfirstlane(static_cast<unsigned>(reinterpret_cast<uintptr_t>(p)));
@@ -224,12 +209,6 @@ template <typename P> __device__ __forceinline__ P *wave_uniform(P *p) {
   const uint32_t lo = __builtin_amdgcn_readfirstlane(static_cast<uint32_t>(v));
   const uint32_t hi = __builtin_amdgcn_readfirstlane(static_cast<uint32_t>(v >> 32));
   return reinterpret_cast<P *>((static_cast<uint64_t>(hi) << 32) | lo);
-}
-
-// A value of a table that the kernel does not write, at a wave-uniform place: by scalar load.
-template <typename V> __device__ __forceinline__ V uniform_load(const V *p, long long i) {
-  typedef const __attribute__((address_space(4))) V *const_ptr;
-  return ((const_ptr)p)[i];
 }
 
 // Workgroup barrier that orders LDS accesses only: unlike __syncthreads it does not wait for the

@@ -27,6 +27,7 @@
 // N4 Hq8 Hkv2 dh128 to 131k tokens: 401 MB in 77 us (5.2 TB/s, a plain copy's rate); N128 Hq16 dh256 W2048:
 // 224 MB in 52 us and 5 us of joining.
 #include "rglru_launch.h"
+#include "rglru_loads.h"
 #include "rglru_mfma.h"
 
 #include <algorithm>

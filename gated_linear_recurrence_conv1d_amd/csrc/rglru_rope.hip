@@ -21,6 +21,7 @@
 // LDS: in registers they would halve the number of waves. There the forward moves its 185 MB at 4.2 TB/s, the
 // backward its 277 MB in 53 us, 5.2 TB/s; a plain copy reaches 5.1 TB/s.
 #include "rglru_launch.h"
+#include "rglru_loads.h"
 #include "rglru_mfma.h"
 
 #include <algorithm>

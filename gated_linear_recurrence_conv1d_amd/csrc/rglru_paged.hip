@@ -430,7 +430,7 @@ PagedPlan paged_plan(int N, int Hq, int Hkv, long long max_len, int window, int 
   const long long groups = static_cast<long long>(N) * Hkv * ((G + 15) / 16);
   constexpr long long kTarget = 512;  // workgroups: two fit a CU at a time (700, 1024, 2048: slower)
   long long chunk = (most * groups + kTarget - 1) / kTarget;
-  chunk = std::max<long long>((chunk + kPgWaves - 1) / kPgWaves * kPgWaves, kPgWaves);
+  chunk = std::max<long long>(chunk, kPgWaves);
   PagedPlan p;
   p.chunk = static_cast<int>(std::min<long long>(chunk, 1 << 28));
   p.splits = static_cast<int>((most + p.chunk - 1) / p.chunk);

@@ -7,6 +7,7 @@
 #pragma once
 
 #include "rglru_loads.h"
+#include "rglru_shares.h"
 
 namespace rglru {
 namespace attn {
@@ -20,10 +21,6 @@ typedef __attribute__((address_space(3))) u32x4_t lds_u32x4_t;
 typedef unsigned u32x2_t __attribute__((ext_vector_type(2)));
 typedef __attribute__((address_space(3))) u32x2_t lds_u32x2_t;
 typedef float f32x4_t __attribute__((ext_vector_type(4)));
-
-constexpr int kWg = 4;          // waves (or pairs of waves) of a workgroup that own 32 rows or keys each
-constexpr int kOwn = 32 * kWg;  // rows or keys per workgroup
-constexpr int kBlk = 32;        // rows per LDS block
 
 // An integer that is the same in every lane, kept in a scalar register (quotients and some minima run on
 // the vector unit; branches on such values, and descriptors made from them, then cost registers).

@@ -20,13 +20,14 @@
 // enough and they fill the gaps between the dependent steps of S. (dq with one wave for both: 220 us where this
 // takes 160 at B4 T2048 Hq10 dh256 W1024.)
 //
-// attn_dkv's items are dealt out in equal shares, one per CU, as the blocks' own numbers differ (the last
-// keys of a sequence are seen by few rows, padded sequences have fewer, sinks are seen by all): 152-168 us
-// instead of 190-202 with the same number of workgroups for every block, at the same sizes. Blocks that
+// attn_dkv's items (rglru_shares.h) are dealt out in equal shares, one per CU, as the blocks' own numbers
+// differ (the last keys of a sequence are seen by few rows, padded sequences have fewer, sinks are seen by all):
+// 152-168 us instead of 190-202 with the same number of workgroups for every block, at the same sizes. Blocks that
 // several workgroups share are summed by attn_dkv_sum, in order, from fp32 parts that lie in the accumulators'
 // order (15 us; 256 shares: with 512, 27 us, and 172-180 us for attn_dkv).
 #include "rglru_attn.h"
 #include "rglru_launch.h"
+#include "rglru_shares.h"
 
 #include <algorithm>
 #include <type_traits>
@@ -271,16 +272,6 @@ __device__ __forceinline__ void dq_side(const AttnBwdArgs &a, DqLds<DH> &sh, int
   }
 }
 
-// attn_dkv's work is a list of items: for each key/value head and each sequence's key blocks (in that order),
-// the (head of the group, 32-row block) pairs that see some of the block's keys. Workgroup w of attn_dkv
-// has the items [lo(w), lo(w + 1)), an equal share whatever the lengths are.
-__device__ __forceinline__ int item_blocks(const AttnBwdArgs &a, int K0, int len) {  // row blocks that see the keys from K0 on
-  if (K0 >= len) return 0;
-  const long long last = K0 < a.sinks ? len - 1 : min(len - 1LL, static_cast<long long>(K0) + kOwn - 2 + a.window);
-  return static_cast<int>(last / kBlk) - K0 / kBlk + 1;
-}
-__device__ __forceinline__ long long share_lo(long long total, int groups, int w) { return total * w / groups; }
-
 // One workgroup's work beside attn_dq: first[e], the items before entry e = (sequence, key block) of one
 // key/value head (the last: all of them), and span, the first and last workgroup that have a block's items
 // (-1: there are none).
@@ -291,7 +282,8 @@ __device__ __forceinline__ void plan_items(const AttnBwdArgs &a) {
     for (int e0 = 0; e0 < n; e0 += 64) {
       const int e = e0 + lane, b = min(e / nkb, a.B - 1);
       const int len = a.lens ? min(max(a.lens[b], 0), a.T) : a.T;
-      const long long own = e < n ? static_cast<long long>(item_blocks(a, (e - b * nkb) * kOwn, len)) * a.group : 0;
+      const long long own =
+          e < n ? static_cast<long long>(row_blocks((e - b * nkb) * kOwn, len, a.window, a.sinks)) * a.group : 0;
       long long sum = own;
 #pragma unroll
       for (int d = 1; d < 64; d <<= 1) {
@@ -305,14 +297,14 @@ __device__ __forceinline__ void plan_items(const AttnBwdArgs &a) {
   }
   __syncthreads();
   const long long per_head = a.first[n], total = per_head * a.Hkv;
-  // the workgroup of item i: the largest w with lo(w) <= i
-  auto wg_of = [&](long long i) { return static_cast<int>(((i + 1) * a.groups - 1) / total); };
+  const int G = share_count(total, a.groups);
   for (long long i = threadIdx.x; i < static_cast<long long>(n) * a.Hkv; i += 64 * 2 * kWg) {
     const long long head = i / n;
     const int e = static_cast<int>(i - head * n);
     const long long from = a.first[e], to = a.first[e + 1];
     a.span[i] = from == to ? make_int2(-1, -1)
-                           : make_int2(wg_of(head * per_head + from), wg_of(head * per_head + to - 1));
+                           : make_int2(share_of(total, G, head * per_head + from),
+                                       share_of(total, G, head * per_head + to - 1));
   }
 }
 
@@ -351,8 +343,10 @@ __device__ __forceinline__ void dkv_side(const AttnBwdArgs &a, DkvLds<DH> &sh, i
   const int T = a.T, Hq = a.Hq, W = a.window, sinks = a.sinks;
   const int nkb = (T + kOwn - 1) / kOwn, n = a.B * nkb;
   const long long per_head = uniform_load(a.first, n), total = per_head * a.Hkv;
+  const int G = share_count(total, a.groups);
+  if (static_cast<int>(blockIdx.x) >= G) return;  // (the whole workgroup)
   // neighbouring shares, which read the same rows, on one XCD
-  const int G = a.groups, wg = G % 8 ? blockIdx.x : blockIdx.x % 8 * (G / 8) + blockIdx.x / 8;
+  const int wg = G % 8 ? blockIdx.x : blockIdx.x % 8 * (G / 8) + blockIdx.x / 8;
   const long long hi = uni64(share_lo(total, G, wg + 1));
   for (long long pos = uni64(share_lo(total, G, wg)); pos < hi;) {  // a key block's items, or some of them
     int lane = lane_;

@@ -627,3 +627,42 @@ def test_streams_by_number():
     finally:
         rg._ext = real
     assert seen == [side.cuda_stream, 0, side.cuda_stream, side.cuda_stream, 0]
+
+
+SHORT = [  # sequences much shorter than T: fewer items of the backward's key side than workgroups
+    (1, 2048, 1, 1, 64, 1024, 0, [100], 0.0),
+    (1, 2048, 10, 1, 128, 1024, 4, [300], 0.0),
+    (4, 2048, 10, 1, 256, 1024, 0, [64] * 4, 0.0),
+    (8, 512, 4, 1, 64, 256, 0, [512] + [20] * 7, 0.0),
+    (3, 700, 6, 3, 128, 90, 2, [0, 1, 0], 0.0),
+    (2, 300, 2, 2, 64, 300, 0, [0, 0], 0.0),
+]
+
+
+@pytest.mark.parametrize("B,T,Hq,Hkv,dh,W,S,lens,scale", SHORT)
+def test_attention_backward_of_short_sequences(B, T, Hq, Hkv, dh, W, S, lens, scale):
+    test_attention(B, T, Hq, Hkv, dh, W, S, lens, scale)
+    test_attention_backward(B, T, Hq, Hkv, dh, W, S, lens, scale)
+
+
+@pytest.mark.parametrize("B,T,Hq,Hkv,dh,W,S,lens", [
+    (1, 1100, 2, 1, 256, 1024, 4, None), (2, 700, 4, 2, 64, 300, 0, [700, 431]), (1, 600, 3, 1, 128, 1 << 30, 0, None),
+    (1, 513, 4, 1, 128, 64, 1, None), (4, 2048, 2, 1, 128, 1024, 0, [64] * 4)])
+def test_attention_gradients_in_the_norm(B, T, Hq, Hkv, dh, W, S, lens):
+    """The gradients' 2-norm, which a factor in all of them cannot hide in: P, dS, o and the result are rounded to
+    bf16, at most 2^-8 of the value each and in random directions, so together, over thousands of values, below
+    2^-7 of the whole. The rows of dq whose delta comes from o (256 and on, W >= 256) also by themselves."""
+    rng = np.random.default_rng(T + W + 5)
+    q, k, v = packed_qkv(rng, B, T, Hq, Hkv, dh)
+    do = normal(rng, B, T, Hq, dh)
+    dev_lens = None if lens is None else torch.tensor(lens, dtype=torch.int32, device=DEV)
+    o, lse = rg.local_attention(q, k, v, W, S, lens=dev_lens, want_lse=True)
+    got = rg.local_attention_backward(q, k, v, o, lse, do, W, S, dev_lens)
+    refs = ab.attention_backward(num(q), num(k), num(v), num(do), W, S, lens)
+    pairs = [(name, num(got[name]), ref) for name, ref in zip(("dq", "dk", "dv"), refs)]
+    if W >= 256 and T > 256 and (lens is None or max(lens) > 256):
+        pairs.append(("dq beyond row 256", pairs[0][1][:, 256:], refs[0][:, 256:]))
+    for name, a, ref in pairs:
+        rel = np.linalg.norm(a - ref) / np.linalg.norm(ref)
+        print(f"{name}: {rel:.2e}", flush=True)
+        assert rel < 2.0 ** -7, name

@@ -15,6 +15,7 @@
 // Bound by the matrix and vector units in turn: they overlap only across the two or three waves of a SIMD. 96 us
 // at B8 T2048 (ragged) Hq10 dh256 W1024 (670 TFLOP/s), 305 us at T16384 Hq8 Hkv2 dh128 W4096 (790 TFLOP/s).
 #include "rglru_attn.h"
+#include "rglru_grid.h"
 #include "rglru_launch.h"
 
 #include <algorithm>
@@ -91,7 +92,9 @@ __global__ __launch_bounds__(64 * kWg * KS, 2) void attn_fwd(AttnArgs x) {
   const float c = x.scale * kLn2Inv;
   // heavy first: query blocks from the last one down, all (sequence, head) pairs of one together
   const int nbh = x.B * Hq, nqb = (T + kRows - 1) / kRows;
-  const int qi = uni(blockIdx.x / nbh), bh = blockIdx.x - qi * nbh;
+  const int id = block_of(blockIdx.y);
+  const int qi = uni(id / nbh), bh = id - qi * nbh;
+  if (qi >= nqb) return;
   const int q0 = (nqb - 1 - qi) * kRows;
   const int b = uni(bh / Hq), h = bh - b * Hq;
   const int kvh = uni(h / (Hq / x.Hkv));
@@ -341,11 +344,11 @@ namespace {
 // keys then (17.5 us instead of 22 at B3 T1111 Hq6 Hkv2 dh128 W300, 7.3 instead of 8.1 at B1 T101 Hq4 dh64).
 template <int DH> hipError_t launch(const AttnArgs &a, hipStream_t s) {
   constexpr unsigned kCus = 256;
-  const unsigned groups = static_cast<unsigned>((a.T + kOwn - 1) / kOwn) * a.B * a.Hq;
+  const long long groups = static_cast<long long>((a.T + kOwn - 1) / kOwn) * a.B * a.Hq;
   if (groups <= kCus && a.T > kBlk)
-    attn_fwd<DH, 2><<<groups, 64 * kWg * 2, 0, s>>>(a);
+    attn_fwd<DH, 2><<<static_cast<unsigned>(groups), 64 * kWg * 2, 0, s>>>(a);
   else
-    attn_fwd<DH, 1><<<groups, 64 * kWg, 0, s>>>(a);
+    attn_fwd<DH, 1><<<dim3(grid_x(groups), grid_rows(groups)), 64 * kWg, 0, s>>>(a);
   return hipGetLastError();
 }
 

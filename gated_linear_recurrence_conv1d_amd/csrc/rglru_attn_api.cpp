@@ -9,6 +9,7 @@
 
 #include "rglru.h"
 #include "rglru_check.h"
+#include "rglru_grid.h"
 #include "rglru_launch.h"
 
 namespace {
@@ -70,15 +71,17 @@ rglru_status check_attn(int B, int T, int Hq, int Hkv, int dh, long long q_strid
   if (B > 65535 || Hq > 65535) return RGLRU_ERR_UNSUPPORTED;
   if (q_stride > kMaxStride || k_stride > kMaxStride || v_stride > kMaxStride)
     return RGLRU_ERR_UNSUPPORTED;
+  // workgroups of 128 rows, and one more in the backward
+  if ((T + 127LL) / 128 * B * Hq >= rglru::kMaxBlocks) return RGLRU_ERR_UNSUPPORTED;
   // a sequence's k and v stay well within 32-bit byte offsets
   constexpr long long kRange = 1LL << 30;
   if (T * k_stride * 2 > kRange || T * v_stride * 2 > kRange) return RGLRU_ERR_UNSUPPORTED;
   return RGLRU_OK;
 }
 
-// The sum over workgroups' parts has dh / 4 workgroups for each key block: a launch's grid has to hold them.
+// The sum over workgroups' parts has dh / 4 workgroups for each key block.
 bool bwd_grid_ok(int B, int T, int Hkv, int dh) {
-  return (T + 127LL) / 128 * B * Hkv * (dh / 4) <= 0x7FFFFFFF;
+  return (T + 127LL) / 128 * B * Hkv * (dh / 4) <= rglru::kMaxBlocks;
 }
 
 // The kernels' running maximum starts here: below every score that matters, and finite in exp2

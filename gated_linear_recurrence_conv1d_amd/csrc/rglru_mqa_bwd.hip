@@ -26,6 +26,7 @@
 // several workgroups share are summed by attn_dkv_sum, in order, from fp32 parts that lie in the accumulators'
 // order (15 us; 256 shares: with 512, 27 us, and 172-180 us for attn_dkv).
 #include "rglru_attn.h"
+#include "rglru_grid.h"
 #include "rglru_launch.h"
 #include "rglru_shares.h"
 
@@ -85,7 +86,7 @@ template <int DH> struct DqLds {
 };
 
 template <int DH, int SIDE>
-__device__ __forceinline__ void dq_side(const AttnBwdArgs &a, DqLds<DH> &sh, int rt, int lane) {
+__device__ __forceinline__ void dq_side(const AttnBwdArgs &a, DqLds<DH> &sh, int id, int rt, int lane) {
   typedef Blk<DH> K;
   const unsigned lds = lds_addr(sh.blocks);
   const int lrow = lane & 31, half = lane >> 5;
@@ -93,7 +94,7 @@ __device__ __forceinline__ void dq_side(const AttnBwdArgs &a, DqLds<DH> &sh, int
   // heavy first: query blocks from the last one down, all (sequence, head) pairs of one together
   const int nbh = a.B * Hq;
   const int nqb = (T + kOwn - 1) / kOwn;
-  const int qi = uni(blockIdx.x / nbh), bh = blockIdx.x - qi * nbh;
+  const int qi = uni(id / nbh), bh = id - qi * nbh;
   const int q0 = (nqb - 1 - qi) * kOwn;
   const int b = uni(bh / Hq), h = bh - b * Hq;
   const int len = clamp_len(a.lens, b, T);
@@ -311,16 +312,17 @@ __device__ __forceinline__ void plan_items(const AttnBwdArgs &a) {
 template <int DH>
 __global__ __launch_bounds__(64 * 2 * kWg, 2) void attn_dq(AttnBwdArgs a) {
   __shared__ DqLds<DH> sh;
-  if (blockIdx.x == gridDim.x - 1) {
-    plan_items(a);
+  const int id = block_of(blockIdx.y), last = (a.T + kOwn - 1) / kOwn * a.B * a.Hq;
+  if (id >= last) {
+    if (id == last) plan_items(a);
     return;
   }
   const int w = uni(threadIdx.x >> 6), lane = threadIdx.x & 63;
   // both sides pass the same number of barriers
   if (w < kWg)
-    dq_side<DH, 0>(a, sh, w, lane);
+    dq_side<DH, 0>(a, sh, id, w, lane);
   else
-    dq_side<DH, 1>(a, sh, w - kWg, lane);
+    dq_side<DH, 1>(a, sh, id, w - kWg, lane);
 }
 
 // Workgroup = 128 keys, 8 waves: wave (kt, side) has keys 32 kt.. . Side 0 holds k (B operands) and
@@ -520,7 +522,9 @@ __global__ __launch_bounds__(64 * 2 * kWg, 2) void attn_dkv(AttnBwdArgs a) {
 // without items. Grid: DH / 4 workgroups for each of span's entries; a lane has four values of a row.
 template <int DH> __global__ __launch_bounds__(256) void attn_dkv_sum(AttnBwdArgs a) {
   constexpr int kPer = DH / 8;  // workgroups for dV, then as many for dK
-  const int i = uni(blockIdx.x / (2 * kPer)), sub = blockIdx.x - i * 2 * kPer;
+  const int id = block_of(blockIdx.y), i = uni(id / (2 * kPer)), sub = id - i * 2 * kPer;
+  const int nkb = (a.T + kOwn - 1) / kOwn, n = a.B * nkb;
+  if (i >= n * a.Hkv) return;
   const int side = sub / kPer, unit = (sub - side * kPer) * 256 + threadIdx.x;  // of 32 DH
   const int2 span = {uniform_load(&a.span[i].x, 0), uniform_load(&a.span[i].y, 0)};
   if (span.x >= 0 && span.x == span.y) return;  // stored by attn_dkv
@@ -540,7 +544,6 @@ template <int DH> __global__ __launch_bounds__(256) void attn_dkv_sum(AttnBwdArg
         if (w0 + j <= span.y) acc += x[j];
     }
   }
-  const int nkb = (a.T + kOwn - 1) / kOwn, n = a.B * nkb;
   const int kvh = uni(i / n), e = i - kvh * n, b = uni(e / nkb), kb = e - b * nkb;
   const int kt = unit / (8 * DH), r = unit - kt * 8 * DH, lane = r & 63;  // r: (4 j + g) 64 + lane
   const int t = kb * kOwn + 32 * kt + (lane & 31);
@@ -568,14 +571,14 @@ AttnBwdPlan attn_bwd_plan(int B, int T, int Hq, int Hkv, int window, int sinks) 
 namespace {
 
 template <int DH> hipError_t launch(const AttnBwdArgs &a, hipStream_t s) {
-  const unsigned nq = static_cast<unsigned>((a.T + kOwn - 1) / kOwn);
-  attn_dq<DH><<<nq * a.B * a.Hq + 1, 64 * 2 * kWg, 0, s>>>(a);
+  const long long nq = (a.T + kOwn - 1) / kOwn, dq = nq * a.B * a.Hq + 1, sum = nq * a.B * a.Hkv * (DH / 4);
+  attn_dq<DH><<<dim3(grid_x(dq), grid_rows(dq)), 64 * 2 * kWg, 0, s>>>(a);
   hipError_t e = hipGetLastError();
   if (e != hipSuccess) return e;
   attn_dkv<DH><<<static_cast<unsigned>(a.groups), 64 * 2 * kWg, 0, s>>>(a);
   e = hipGetLastError();
   if (e != hipSuccess) return e;
-  attn_dkv_sum<DH><<<nq * a.B * a.Hkv * (DH / 4), 256, 0, s>>>(a);
+  attn_dkv_sum<DH><<<dim3(grid_x(sum), grid_rows(sum)), 256, 0, s>>>(a);
   return hipGetLastError();
 }
 

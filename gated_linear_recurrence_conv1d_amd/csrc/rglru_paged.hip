@@ -26,6 +26,7 @@
 //
 // N4 Hq8 Hkv2 dh128 to 131k tokens: 401 MB in 77 us (5.2 TB/s, a plain copy's rate); N128 Hq16 dh256 W2048:
 // 224 MB in 52 us and 5 us of joining.
+#include "rglru_grid.h"
 #include "rglru_launch.h"
 #include "rglru_loads.h"
 #include "rglru_mfma.h"
@@ -85,7 +86,8 @@ __global__ __launch_bounds__(64 * kPgWaves, 2) void paged_fwd(PagedArgs a, int c
   const int lane = threadIdx.x & 63;
   const int w = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int c16 = lane & 15, g = lane >> 4;
-  const int n = blockIdx.x / splits, sp = blockIdx.x - n * splits;
+  const int id = block_of(blockIdx.z), n = id / splits, sp = id - n * splits;
+  if (n >= a.N) return;
   const int G = a.Hq / a.Hkv, gt = (G + 15) / 16;
   const int kvh = blockIdx.y / gt;
   const int h0 = (blockIdx.y - kvh * gt) * 16;  // first head of the group's part
@@ -442,13 +444,15 @@ namespace {
 
 template <typename T, int DH> hipError_t launch(const PagedArgs &a, const PagedPlan &p, hipStream_t s) {
   const int G = a.Hq / a.Hkv;
-  const dim3 grid(static_cast<unsigned>(a.N) * p.splits, a.Hkv * ((G + 15) / 16));
+  const long long cols = static_cast<long long>(a.N) * p.splits;
+  const dim3 grid(grid_x(cols), a.Hkv * ((G + 15) / 16), grid_rows(cols));
   if (a.page % 16 == 0)
     paged_fwd<T, DH, true><<<grid, 64 * kPgWaves, 0, s>>>(a, p.chunk, p.splits);
   else
     paged_fwd<T, DH, false><<<grid, 64 * kPgWaves, 0, s>>>(a, p.chunk, p.splits);
   const hipError_t e = hipGetLastError();
   if (e != hipSuccess || p.splits == 1) return e;
+  // (rows are split only where they are few: N * Hq is at most 16 * 512, see paged_plan)
   paged_join<T, DH><<<static_cast<unsigned>(a.N) * a.Hq, 256, 0, s>>>(a, p.chunk, p.splits);
   return hipGetLastError();
 }

@@ -285,3 +285,15 @@ def test_binding_refuses_by_argument():
     # a window that no integer of the entry point holds is the widest one; here the device is what is wrong
     with pytest.raises(ValueError, match="device"):
         rg.rglru_local_attention(q, k, k, q, 1 << 70)
+
+
+def test_attention_grid_limit():
+    """65535 sequences of 16384 heads: their blocks of 128 rows have numbers below 2^31 - 1 up to 256 tokens (the call
+    then ends at its missing output), and are refused beyond, with nothing launched."""
+    wide = dict(B=65535, Hq=16384, Hkv=1, dh=64, q_stride=1 << 20, k_stride=64, v_stride=64)
+    assert attn(T=256, o=None, **wide) == BAD
+    assert attn(T=257, **wide) == UNSUP
+    assert attn_bwd(T=256, lse=None, dq_stride=1 << 20, dk_stride=64, dv_stride=64, **wide) == BAD
+    assert attn_bwd(T=257, dq_stride=1 << 20, dk_stride=64, dv_stride=64, **wide) == UNSUP
+    assert rg.rglru_local_attention_backward_workspace_size(65535, 257, 16384, 1, 64, 16) == 0
+    assert rg.rglru_local_attention_backward_workspace_size(65535, 256, 16384, 1, 64, 16) > 0

@@ -666,3 +666,30 @@ def test_attention_gradients_in_the_norm(B, T, Hq, Hkv, dh, W, S, lens):
         rel = np.linalg.norm(a - ref) / np.linalg.norm(ref)
         print(f"{name}: {rel:.2e}", flush=True)
         assert rel < 2.0 ** -7, name
+
+
+def test_attention_of_more_threads_than_a_dimension_holds():
+    """Single tokens of 65535 sequences and 264 heads: 17.3 million workgroups of the forward (256 threads) and of
+    dq (512), 277 million of the sum, where one dimension of a launch holds 2^32 threads. A token that sees itself
+    alone gives o = v, lse = its score, dv = do and no other gradient, exactly."""
+    B, H, dh = 65535, 264, 64
+    gen = torch.Generator(device=DEV).manual_seed(1)
+    q, k, v, do = (torch.randn(B, 1, H, dh, generator=gen, device=DEV, dtype=BF) for _ in range(4))
+    o, lse = rg.local_attention(q, k, v, 5, want_lse=True)
+    assert torch.equal(o, v)
+    score = torch.stack([(q[b].float() * k[b].float()).sum(-1) / 8 for b in (0, B // 2, B - 1)]).squeeze(1)
+    assert torch.allclose(lse[[0, B // 2, B - 1], :, 0], score, rtol=0, atol=(dh + 4) * W24 * 64)
+    g = rg.local_attention_backward(q, k, v, o, lse, do, 5)
+    assert torch.equal(g["dv"], do)
+    assert not g["dq"].any() and not g["dk"].any()
+
+
+def test_paged_attention_of_more_threads_than_a_dimension_holds():
+    """2^24 + 3 sequences of one cached token each: o is its value."""
+    N, dh, page = (1 << 24) + 3, 64, 16
+    gen = torch.Generator(device=DEV).manual_seed(2)
+    q = torch.randn(N, 1, dh, generator=gen, device=DEV, dtype=BF)
+    kp, vp = (torch.randn(64, page, 1, dh, generator=gen, device=DEV, dtype=BF) for _ in range(2))
+    table = torch.randint(0, 64, (N, 1), generator=gen, device=DEV, dtype=torch.int32)
+    got = rg.paged_attention(q, kp, vp, table, torch.ones(N, dtype=torch.int32, device=DEV), 100)
+    assert torch.equal(got, vp[:, 0][table[:, 0].long()])

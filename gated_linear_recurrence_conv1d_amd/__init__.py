@@ -391,32 +391,50 @@ def rglru_backward(x, conv_w, W_a, b_a, W_x, b_x, Lambda, h0, y, dy, dh_T, dx, d
 # ---- the local attention block's operators. Tensors of heads are [..., H, dh] with the heads of a
 # token contiguous and one stride from token to token, so slices of a packed projection need no
 # copy. All tensors of a call live on one device, which need not be the current one; the call runs on
-# `stream`, else on that device's current stream.
+# `stream` (a torch stream or a stream's number), else on that device's current stream. What a call makes
+# belongs to the stream it runs on, and may be used on the one that was current, once that waits for it; the
+# tensors it is given have to be ready on that stream, and to live until it is done with them.
 _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (
     lambda index: torch.cuda.current_stream(index).cuda_stream)
 _current_device = getattr(torch._C, "_cuda_getDevice", None) or torch.cuda.current_device
 
 
-def _call(where, fn, q, stream, keep, *args):
-    """fn(*args, stream), which checks its tensors (csrc/rglru_torch.cpp), on q's device; `keep`: tensors
-    allocated for it here."""
+def _as_stream(stream, q):
+    """A stream of q's device, or its number, as a torch stream."""
+    index = q.get_device()
+    if not isinstance(stream, torch.cuda.Stream):
+        return (torch.cuda.ExternalStream(int(stream), device=index) if int(stream) else
+                torch.cuda.default_stream(index))  # (0 would be a new one)
+    if stream.device_index != index:
+        raise ValueError(f"stream: on {stream.device}, q on {q.device}")
+    return stream
+
+
+def _on(stream, q, f):
+    """f() with `stream` current, so that what f allocates comes from that stream's pool: a block of the pool of
+    the stream that is current now may still be in use there, by work queued before it was freed. The results
+    are recorded on that stream, as the caller may use them there."""
+    if not isinstance(q, torch.Tensor) or not q.is_cuda:
+        return f()  # refused there
+    stream, here = _as_stream(stream, q), torch.cuda.current_stream(q.device)
+    with torch.cuda.stream(stream):
+        out = f()
+    if stream != here:
+        for t in out.values() if isinstance(out, dict) else out if isinstance(out, tuple) else (out,):
+            if t is not None:
+                t.record_stream(here)
+    return out
+
+
+def _call(where, fn, q, stream, *args):
+    """fn(*args, stream), which checks its tensors (csrc/rglru_torch.cpp), on q's device."""
     if not isinstance(q, torch.Tensor):
         raise TypeError("q: expected a torch.Tensor")
     index = q.get_device()
     if index < 0:
         status = fn(*args, 0)  # refused there, by what is wrong with the tensors
     else:
-        if stream is None:
-            s = _raw_stream(index)
-        else:
-            if not isinstance(stream, torch.cuda.Stream):
-                stream = (torch.cuda.ExternalStream(int(stream), device=index) if int(stream) else
-                          torch.cuda.default_stream(index))  # (0 would be a new one)
-            elif stream.device_index != index:
-                raise ValueError(f"stream: on {stream.device}, q on {q.device}")
-            for t in keep:  # from the current stream's pool: not reused before this stream is done
-                t.record_stream(stream)
-            s = stream.cuda_stream
+        s = _raw_stream(index) if stream is None else _as_stream(stream, q).cuda_stream
         if index == _current_device():  # a tensor lives there: the runtime is up
             status = fn(*args, s)
         else:
@@ -432,25 +450,23 @@ def _int32(n):
 
 
 def rglru_qk_norm_rope(q, k, positions, inv_freq, q_out, k_out, q_w=None, k_w=None, eps=1e-6,
-                       v=None, k_pages=None, v_pages=None, slots=None, stream=None, _keep=()):
+                       v=None, k_pages=None, v_pages=None, slots=None, stream=None):
     """q [..., Hq, dh], k, v [..., Hkv, dh]; positions int32 and slots int64 [...]; inv_freq f32
     [rot / 2]; k_pages, v_pages [pages, page, Hkv, dh]. k_out may be None with slots."""
-    _call("rglru_qk_norm_rope", _ext.qk_norm_rope, q, stream, _keep, q, k, v, q_w, k_w, inv_freq,
+    _call("rglru_qk_norm_rope", _ext.qk_norm_rope, q, stream, q, k, v, q_w, k_w, inv_freq,
           positions, slots, q_out, k_out, k_pages, v_pages, eps)
 
 
 def qk_norm_rope(q, k, positions, inv_freq, q_w=None, k_w=None, eps=1e-6, v=None, k_pages=None,
                  v_pages=None, slots=None, q_out=None, k_out=None, stream=None):
     """Returns (q_out, k_out), new contiguous tensors unless given (q and k themselves: in place)."""
-    new = []
-    if q_out is None:
-        q_out = _ext.empty_as(q)
-        new.append(q_out)
-    if k_out is None:
-        k_out = _ext.empty_as(k)
-        new.append(k_out)
+    if stream is not None:
+        return _on(stream, q, lambda: qk_norm_rope(q, k, positions, inv_freq, q_w, k_w, eps, v, k_pages,
+                                                   v_pages, slots, q_out, k_out))
+    q_out = _ext.empty_as(q) if q_out is None else q_out
+    k_out = _ext.empty_as(k) if k_out is None else k_out
     rglru_qk_norm_rope(q, k, positions, inv_freq, q_out, k_out, q_w, k_w, eps, v, k_pages, v_pages,
-                       slots, stream, _keep=new)
+                       slots)
     return q_out, k_out
 
 
@@ -460,21 +476,22 @@ def rglru_qk_norm_rope_backward_workspace_size(rows, dh) -> int:
 
 def rglru_qk_norm_rope_backward(q, k, positions, inv_freq, dq_out, dk_out, dq, dk, q_w=None,
                                 k_w=None, dq_w=None, dk_w=None, eps=1e-6, workspace=None,
-                                stream=None, _keep=()):
-    _call("rglru_qk_norm_rope_backward", _ext.qk_norm_rope_backward, q, stream, _keep, q, k, q_w, k_w,
-          inv_freq, positions, dq_out, dk_out, dq, dk, dq_w, dk_w, eps, workspace)
+                                stream=None):
+    _call("rglru_qk_norm_rope_backward", _ext.qk_norm_rope_backward, q, stream, q, k, q_w, k_w, inv_freq,
+          positions, dq_out, dk_out, dq, dk, dq_w, dk_w, eps, workspace)
 
 
 def qk_norm_rope_backward(q, k, positions, inv_freq, dq_out, dk_out, q_w=None, k_w=None, eps=1e-6,
                           dq=None, dk=None, workspace=None, stream=None):
     """Returns a dict with dq, dk (new contiguous tensors unless given) and fp32 dq_w, dk_w [dh]
     (None without weights)."""
+    if stream is not None:
+        return _on(stream, q, lambda: qk_norm_rope_backward(q, k, positions, inv_freq, dq_out, dk_out, q_w,
+                                                            k_w, eps, dq, dk, workspace))
     dev, dh = q.device, q.shape[-1]
-    new = []
 
     def empty(shape, dtype):
-        new.append(torch.empty(shape, dtype=dtype, device=dev))
-        return new[-1]
+        return torch.empty(shape, dtype=dtype, device=dev)
 
     dq = empty(q.shape, q.dtype) if dq is None else dq
     dk = empty(k.shape, k.dtype) if dk is None else dk
@@ -485,27 +502,27 @@ def qk_norm_rope_backward(q, k, positions, inv_freq, dq_out, dk_out, q_w=None, k
             workspace = empty((rglru_qk_norm_rope_backward_workspace_size(positions.numel(), dh),),
                               torch.uint8)
     rglru_qk_norm_rope_backward(q, k, positions, inv_freq, dq_out, dk_out, dq, dk, q_w, k_w, dq_w,
-                                dk_w, eps, workspace, stream, _keep=new)
+                                dk_w, eps, workspace)
     return {"dq": dq, "dk": dk, "dq_w": dq_w, "dk_w": dk_w}
 
 
-def rglru_local_attention(q, k, v, o, window, sinks=0, lens=None, scale=0.0, lse=None, stream=None,
-                          _keep=()):
+def rglru_local_attention(q, k, v, o, window, sinks=0, lens=None, scale=0.0, lse=None, stream=None):
     """q [B,T,Hq,dh], k, v [B,T,Hkv,dh], o as q and contiguous, bf16; lens int32 [B]; lse f32
     [B,Hq,T]."""
-    _call("rglru_local_attention", _ext.local_attention, q, stream, _keep, q, k, v, lens, o, lse,
+    _call("rglru_local_attention", _ext.local_attention, q, stream, q, k, v, lens, o, lse,
           window, sinks, scale)
 
 
 def local_attention(q, k, v, window, sinks=0, lens=None, scale=0.0, want_lse=False, stream=None):
     """Returns o [B,T,Hq,dh] (bf16), or (o, lse) with lse f32 [B,Hq,T], which the backward needs."""
-    new = [_ext.empty_as(q)]
+    if stream is not None:
+        return _on(stream, q, lambda: local_attention(q, k, v, window, sinks, lens, scale, want_lse))
+    o, lse = _ext.empty_as(q), None
     if want_lse:
         B, T, Hq, _ = q.shape
-        new.append(torch.empty((B, Hq, T), dtype=torch.float32, device=q.device))
-    rglru_local_attention(q, k, v, new[0], window, sinks, lens, scale, new[1] if want_lse else None,
-                          stream, _keep=new)
-    return tuple(new) if want_lse else new[0]
+        lse = torch.empty((B, Hq, T), dtype=torch.float32, device=q.device)
+    rglru_local_attention(q, k, v, o, window, sinks, lens, scale, lse)
+    return (o, lse) if want_lse else o
 
 
 def rglru_local_attention_backward_workspace_size(B, T, Hq, Hkv, dh, window, sinks=0) -> int:
@@ -514,9 +531,9 @@ def rglru_local_attention_backward_workspace_size(B, T, Hq, Hkv, dh, window, sin
 
 
 def rglru_local_attention_backward(q, k, v, o, lse, do, dq, dk, dv, window, sinks=0, lens=None,
-                                   scale=0.0, workspace=None, stream=None, _keep=()):
+                                   scale=0.0, workspace=None, stream=None):
     """o, do as q and contiguous; dq as q, dk and dv as k (slices of a packed gradient are fine)."""
-    _call("rglru_local_attention_backward", _ext.local_attention_backward, q, stream, _keep, q, k, v,
+    _call("rglru_local_attention_backward", _ext.local_attention_backward, q, stream, q, k, v,
           lens, o, lse, do, dq, dk, dv, window, sinks, scale, workspace)
 
 
@@ -524,11 +541,12 @@ def local_attention_backward(q, k, v, o, lse, do, window, sinks=0, lens=None, sc
                              dk=None, dv=None, workspace=None, stream=None):
     """Gradients through local_attention(.., want_lse=True). Returns a dict with dq, dk, dv (bf16;
     new contiguous tensors unless given)."""
-    new = []
+    if stream is not None:
+        return _on(stream, q, lambda: local_attention_backward(q, k, v, o, lse, do, window, sinks, lens, scale,
+                                                               dq, dk, dv, workspace))
 
     def empty(shape, dtype):
-        new.append(torch.empty(shape, dtype=dtype, device=q.device))
-        return new[-1]
+        return torch.empty(shape, dtype=dtype, device=q.device)
 
     dq = empty(q.shape, q.dtype) if dq is None else dq
     dk = empty(k.shape, k.dtype) if dk is None else dk
@@ -538,7 +556,7 @@ def local_attention_backward(q, k, v, o, lse, do, window, sinks=0, lens=None, sc
                                                           window, sinks)
         workspace = empty((n,), torch.uint8)
     rglru_local_attention_backward(q, k, v, o, lse, do, dq, dk, dv, window, sinks, lens, scale,
-                                   workspace, stream, _keep=new)
+                                   workspace)
     return {"dq": dq, "dk": dk, "dv": dv}
 
 
@@ -551,17 +569,20 @@ def rglru_paged_attention_workspace_size(N, Hq, Hkv, dh, page_size, max_pages, w
 
 
 def rglru_paged_attention(q, k_pages, v_pages, block_table, lens, o, window, sinks=0, scale=0.0,
-                          workspace=None, stream=None, _keep=()):
+                          workspace=None, stream=None):
     """q [N,Hq,dh], k_pages, v_pages [pages,page,Hkv,dh] of one type (bf16 or f32); block_table
     int32 [N,max_pages], lens int32 [N]; o as q and contiguous."""
-    _call("rglru_paged_attention", _ext.paged_attention, q, stream, _keep, q, k_pages, v_pages,
+    _call("rglru_paged_attention", _ext.paged_attention, q, stream, q, k_pages, v_pages,
           block_table, lens, o, window, sinks, scale, workspace)
 
 
 def paged_attention(q, k_pages, v_pages, block_table, lens, window, sinks=0, scale=0.0,
                     workspace=None, stream=None):
     """Returns o [N,Hq,dh] of q's type."""
-    new = [_ext.empty_as(q)]
+    if stream is not None:
+        return _on(stream, q, lambda: paged_attention(q, k_pages, v_pages, block_table, lens, window, sinks,
+                                                      scale, workspace))
+    o = _ext.empty_as(q)
     if workspace is None and q.dim() == 3 and k_pages.dim() == 4 and block_table.dim() == 2:
         N, Hq, dh = q.shape
         _, page, Hkv, _ = k_pages.shape
@@ -569,10 +590,8 @@ def paged_attention(q, k_pages, v_pages, block_table, lens, window, sinks=0, sca
                                                  sinks, q.dtype)
         if n:
             workspace = _ext.empty_bytes(q, n)
-            new.append(workspace)
-    rglru_paged_attention(q, k_pages, v_pages, block_table, lens, new[0], window, sinks, scale,
-                          workspace, stream, _keep=new)
-    return new[0]
+    rglru_paged_attention(q, k_pages, v_pages, block_table, lens, o, window, sinks, scale, workspace)
+    return o
 
 
 # ---- convenience wrappers (allocate outputs with torch, then call the entry points above) ----

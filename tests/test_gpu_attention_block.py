@@ -693,3 +693,82 @@ def test_paged_attention_of_more_threads_than_a_dimension_holds():
     table = torch.randint(0, 64, (N, 1), generator=gen, device=DEV, dtype=torch.int32)
     got = rg.paged_attention(q, kp, vp, table, torch.ones(N, dtype=torch.int32, device=DEV), 100)
     assert torch.equal(got, vp[:, 0][table[:, 0].long()])
+
+
+def calls_that_allocate(rng):
+    """(name, call taking a stream) for each function that makes its outputs and workspaces, and its inputs."""
+    B, T, Hq, Hkv, dh = 2, 300, 4, 2, 128
+    q, k, v = packed_qkv(rng, B, T, Hq, Hkv, dh)
+    do, w = normal(rng, B, T, Hq, dh), 1 + 0.1 * normal(rng, dh, dtype=F32)
+    pos, freq = torch.arange(B * T, device=DEV, dtype=torch.int32).view(B, T), torch.rand(32, device=DEV)
+    o, lse = rg.local_attention(q, k, v, 70, 3, want_lse=True)
+    pq, kp, vp, table, dl = paged_inputs(rng, BF, [900, 1, 33], Hq, Hkv, dh, 16)
+    return [
+        ("norm_rope", lambda s: rg.qk_norm_rope(q, k, pos, freq, w, w, stream=s)),
+        ("norm_rope_backward", lambda s: rg.qk_norm_rope_backward(q, k, pos, freq, do, k, w, w, stream=s)),
+        ("attention", lambda s: rg.local_attention(q, k, v, 70, 3, want_lse=True, stream=s)),
+        ("attention_backward", lambda s: rg.local_attention_backward(q, k, v, o, lse, do, 70, 3, stream=s)),
+        ("paged_attention", lambda s: rg.paged_attention(pq, kp, vp, table, dl, 1 << 30, stream=s)),
+    ]
+
+
+def tensors(out):
+    return list(out.values()) if isinstance(out, dict) else list(out) if isinstance(out, tuple) else [out]
+
+
+def test_given_stream_owns_what_is_made_for_it(monkeypatch):
+    """Outputs and workspaces come from the given stream's pool."""
+    calls = calls_that_allocate(np.random.default_rng(41))
+    side, real = torch.cuda.Stream(), rg._call
+    side.wait_stream(torch.cuda.current_stream())
+
+    def pool_of(t):
+        at = t.data_ptr()
+        return [s["stream"] for s in torch.cuda.memory_snapshot() if s["address"] <= at < s["address"] + s["total_size"]]
+
+    for name, call in calls:
+        want, made = tensors(call(None)), []
+
+        def spy(where, fn, q, stream, *args):
+            at = [(a, pool_of(a)) for a in args if isinstance(a, torch.Tensor)]
+            made.extend(p for _, p in at if p == [side.cuda_stream])
+            return real(where, fn, q, stream, *args)
+
+        monkeypatch.setattr(rg, "_call", spy)
+        for given in (side, side.cuda_stream):
+            made.clear()
+            got = tensors(call(given))
+            torch.cuda.synchronize()
+            assert all(pool_of(t) == [side.cuda_stream] for t in got), name
+            assert len(made) == len(got) + (name in ("norm_rope_backward", "attention_backward", "paged_attention")), name
+            assert all(torch.equal(a, b) for a, b in zip(got, want)), name
+        monkeypatch.setattr(rg, "_call", real)
+
+
+def test_given_stream_beside_a_busy_one():
+    """The current stream still has to fill memory that it has given back; what a call on another stream makes lies
+    elsewhere, and what it made is not reused before the current stream has read it."""
+    side = torch.cuda.Stream()
+    for name, call in calls_that_allocate(np.random.default_rng(42)):
+        want = [t.clone() for t in tensors(call(None))]
+        sizes = [(t.shape, t.dtype) for t in want]
+        torch.cuda.synchronize()
+        torch.cuda.empty_cache()
+        old = [torch.empty(s, dtype=d, device=DEV) for s, d in sizes]
+        torch.cuda._sleep(20_000_000)
+        for t in old:
+            t.fill_(float("nan"))
+        del old, t
+        got = tensors(call(side))
+        side.synchronize()
+        torch.cuda.synchronize()
+        assert all(torch.equal(a, b) for a, b in zip(got, want)), name
+        # read by the current stream, then given back and overwritten on the side stream
+        torch.cuda._sleep(20_000_000)
+        kept = [t.clone() for t in got]
+        del got
+        with torch.cuda.stream(side):
+            new = [torch.full(s, float("nan"), dtype=d, device=DEV) for s, d in sizes]
+        torch.cuda.synchronize()
+        assert all(torch.equal(a, b) for a, b in zip(kept, want)), name
+        del new

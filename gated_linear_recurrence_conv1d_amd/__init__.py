@@ -169,6 +169,33 @@ def _stream(stream):
     return int(stream)
 
 
+def _as_stream(stream, t):
+    """A stream of t's device, or its number, as a torch stream."""
+    index = t.get_device()
+    if not isinstance(stream, torch.cuda.Stream):
+        return (torch.cuda.ExternalStream(int(stream), device=index) if int(stream) else
+                torch.cuda.default_stream(index))  # (0 would be a new one)
+    if stream.device_index != index:
+        raise ValueError(f"stream: on {stream.device}, expected {t.device}")
+    return stream
+
+
+def _on(stream, t, f):
+    """f() with `stream` current, so that what f allocates comes from that stream's pool: a block of the pool of
+    the stream that is current now may still be in use there, by work queued before it was freed. The results
+    are recorded on the one that is current now, where the caller may use them."""
+    if not isinstance(t, torch.Tensor) or not t.is_cuda:
+        return f()  # refused there
+    stream, here = _as_stream(stream, t), torch.cuda.current_stream(t.device)
+    with torch.cuda.stream(stream):
+        out = f()
+    if stream != here:
+        for x in out.values() if isinstance(out, dict) else out if isinstance(out, tuple) else (out,):
+            if x is not None:
+                x.record_stream(here)
+    return out
+
+
 def _check(status, where):
     if status != RGLRU_OK:
         raise RglruError(status, where)
@@ -332,9 +359,11 @@ def rglru_prefill_state(x, conv_state, stream=None):
 
 def prefill_state(x, stream=None):
     """A new conv-state tensor [B,3,D] for continuing x [B,T,D] with decode steps."""
+    if stream is not None:
+        return _on(stream, x, lambda: prefill_state(x))
     B, T, D = x.shape
     cs = torch.empty((B, 3, D), dtype=x.dtype, device=x.device)
-    rglru_prefill_state(x, cs, stream)
+    rglru_prefill_state(x, cs)
     return cs
 
 
@@ -354,8 +383,10 @@ def rglru_local_mqa(q, k, v, o, window, scale=0.0, stream=None):
 
 def local_mqa(q, k, v, window, scale=0.0, stream=None):
     """Returns o [B,T,Hq,dh] (bf16)."""
+    if stream is not None:
+        return _on(stream, q, lambda: local_mqa(q, k, v, window, scale))
     o = torch.empty_like(q)
-    rglru_local_mqa(q, k, v, o, window, scale, stream)
+    rglru_local_mqa(q, k, v, o, window, scale)
     return o
 
 
@@ -397,33 +428,6 @@ def rglru_backward(x, conv_w, W_a, b_a, W_x, b_x, Lambda, h0, y, dy, dh_T, dx, d
 _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (
     lambda index: torch.cuda.current_stream(index).cuda_stream)
 _current_device = getattr(torch._C, "_cuda_getDevice", None) or torch.cuda.current_device
-
-
-def _as_stream(stream, q):
-    """A stream of q's device, or its number, as a torch stream."""
-    index = q.get_device()
-    if not isinstance(stream, torch.cuda.Stream):
-        return (torch.cuda.ExternalStream(int(stream), device=index) if int(stream) else
-                torch.cuda.default_stream(index))  # (0 would be a new one)
-    if stream.device_index != index:
-        raise ValueError(f"stream: on {stream.device}, q on {q.device}")
-    return stream
-
-
-def _on(stream, q, f):
-    """f() with `stream` current, so that what f allocates comes from that stream's pool: a block of the pool of
-    the stream that is current now may still be in use there, by work queued before it was freed. The results
-    are recorded on that stream, as the caller may use them there."""
-    if not isinstance(q, torch.Tensor) or not q.is_cuda:
-        return f()  # refused there
-    stream, here = _as_stream(stream, q), torch.cuda.current_stream(q.device)
-    with torch.cuda.stream(stream):
-        out = f()
-    if stream != here:
-        for t in out.values() if isinstance(out, dict) else out if isinstance(out, tuple) else (out,):
-            if t is not None:
-                t.record_stream(here)
-    return out
 
 
 def _call(where, fn, q, stream, *args):
@@ -606,6 +610,9 @@ def pre_buffer(x):
 def forward(x, conv_w, W_a, b_a, W_x, b_x, Lambda, h0=None, plan="auto", chunk_len=0,
             workspace=None, stream=None):
     """Returns (y, h_T)."""
+    if stream is not None:
+        return _on(stream, x, lambda: forward(x, conv_w, W_a, b_a, W_x, b_x, Lambda, h0, plan, chunk_len,
+                                              workspace))
     B, T, D = x.shape
     H = W_a.shape[0]
     y = torch.empty_like(x)
@@ -617,14 +624,16 @@ def forward(x, conv_w, W_a, b_a, W_x, b_x, Lambda, h0=None, plan="auto", chunk_l
                              "rglru_forward_workspace_size_planned")
         workspace = torch.empty(n, dtype=torch.uint8, device=x.device)
     rglru_forward_planned(x, conv_w, W_a, b_a, W_x, b_x, Lambda, h0, y, h_T, workspace, plan,
-                          chunk_len, stream)
+                          chunk_len)
     return y, h_T
 
 
 def decode_step(x_t, conv_state, h, conv_w, W_a, b_a, W_x, b_x, Lambda, stream=None):
     """In place on conv_state and h; returns y_t."""
+    if stream is not None:
+        return _on(stream, x_t, lambda: decode_step(x_t, conv_state, h, conv_w, W_a, b_a, W_x, b_x, Lambda))
     y_t = torch.empty_like(x_t)
-    rglru_decode_step(x_t, conv_state, h, y_t, conv_w, W_a, b_a, W_x, b_x, Lambda, stream)
+    rglru_decode_step(x_t, conv_state, h, y_t, conv_w, W_a, b_a, W_x, b_x, Lambda)
     return y_t
 
 
@@ -632,6 +641,9 @@ def backward(x, conv_w, W_a, b_a, W_x, b_x, Lambda, h0, y, dy, dh_T=None, want_d
              workspace=None, stream=None):
     """Gradients through the forward. Returns a dict with dx (x's dtype) and fp32 dconv_w [4,D],
     dW_a, dW_x [H,Dh,Dh], db_a, db_x, dLam [D] and dh0 [B,D] (None unless want_dh0)."""
+    if stream is not None:
+        return _on(stream, x, lambda: backward(x, conv_w, W_a, b_a, W_x, b_x, Lambda, h0, y, dy, dh_T,
+                                               want_dh0, workspace))
     B, T, D = x.shape
     H = W_a.shape[0]
     Dh = D // H
@@ -649,5 +661,5 @@ def backward(x, conv_w, W_a, b_a, W_x, b_x, Lambda, h0, y, dy, dh_T=None, want_d
                                 dtype=torch.uint8, device=dev)
     rglru_backward(x, conv_w, W_a, b_a, W_x, b_x, Lambda, h0, y, dy, dh_T, out["dx"],
                    out["dconv_w"], out["dW_a"], out["db_a"], out["dW_x"], out["db_x"],
-                   out["dLam"], out["dh0"], workspace, stream)
+                   out["dLam"], out["dh0"], workspace)
     return out

@@ -16,7 +16,7 @@
 //   O^T += V^T P^T: S^T leaves lane (head c, group g) with keys 4g..4g+3 of each 16: already the B
 //     operand if V^T takes its k index in that order. For V^T the lane loads 16 bytes of each of
 //     those 8 key rows (values 8c..8c+7); operand e (value 8c + e of the 8 keys) is put together with
-//     byte permutes, 4 for 8 keys. Output tile e then has O's values 8c + e.
+//     byte permutes, 4 for 8 keys. Output tile e then has O's values 8c + e. P enters as bf16 hi + lo.
 //   fp32 uses the 16x16x4 fp32 instruction: the same layouts with one value a lane, no permutes.
 // K of the next tile is loaded when S has used up this tile's, V after O has: one of them is
 // always in flight.
@@ -54,6 +54,9 @@ template <typename T, int DH> struct Paged {
   static constexpr int kVW = kE * static_cast<int>(sizeof(T)) / 4;  // 32-bit words per V load
   static constexpr int kOT = DH / 16;                // O^T tiles
   static constexpr int kLdO = DH + 1;                // LDS row of O (one word against conflicts)
+  // q from LDS, tile by tile, where registers do not hold it beside K, V and O: what is spilled is read back behind the
+  // loads in flight (N128 Hq16 dh256 W2048: 65 us with 9 spilled registers)
+  static constexpr bool kQLds = DH == 256;
 };
 
 // Tiles a row has to walk: first those that hold sinks before the window's first tile, then the
@@ -80,9 +83,11 @@ template <int KEYS> __host__ __device__ inline Walk walk_of(int len, int W, int 
 template <typename T, int DH, bool UNI>
 __global__ __launch_bounds__(64 * kPgWaves, 2) void paged_fwd(PagedArgs a, int chunk, int splits) {
   typedef Paged<T, DH> M;
-  __shared__ float so[kPgWaves][16][M::kLdO];
+  __shared__ __attribute__((aligned(16))) float so[kPgWaves][16][M::kLdO];
   __shared__ float sm[kPgWaves][16], sl[kPgWaves][16];
   __shared__ int sbad[kPgWaves];
+  u32x4_t(*const sq)[64] = reinterpret_cast<u32x4_t(*)[64]>(so);  // q lies there until the waves are joined
+  static_assert(!M::kQLds || M::kKS * 64 * sizeof(u32x4_t) <= sizeof(so), "room for q");
   const int lane = threadIdx.x & 63;
   const int w = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int c16 = lane & 15, g = lane >> 4;
@@ -105,12 +110,21 @@ __global__ __launch_bounds__(64 * kPgWaves, 2) void paged_fwd(PagedArgs a, int c
   const char *vp = static_cast<const char *>(a.v_pages) + static_cast<size_t>(kvh) * DH * sizeof(T);
 
   // Q^T operand: head column c16 (heads past the group read the last one; never stored)
-  u32x4_t qf[M::kKS];
+  u32x4_t qf[M::kQLds ? 1 : M::kKS];
   {
     const T *qp = static_cast<const T *>(a.q) + static_cast<size_t>(n) * a.q_stride +
                   static_cast<size_t>(hq + min(c16, nh - 1)) * DH + g * (M::kDims / 4);
+    if constexpr (M::kQLds) {
 #pragma unroll
-    for (int s = 0; s < M::kKS; ++s) qf[s] = *reinterpret_cast<const u32x4_t *>(qp + s * M::kDims);
+      for (int s = 0; s < M::kKS / kPgWaves; ++s) {
+        const int ws = w + kPgWaves * s;
+        sq[ws][lane] = *reinterpret_cast<const u32x4_t *>(qp + ws * M::kDims);
+      }
+      __syncthreads();
+    } else {
+#pragma unroll
+      for (int s = 0; s < M::kKS; ++s) qf[s] = *reinterpret_cast<const u32x4_t *>(qp + s * M::kDims);
+    }
   }
   f32x4_t oacc[M::kOT];
 #pragma unroll
@@ -218,21 +232,24 @@ __global__ __launch_bounds__(64 * kPgWaves, 2) void paged_fwd(PagedArgs a, int c
       f32x4_t s[M::kSub];
 #pragma unroll
       for (int j = 0; j < M::kSub; ++j) s[j] = f32x4_t{};
+      int ql = lane;
+      asm volatile("" : "+v"(ql));  // read in every tile: kept, q would take registers again
 #pragma unroll
-      for (int d = 0; d < M::kKS; ++d)
+      for (int d = 0; d < M::kKS; ++d) {
+        const u32x4_t qd = M::kQLds ? sq[d][ql] : qf[M::kQLds ? 0 : d];
 #pragma unroll
         for (int j = 0; j < M::kSub; ++j) {
           if constexpr (M::kHalf) {
             s[j] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8_t, kf[j][d]),
-                                                           __builtin_bit_cast(bf16x8_t, qf[d]), s[j],
-                                                           0, 0, 0);
+                                                           __builtin_bit_cast(bf16x8_t, qd), s[j], 0, 0, 0);
           } else {
 #pragma unroll
             for (int e = 0; e < 4; ++e)
               s[j] = __builtin_amdgcn_mfma_f32_16x16x4f32(__uint_as_float(kf[j][d][e]),
-                                                          __uint_as_float(qf[d][e]), s[j], 0, 0, 0);
+                                                          __uint_as_float(qd[e]), s[j], 0, 0, 0);
           }
         }
+      }
       if (more) load_k(at);
       // ---- mask: tiles that are not visible throughout
       const bool full = u0 + M::kKeys <= wk.len && (u0 >= wk.w0 || u0 + M::kKeys <= a.sinks);
@@ -271,8 +288,14 @@ __global__ __launch_bounds__(64 * kPgWaves, 2) void paged_fwd(PagedArgs a, int c
       }
       // ---- O^T += V^T P^T
       if constexpr (M::kHalf) {
-        const u32x4_t pk = {pack_bf16x2(p[0], p[1]), pack_bf16x2(p[2], p[3]),
-                            pack_bf16x2(p[4], p[5]), pack_bf16x2(p[6], p[7])};
+        // P as bf16 hi + lo: bf16 alone would be most of o's error, and the second product is hardly seen beside the
+        // cache's bytes (N4 to 131k tokens 77.0 -> 77.6 us, N1 11.5 -> 11.7; N128 56.4 -> 55.7 with q in LDS)
+        u32x4_t ph, pl;
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+          ph[k] = pack_bf16x2(p[2 * k], p[2 * k + 1]);
+          pl[k] = pack_bf16x2(p[2 * k] - bf16lo(ph[k]), p[2 * k + 1] - bf16hi(ph[k]));
+        }
 #pragma unroll
         for (int b = 0; b < M::kVB; ++b)
 #pragma unroll
@@ -282,9 +305,11 @@ __global__ __launch_bounds__(64 * kPgWaves, 2) void paged_fwd(PagedArgs a, int c
             for (int k = 0; k < 4; ++k)
               v[k] = __builtin_amdgcn_perm(vf[2 * k + 1][b][e / 2], vf[2 * k][b][e / 2],
                                            e & 1 ? 0x07060302u : 0x05040100u);
-            oacc[b * M::kE + e] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(
-                __builtin_bit_cast(bf16x8_t, v), __builtin_bit_cast(bf16x8_t, pk),
-                oacc[b * M::kE + e], 0, 0, 0);
+            f32x4_t &o = oacc[b * M::kE + e];
+            o = __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8_t, v),
+                                                        __builtin_bit_cast(bf16x8_t, ph), o, 0, 0, 0);
+            o = __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8_t, v),
+                                                        __builtin_bit_cast(bf16x8_t, pl), o, 0, 0, 0);
           }
       } else {
 #pragma unroll

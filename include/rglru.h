@@ -219,7 +219,8 @@ rglru_status rglru_prefill_state(const void *x, void *conv_state, int B, int T, 
  *  o  [B][T][Hq][dh] bf16, out, must not overlap q, k or v
  *  window >= 1; scale > 0, or 0 for 1/sqrt(dh)
  * Softmax and both contractions accumulate in fp32 (MFMA); probabilities enter the second
- * contraction as bf16 hi + lo (about 16 bits). Supported: dt = RGLRU_BF16, dh in {64, 128, 256},
+ * contraction as bf16, and as bf16 hi + lo (about 16 bits) in blocks of rows of which some sees fewer than
+ * 256 keys. Supported: dt = RGLRU_BF16, dh in {64, 128, 256},
  * T * dh * 2 <= 2^30 bytes per sequence of k (else RGLRU_ERR_UNSUPPORTED). No workspace. */
 rglru_status rglru_local_mqa(const void *q, const void *k, const void *v, void *o, int B, int T,
                              int Hq, int dh, int window, float scale, rglru_dtype dt,
@@ -290,6 +291,9 @@ rglru_status rglru_qk_norm_rope_backward(const void *q, const void *k, const flo
  *  o [B][T][Hq][dh] bf16, contiguous, out; must not overlap the inputs
  *  lse [B][Hq][T] f32 or NULL, out: ln sum_u exp(scale * s_u); -inf for rows t >= lens[b]
  *  window >= 1, sinks >= 0; scale > 0, or 0 for 1/sqrt(dh)
+ * Softmax and both contractions accumulate in fp32; the probabilities enter the second one as bf16, and as
+ * bf16 hi + lo (about 16 bits) in blocks of 128 rows of which some sees fewer than 256 keys of its window, where
+ * their rounding would not average out.
  * An infinite or NaN k or v reaches the rows that see it and no others. Supported: dt = RGLRU_BF16,
  * dh in {64, 128, 256}, Hq % Hkv == 0, strides <= 2^20, T * stride * 2 <= 2^30 bytes for k and v. */
 rglru_status rglru_local_attention(const void *q, const void *k, const void *v, const int *lens,
@@ -337,7 +341,9 @@ rglru_status rglru_local_attention_backward(
  * A row whose length is negative or over max_pages * page_size, or that needs a page outside [0,
  * num_pages), becomes NaN; nothing outside the pool is read. Supported: f32 and bf16, dh in {64,
  * 128, 256}, Hq % Hkv == 0, any page_size >= 1, max_pages * page_size and num_pages * page_size
- * below 2^31 - 256. Sums are taken in a fixed order: results are bitwise reproducible. */
+ * below 2^31 - 256. Softmax and both contractions accumulate in fp32; for bf16 the probabilities enter the
+ * second one as bf16 hi + lo (about 16 bits) at every length. Sums are taken in a fixed order: results are
+ * bitwise reproducible. */
 size_t rglru_paged_attention_workspace_size(int N, int Hq, int Hkv, int dh, int page_size,
                                             int max_pages, int window, int sinks, rglru_dtype dt);
 rglru_status rglru_paged_attention(const void *q, const void *k_pages, const void *v_pages,

@@ -772,3 +772,17 @@ def test_given_stream_beside_a_busy_one():
         torch.cuda.synchronize()
         assert all(torch.equal(a, b) for a, b in zip(kept, want)), name
         del new
+
+
+@pytest.mark.parametrize("dtype,lens,Hq,Hkv,dh,page,W,S", [c for c in PAGED if c[0] == BF] + [
+    (BF, list(range(1, 65)), 10, 1, 256, 16, 1 << 30, 0), (BF, list(range(1, 65)), 4, 2, 64, 5, 1 << 30, 0),
+    (BF, [40000, 9000], 8, 2, 128, 32, 1 << 30, 0), (BF, [200, 3000], 17, 1, 256, 7, 1 << 30, 0)])
+def test_paged_attention_holds_probabilities_in_16_bits(dtype, lens, Hq, Hkv, dh, page, W, S):
+    """P enters its product as bf16 hi + lo: hi is off by at most 2^-8 of P, lo by 2^-8 of that. So o is within
+    2^-16 of its terms (and the bound's fp32 part) before its own rounding, at one cached token as at many."""
+    rng = np.random.default_rng(len(lens) + dh)
+    q, kp, vp, table, dl = paged_inputs(rng, dtype, lens, Hq, Hkv, dh, page)
+    got = rg.paged_attention(q, kp, vp, table, dl, W, S)
+    ref, mag, most = ab.paged_attention(num(q), num(kp), num(vp), table.cpu().numpy(), lens, W, S)
+    rp = 2 * (dh + 2) * W24 * most + (max(lens) + 8) * 2 * W24
+    check(got, ref, ((rp + 2.0 ** -16) * mag + 2.0 ** -8 * np.abs(ref)) * (1 + 2.0 ** -7), "o")

@@ -3,7 +3,9 @@
 Each function takes torch tensors, checks dtype / device / contiguity, passes raw device pointers
 and the current HIP stream to the C entry point of the same name, and raises RglruError on a
 non-zero status. Every step of the computation runs in the library's HIP kernels; there is no
-fallback of any kind: if librglru.so is missing or fails to load, importing this package fails.
+fallback of any kind: if librglru.so is missing or fails to load, importing this package fails. The local
+attention block's operators go through a second module, _rglru_torch.so, built against this interpreter's
+torch; if that is missing, they raise ImportError and the recurrent block's work without it.
 """
 from __future__ import annotations
 
@@ -20,11 +22,24 @@ if not os.path.exists(LIB_PATH):
     raise ImportError(f"{LIB_PATH} is not built; run gated_linear_recurrence_conv1d_amd/build.py "
                       "(or __graft_entry__.build())")
 _lib = ctypes.CDLL(LIB_PATH)
+
+
+class _NotThere:
+    """Stands where the module _rglru_torch should be: any use of it says what is missing."""
+
+    def __init__(self, why):
+        self._why = why
+
+    def __getattr__(self, name):
+        raise ImportError("_rglru_torch.so, which the attention block's operators need, is not built or does not "
+                          "load; run gated_linear_recurrence_conv1d_amd/build.py (or __graft_entry__.build())"
+                          ) from self._why
+
+
 try:
     from . import _rglru_torch as _ext  # checks and calls of the attention block's operators
-except ImportError as e:
-    raise ImportError("_rglru_torch.so is not built; run gated_linear_recurrence_conv1d_amd/build.py "
-                      "(or __graft_entry__.build())") from e
+except ImportError as e:  # the recurrent block's operators need none of it
+    _ext = _NotThere(e)
 
 RGLRU_OK = 0
 RGLRU_ERR_INVALID_ARG = 1

@@ -73,9 +73,10 @@ rglru_status check_attn(int B, int T, int Hq, int Hkv, int dh, long long q_strid
     return RGLRU_ERR_UNSUPPORTED;
   // workgroups of 128 rows, and one more in the backward
   if ((T + 127LL) / 128 * B * Hq >= rglru::kMaxBlocks) return RGLRU_ERR_UNSUPPORTED;
-  // a sequence's k and v stay well within 32-bit byte offsets
-  constexpr long long kRange = 1LL << 30;
-  if (T * k_stride * 2 > kRange || T * v_stride * 2 > kRange) return RGLRU_ERR_UNSUPPORTED;
+  // a sequence's k and v below 2 GiB: the sizes that are tested (the kernels' addresses are 64-bit down to a block
+  // of 32 rows, whose offsets kMaxStride bounds)
+  constexpr long long kRange = 1LL << 31;
+  if (T * k_stride * 2 >= kRange || T * v_stride * 2 >= kRange) return RGLRU_ERR_UNSUPPORTED;
   return RGLRU_OK;
 }
 

@@ -295,7 +295,7 @@ rglru_status rglru_qk_norm_rope_backward(const void *q, const void *k, const flo
  * bf16 hi + lo (about 16 bits) in blocks of 128 rows of which some sees fewer than 256 keys of its window, where
  * their rounding would not average out.
  * An infinite or NaN k or v reaches the rows that see it and no others. Supported: dt = RGLRU_BF16,
- * dh in {64, 128, 256}, Hq % Hkv == 0, strides <= 2^20, T * stride * 2 <= 2^30 bytes for k and v. */
+ * dh in {64, 128, 256}, Hq % Hkv == 0, strides <= 2^20, T * stride * 2 < 2^31 bytes for k and v. */
 rglru_status rglru_local_attention(const void *q, const void *k, const void *v, const int *lens,
                                    void *o, float *lse, int B, int T, int Hq, int Hkv, int dh,
                                    long long q_stride, long long k_stride, long long v_stride,

@@ -297,3 +297,14 @@ def test_attention_grid_limit():
     assert attn_bwd(T=257, dq_stride=1 << 20, dk_stride=64, dv_stride=64, **wide) == UNSUP
     assert rg.rglru_local_attention_backward_workspace_size(65535, 257, 16384, 1, 64, 16) == 0
     assert rg.rglru_local_attention_backward_workspace_size(65535, 256, 16384, 1, 64, 16) > 0
+
+
+def test_attention_range():
+    """k and v of a sequence may span up to 2^31 bytes: 233016 tokens of a projection of 16 + 2 heads of 256 (the
+    calls below then end at their missing output)."""
+    packed = dict(B=1, Hq=16, Hkv=1, dh=256, q_stride=4608, k_stride=4608, v_stride=4608)
+    grads = dict(dq_stride=4608, dk_stride=4608, dv_stride=4608)
+    for T, status in ((120000, BAD), (233016, BAD), (233017, UNSUP)):
+        assert attn(T=T, o=None, **packed) == status
+        assert attn_bwd(T=T, lse=None, **packed, **grads) == status
+    assert attn(T=1 << 13, o=None, **dict(packed, v_stride=1 << 17)) == UNSUP

@@ -786,3 +786,31 @@ def test_paged_attention_holds_probabilities_in_16_bits(dtype, lens, Hq, Hkv, dh
     ref, mag, most = ab.paged_attention(num(q), num(kp), num(vp), table.cpu().numpy(), lens, W, S)
     rp = 2 * (dh + 2) * W24 * most + (max(lens) + 8) * 2 * W24
     check(got, ref, ((rp + 2.0 ** -16) * mag + 2.0 ** -8 * np.abs(ref)) * (1 + 2.0 ** -7), "o")
+
+
+def test_attention_beyond_a_gibibyte_of_keys():
+    """A prompt whose k and v span more than 2^30 bytes of a packed projection, and its gradients: the last rows
+    against the oracle on the last 640 tokens. With a window of 64 what rows (keys) from 64 on give there is what
+    they give in the whole."""
+    rng = np.random.default_rng(51)
+    Hq, Hkv, dh, W, tail = 16, 1, 256, 64, 640
+    T = 120000
+    gen = torch.Generator(device=DEV).manual_seed(51)
+    x = torch.randn(1, T, Hq + 2 * Hkv, dh, generator=gen, device=DEV, dtype=BF)
+    q, k, v = x[:, :, :Hq], x[:, :, Hq:Hq + Hkv], x[:, :, Hq + Hkv:]
+    assert T * x.stride(1) * 2 > 1 << 30
+    do = torch.zeros(1, T, Hq, dh, dtype=BF, device=DEV)
+    do[:, -tail:] = normal(rng, 1, tail, Hq, dh)
+    o, lse = rg.local_attention(q, k, v, W, want_lse=True)
+    g = torch.empty_like(x)
+    dq, dk, dv = g[:, :, :Hq], g[:, :, Hq:Hq + Hkv], g[:, :, Hq + Hkv:]
+    rg.local_attention_backward(q, k, v, o, lse, do, W, dq=dq, dk=dk, dv=dv)
+    args = [num(t[:, -tail:]) for t in (q, k, v)]
+    gn = num(do[:, -tail:])
+    ro, rl = ab.attention(*args, W)
+    refs = ab.attention_backward(*args, gn, W)
+    el, eo, eq, ek, ev = ab.attention_bounds(*args, gn, W)
+    check(lse[:, :, 64 - tail:], rl[:, :, 64:], el[:, :, 64:], "lse")
+    for got, ref, e, name in ((o, ro, eo, "o"), (dq, refs[0], eq, "dq"), (dk, refs[1], ek, "dk"), (dv, refs[2], ev, "dv")):
+        check(got[:, 64 - tail:], ref[:, 64:], e[:, 64:], name)
+    assert not g[:, :T - tail - W].any()  # no gradient came in there

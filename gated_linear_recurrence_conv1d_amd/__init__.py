@@ -580,11 +580,15 @@ def local_attention_backward(q, k, v, o, lse, do, window, sinks=0, lens=None, sc
 
 
 @functools.lru_cache(maxsize=256)
+def _paged_bytes(N, Hq, Hkv, dh, page_size, max_pages, window, sinks, dtype) -> int:
+    return int(_lib.rglru_paged_attention_workspace_size(N, Hq, Hkv, dh, page_size, max_pages, window, sinks,
+                                                         _dt(dtype)))
+
+
 def rglru_paged_attention_workspace_size(N, Hq, Hkv, dh, page_size, max_pages, window, sinks,
                                          dtype) -> int:
-    return int(_lib.rglru_paged_attention_workspace_size(
-        N, Hq, Hkv, dh, page_size, max_pages, _int32(window),
-        _int32(sinks), _dt(dtype)))
+    # (plain integers: a size must not be remembered for a tensor, whose value may change)
+    return _paged_bytes(N, Hq, Hkv, dh, page_size, max_pages, _int32(window), _int32(sinks), dtype)
 
 
 def rglru_paged_attention(q, k_pages, v_pages, block_table, lens, o, window, sinks=0, scale=0.0,

@@ -308,3 +308,13 @@ def test_attention_range():
         assert attn(T=T, o=None, **packed) == status
         assert attn_bwd(T=T, lse=None, **packed, **grads) == status
     assert attn(T=1 << 13, o=None, **dict(packed, v_stride=1 << 17)) == UNSUP
+
+
+def test_workspace_size_follows_a_window_that_changes():
+    """A window given as a tensor is read anew: the size is that of its value now."""
+    window = torch.tensor(64)
+    args = (4, 8, 2, 128, 32, 4096)
+    few = rg.rglru_paged_attention_workspace_size(*args, window, 0, "bf16")
+    window.fill_(1 << 20)
+    many = rg.rglru_paged_attention_workspace_size(*args, window, 0, "bf16")
+    assert few < many == rg.rglru_paged_attention_workspace_size(*args, 1 << 20, 0, "bf16")

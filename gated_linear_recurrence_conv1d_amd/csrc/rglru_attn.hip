@@ -12,8 +12,10 @@
 // CU, and each wave works alone between the barriers (one per 32-key block), so that one wave's matrix
 // work runs beside another's exponentials.
 //
-// Bound by the matrix and vector units in turn: they overlap only across the two or three waves of a SIMD. 96 us
-// at B8 T2048 (ragged) Hq10 dh256 W1024 (670 TFLOP/s), 305 us at T16384 Hq8 Hkv2 dh128 W4096 (790 TFLOP/s).
+// Bound at dh 128 by the matrix and vector units in turn, which overlap only across the two or three waves of a SIMD
+// (busy 37% and 39% of the cycles, CUs 75%); at dh 256 by the waits between a wave's steps beside them (31% and 27%
+// of 75%). LDS is busy 17-19%. 96 us at B8 T2048 (ragged) Hq10 dh256 W1024 (670 TFLOP/s), 310 us at T16384 Hq8 Hkv2
+// dh128 W4096 (780 TFLOP/s).
 #include "rglru_attn.h"
 #include "rglru_grid.h"
 #include "rglru_launch.h"

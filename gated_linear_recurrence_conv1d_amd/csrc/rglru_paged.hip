@@ -24,8 +24,8 @@
 // Positions outside the visible set get P = 0 and their V is cleared, so what lies on their part of
 // a page does not matter. Page numbers outside the pool are not followed: the row becomes NaN.
 //
-// N4 Hq8 Hkv2 dh128 to 131k tokens: 401 MB in 77 us (5.2 TB/s, a plain copy's rate); N128 Hq16 dh256 W2048:
-// 224 MB in 52 us and 5 us of joining.
+// N4 Hq8 Hkv2 dh128 to 131k tokens: 401 MB in 77.6 us (5.2 TB/s, a plain copy's rate); N128 Hq16 dh256 W2048:
+// 224 MB in 50 us and 5 us of joining, in fp32 449 MB in 97 and 5.
 #include "rglru_grid.h"
 #include "rglru_launch.h"
 #include "rglru_loads.h"

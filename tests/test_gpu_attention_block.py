@@ -814,3 +814,28 @@ def test_attention_beyond_a_gibibyte_of_keys():
     for got, ref, e, name in ((o, ro, eo, "o"), (dq, refs[0], eq, "dq"), (dk, refs[1], ek, "dk"), (dv, refs[2], ev, "dv")):
         check(got[:, 64 - tail:], ref[:, 64:], e[:, 64:], name)
     assert not g[:, :T - tail - W].any()  # no gradient came in there
+
+
+def test_given_stream_in_a_graph():
+    """Calls on a stream that joins a capture, their outputs and workspaces in the graph's own memory: every replay
+    against the eager result, with eager work of other sizes between them."""
+    rng = np.random.default_rng(43)
+    calls = calls_that_allocate(rng)
+    want = [[t.clone() for t in tensors(call(None))] for _, call in calls]
+    torch.cuda.synchronize()
+    graph, side = torch.cuda.CUDAGraph(), torch.cuda.Stream()
+    with torch.cuda.graph(graph):
+        here = torch.cuda.current_stream()
+        side.wait_stream(here)
+        got = [tensors(call(side)) for _, call in calls]
+        here.wait_stream(side)
+    for i in range(4):
+        for out in got:
+            for t in out:
+                t.fill_(float("nan"))
+        other = [torch.full((100_000 * (i + 1),), float("nan"), device=DEV) for _ in range(4)]
+        graph.replay()
+        torch.cuda.synchronize()
+        del other
+        for (name, _), out, ref in zip(calls, got, want):
+            assert all(torch.equal(a, b) for a, b in zip(out, ref)), (i, name)

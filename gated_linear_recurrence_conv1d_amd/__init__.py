@@ -115,6 +115,25 @@ _lib.rglru_paged_attention.argtypes = ([_vp] * 6 + [_i] * 4 + [_ll] + [_i] * 5 +
                                        [_f, _i, _vp, _sz, _vp])
 _lib.rglru_paged_attention.restype = _i
 
+_lib.rglru_cache_quantize.argtypes = [_vp] * 7 + [_i] * 3 + [_ll] * 3 + [_i, _vp]
+_lib.rglru_cache_quantize.restype = _i
+_lib.rglru_cache_dequantize.argtypes = [_vp] * 9 + [_i] * 4 + [_ll] * 2 + [_i] * 5 + [_vp]
+_lib.rglru_cache_dequantize.restype = _i
+_lib.rglru_paged_attention_e4m3_workspace_size.argtypes = [_i] * 8
+_lib.rglru_paged_attention_e4m3_workspace_size.restype = _sz
+_lib.rglru_paged_attention_e4m3.argtypes = [_vp] * 8 + [_i] * 4 + [_ll] + [_i] * 5 + [_f, _vp, _sz, _vp]
+_lib.rglru_paged_attention_e4m3.restype = _i
+_lib.rglru_prefix_attention_workspace_size.argtypes = [_i] * 9
+_lib.rglru_prefix_attention_workspace_size.restype = _sz
+_lib.rglru_prefix_attention.argtypes = [_vp] * 10 + [_i] * 4 + [_ll] + [_i] * 6 + [_f, _i, _vp, _sz, _vp]
+_lib.rglru_prefix_attention.restype = _i
+_lib.rglru_linear_attention_workspace_size.argtypes = [_i] * 6
+_lib.rglru_linear_attention_workspace_size.restype = _sz
+_lib.rglru_linear_attention.argtypes = [_vp] * 8 + [_i] * 6 + [_ll] * 3 + [_i, _f, _i, _vp, _sz, _vp]
+_lib.rglru_linear_attention.restype = _i
+_lib.rglru_linear_attention_step.argtypes = [_vp] * 7 + [_i] * 5 + [_ll] * 3 + [_i, _f, _i, _vp]
+_lib.rglru_linear_attention_step.restype = _i
+
 
 class RglruError(RuntimeError):
     def __init__(self, status: int, where: str):
@@ -445,10 +464,10 @@ _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (
 _current_device = getattr(torch._C, "_cuda_getDevice", None) or torch.cuda.current_device
 
 
-def _call(where, fn, q, stream, *args):
+def _call(where, fn, q, stream, *args, name="q"):
     """fn(*args, stream), which checks its tensors (csrc/rglru_torch.cpp), on q's device."""
     if not isinstance(q, torch.Tensor):
-        raise TypeError("q: expected a torch.Tensor")
+        raise TypeError(f"{name}: expected a torch.Tensor")
     index = q.get_device()
     if index < 0:
         status = fn(*args, 0)  # refused there, by what is wrong with the tensors
@@ -614,6 +633,161 @@ def paged_attention(q, k_pages, v_pages, block_table, lens, window, sinks=0, sca
         if n:
             workspace = _ext.empty_bytes(q, n)
     rglru_paged_attention(q, k_pages, v_pages, block_table, lens, o, window, sinks, scale, workspace)
+    return o
+
+
+# ---- serving: the cache in 8 bits, a shared prefix, linear attention. Tensors of heads, devices and streams as for the
+# attention block. An e4m3 cache is k_pages, v_pages (torch.float8_e4m3fn [pages, page, Hkv, dh]) with k_scales, v_scales
+# (torch.float8_e8m0fnu [pages, page, Hkv]); a fresh one may hold anything.
+def rglru_cache_quantize(k, v, slots, k_pages, v_pages, k_scales, v_scales, stream=None):
+    """k, v [..., Hkv, dh], bf16 or f32; slots int64 [...]. Writes into the cache, in place."""
+    _call("rglru_cache_quantize", _ext.cache_quantize, k, stream, k, v, slots, k_pages, v_pages, k_scales, v_scales,
+          name="k")
+
+
+def cache_quantize(k, v, slots, k_pages, v_pages, k_scales, v_scales, stream=None):
+    """rglru_cache_quantize: nothing is made, and nothing returned."""
+    rglru_cache_quantize(k, v, slots, k_pages, v_pages, k_scales, v_scales, stream)
+
+
+def rglru_cache_dequantize(k_pages, v_pages, k_scales, v_scales, block_table, lens, k_out, v_out, starts=None,
+                           zero_rest=False, stream=None):
+    """k_out, v_out [B, T, Hkv, dh], bf16 or f32; block_table int32 [B, max_pages], lens and starts int32 [B]. Rows
+    behind a sequence's last token are left as they are, or zeros."""
+    _call("rglru_cache_dequantize", _ext.cache_dequantize, k_out, stream, k_pages, v_pages, k_scales, v_scales,
+          block_table, lens, starts, k_out, v_out, bool(zero_rest), name="k_out")
+
+
+def cache_dequantize(k_pages, v_pages, k_scales, v_scales, block_table, lens, T, starts=None, dtype=torch.bfloat16,
+                     stream=None):
+    """Returns (k, v) [B, T, Hkv, dh]: of each sequence the tokens from its start on, then zeros."""
+    if stream is not None:
+        return _on(stream, k_pages, lambda: cache_dequantize(k_pages, v_pages, k_scales, v_scales, block_table, lens, T,
+                                                             starts, dtype))
+    shape = (block_table.shape[0], T, *k_pages.shape[2:])
+    k_out = torch.empty(shape, dtype=dtype, device=k_pages.device)
+    v_out = _ext.empty_as(k_out)
+    rglru_cache_dequantize(k_pages, v_pages, k_scales, v_scales, block_table, lens, k_out, v_out, starts, True)
+    return k_out, v_out
+
+
+def rglru_paged_attention_e4m3_workspace_size(N, Hq, Hkv, dh, page_size, max_pages, window, sinks) -> int:
+    return rglru_paged_attention_workspace_size(N, Hq, Hkv, dh, page_size, max_pages, window, sinks, torch.bfloat16)
+
+
+def rglru_paged_attention_e4m3(q, k_pages, v_pages, k_scales, v_scales, block_table, lens, o, window, sinks=0,
+                               scale=0.0, workspace=None, stream=None):
+    """rglru_paged_attention over an e4m3 cache; q [N,Hq,dh] and o bf16."""
+    _call("rglru_paged_attention_e4m3", _ext.paged_attention_e4m3, q, stream, q, k_pages, v_pages, k_scales, v_scales,
+          block_table, lens, o, window, sinks, scale, workspace)
+
+
+def paged_attention_e4m3(q, k_pages, v_pages, k_scales, v_scales, block_table, lens, window, sinks=0, scale=0.0,
+                         workspace=None, stream=None):
+    """Returns o [N,Hq,dh] (bf16)."""
+    if stream is not None:
+        return _on(stream, q, lambda: paged_attention_e4m3(q, k_pages, v_pages, k_scales, v_scales, block_table, lens,
+                                                           window, sinks, scale, workspace))
+    o = _ext.empty_as(q)
+    if workspace is None and q.dim() == 3 and k_pages.dim() == 4 and block_table.dim() == 2:
+        N, Hq, dh = q.shape
+        _, page, Hkv, _ = k_pages.shape
+        n = rglru_paged_attention_e4m3_workspace_size(N, Hq, Hkv, dh, page, block_table.shape[1], window, sinks)
+        if n:
+            workspace = _ext.empty_bytes(q, n)
+    rglru_paged_attention_e4m3(q, k_pages, v_pages, k_scales, v_scales, block_table, lens, o, window, sinks, scale,
+                               workspace)
+    return o
+
+
+@functools.lru_cache(maxsize=256)
+def _prefix_bytes(N, Hq, Hkv, dh, page_size, prefix_pages, max_pages, window, sinks) -> int:
+    return int(_lib.rglru_prefix_attention_workspace_size(N, Hq, Hkv, dh, page_size, prefix_pages, max_pages, window,
+                                                          sinks))
+
+
+def rglru_prefix_attention_workspace_size(N, Hq, Hkv, dh, page_size, prefix_pages, max_pages, window, sinks) -> int:
+    return _prefix_bytes(N, Hq, Hkv, dh, page_size, prefix_pages, max_pages, _int32(window), _int32(sinks))
+
+
+def rglru_prefix_attention(q, k_pages, v_pages, prefix_table, prefix_len, block_table, lens, o, window, sinks=0,
+                           scale=0.0, k_scales=None, v_scales=None, workspace=None, stream=None):
+    """q [N,Hq,dh] bf16, o as q and contiguous; the cache in bf16, or in e4m3 with its scales; prefix_table int32
+    [prefix_pages], prefix_len int32 [1]; block_table int32 [N,max_pages] and lens int32 [N] of the own tokens."""
+    _call("rglru_prefix_attention", _ext.prefix_attention, q, stream, q, k_pages, v_pages, k_scales, v_scales,
+          prefix_table, prefix_len, block_table, lens, o, window, sinks, scale, workspace)
+
+
+def prefix_attention(q, k_pages, v_pages, prefix_table, prefix_len, block_table, lens, window, sinks=0, scale=0.0,
+                     k_scales=None, v_scales=None, workspace=None, stream=None):
+    """Returns o [N,Hq,dh] (bf16)."""
+    if stream is not None:
+        return _on(stream, q, lambda: prefix_attention(q, k_pages, v_pages, prefix_table, prefix_len, block_table, lens,
+                                                       window, sinks, scale, k_scales, v_scales, workspace))
+    o = _ext.empty_as(q)
+    if (workspace is None and q.dim() == 3 and k_pages.dim() == 4 and block_table.dim() == 2 and
+            prefix_table.dim() == 1):
+        N, Hq, dh = q.shape
+        _, page, Hkv, _ = k_pages.shape
+        n = rglru_prefix_attention_workspace_size(N, Hq, Hkv, dh, page, prefix_table.shape[0], block_table.shape[1],
+                                                  window, sinks)
+        if n:
+            workspace = _ext.empty_bytes(q, n)
+    rglru_prefix_attention(q, k_pages, v_pages, prefix_table, prefix_len, block_table, lens, o, window, sinks, scale,
+                           k_scales, v_scales, workspace)
+    return o
+
+
+@functools.lru_cache(maxsize=256)
+def _linear_bytes(B, T, Hk, H, dk, dv) -> int:
+    return int(_lib.rglru_linear_attention_workspace_size(B, T, Hk, H, dk, dv))
+
+
+def rglru_linear_attention_workspace_size(B, T, Hk, H, dk, dv) -> int:
+    return _linear_bytes(B, T, Hk, H, dk, dv)
+
+
+def rglru_linear_attention(q, k, v, log_decay, o, state=None, state_out=None, lens=None, scale=0.0, workspace=None,
+                           stream=None):
+    """q, k [B,T,Hk,dk], v [B,T,H,dv], o as v and contiguous, bf16; log_decay f32 [H] or [B,T,H]; state and state_out f32
+    [B,H,dk,dv] (state_out may be state); lens int32 [B]."""
+    _call("rglru_linear_attention", _ext.linear_attention, q, stream, q, k, v, log_decay, lens, state, o, state_out,
+          scale, workspace)
+
+
+def linear_attention(q, k, v, log_decay, state=None, lens=None, scale=0.0, state_out=None, workspace=None,
+                     stream=None):
+    """Returns (o, state_out): o [B,T,H,dv] (bf16) and the state f32 [B,H,dk,dv] after the last token, a new tensor
+    unless given (state itself: in place)."""
+    if stream is not None:
+        return _on(stream, q, lambda: linear_attention(q, k, v, log_decay, state, lens, scale, state_out, workspace))
+    o = _ext.empty_as(v)
+    if q.dim() == 4 and v.dim() == 4:
+        B, T, Hk, dk = q.shape
+        _, _, H, dv = v.shape
+        if state_out is None:
+            state_out = torch.empty((B, H, dk, dv), dtype=torch.float32, device=q.device)
+        if workspace is None:
+            n = rglru_linear_attention_workspace_size(B, T, Hk, H, dk, dv)
+            if n:
+                workspace = _ext.empty_bytes(q, n)
+    rglru_linear_attention(q, k, v, log_decay, o, state, state_out, lens, scale, workspace)
+    return o, state_out
+
+
+def rglru_linear_attention_step(q, k, v, log_decay, o, state, state_out, scale=0.0, stream=None):
+    """q, k [N,Hk,dk], v [N,H,dv], o as v and contiguous, bf16; log_decay f32 [H] or [N,H]; state and state_out f32
+    [N,H,dk,dv] (state_out may be state)."""
+    _call("rglru_linear_attention_step", _ext.linear_attention_step, q, stream, q, k, v, log_decay, state, state_out, o,
+          scale)
+
+
+def linear_attention_step(q, k, v, log_decay, state, scale=0.0, state_out=None, stream=None):
+    """Returns o [N,H,dv] (bf16); the state is updated in place unless state_out is given."""
+    if stream is not None:
+        return _on(stream, q, lambda: linear_attention_step(q, k, v, log_decay, state, scale, state_out))
+    o = _ext.empty_as(v)
+    rglru_linear_attention_step(q, k, v, log_decay, o, state, state if state_out is None else state_out, scale)
     return o
 
 

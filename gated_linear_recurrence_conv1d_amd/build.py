@@ -15,7 +15,8 @@ EXT = os.path.join(PKG, "_rglru_torch.so")
 SOURCES = ["rglru_api.cpp", "rglru_gates.hip", "rglru_scan.hip", "rglru_decode.hip",
            "rglru_fused.hip", "rglru_backward.hip", "rglru_bwd_tiles.hip", "rglru_bwd_fused.hip",
            "rglru_mqa.hip", "rglru_noalloc.hip", "rglru_attn_api.cpp", "rglru_rope.hip",
-           "rglru_paged.hip", "rglru_mqa_bwd.hip", "rglru_attn.hip"]
+           "rglru_paged.hip", "rglru_mqa_bwd.hip", "rglru_attn.hip", "rglru_cache.hip", "rglru_prefix.hip",
+           "rglru_linear.hip", "rglru_serve_api.cpp"]
 EXT_SOURCE = "rglru_torch.cpp"
 HIPCC = os.environ.get("HIPCC", "/opt/rocm/bin/hipcc")
 CXX = os.environ.get("CXX", "g++")

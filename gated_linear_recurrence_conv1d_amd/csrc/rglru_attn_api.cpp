@@ -15,35 +15,20 @@
 namespace {
 
 using rglru::aligned;
+using rglru::check_heads;
 using rglru::elem_bytes;
+using rglru::flat;
+using rglru::heads_of;
 using rglru::hip_status;
 using rglru::kBF16;
 using rglru::kF32;
+using rglru::kMaxStride;
+using rglru::kMaxTokens;
+using rglru::max_floor;
 using rglru::overlaps;
 using rglru::Rows;
 using rglru::same;
-
-constexpr long long kMaxStride = 1LL << 20;  // elements from token to token
-constexpr long long kMaxTokens = 0x7FFFFF00;  // token and cache row indices stay in an int
-
-Rows heads_of(const void *p, size_t rows, int heads, int dh, long long stride, rglru_dtype dt) {
-  const size_t e = elem_bytes(dt);
-  return {p, rows, static_cast<size_t>(heads) * dh * e, static_cast<size_t>(stride) * e};
-}
-
-Rows flat(const void *p, size_t bytes) { return {p, p ? size_t{1} : 0, bytes, bytes}; }
-
-// Sizes and types every operator on rows of heads shares.
-rglru_status check_heads(long long rows, int Hq, int Hkv, int dh, rglru_dtype dt) {
-  if (rows < 1 || Hq < 1 || Hkv < 1 || dh < 1) return RGLRU_ERR_INVALID_ARG;
-  if (dt != RGLRU_F32 && dt != RGLRU_BF16) return RGLRU_ERR_UNSUPPORTED;
-  if (Hq > 65535 || Hkv > 65535) return RGLRU_ERR_UNSUPPORTED;
-  return RGLRU_OK;
-}
-
-bool stride_ok(long long stride, int heads, int dh) {
-  return stride >= static_cast<long long>(heads) * dh;
-}
+using rglru::stride_ok;
 
 rglru_status check_rope(int rows, int Hq, int Hkv, int dh, int rot, float eps, rglru_dtype dt,
                         const float *q_w, const float *k_w, const float *inv_freq) {
@@ -84,10 +69,6 @@ rglru_status check_attn(int B, int T, int Hq, int Hkv, int dh, long long q_strid
 bool bwd_grid_ok(int B, int T, int Hkv, int dh) {
   return (T + 127LL) / 128 * B * Hkv * (dh / 4) <= rglru::kMaxBlocks;
 }
-
-// The kernels' running maximum starts here: below every score that matters, and finite in exp2
-// units.
-float max_floor(float c) { return -2.9e38f / (c > 1.0f ? c : 1.0f); }
 
 // Where the parts of the attention backward's workspace begin (lse2 first), and its size.
 struct AttnBwdLayout {
@@ -133,6 +114,90 @@ size_t paged_bytes(const rglru::PagedPlan &p, int N, int Hq, int dh) {
   if (p.splits == 1) return 0;
   return paged_part_bytes(p, N, Hq, dh) +
          rglru::align_up(static_cast<size_t>(N) * p.splits * Hq * 2 * sizeof(float));
+}
+
+// What every attention over a paged cache asks of its tensors.
+rglru_status check_paged_tensors(const void *q, const void *k_pages, const void *v_pages, const void *k_scales,
+                                 const void *v_scales, const int *block_table, const int *lens, const void *o, int N,
+                                 int Hq, int Hkv, int dh, long long q_stride, int num_pages, int page_size,
+                                 int max_pages, float scale, rglru_dtype dt, const void *workspace,
+                                 size_t workspace_bytes, size_t need) {
+  if (num_pages < 1 || !(scale == scale) || scale < 0.0f || std::isinf(scale))
+    return RGLRU_ERR_INVALID_ARG;
+  if (static_cast<long long>(num_pages) * page_size >= kMaxTokens) return RGLRU_ERR_UNSUPPORTED;
+  if (!q || !k_pages || !v_pages || !block_table || !lens || !o) return RGLRU_ERR_INVALID_ARG;
+  const size_t e = elem_bytes(dt);
+  if (!stride_ok(q_stride, Hq, dh) || q_stride * e % 16) return RGLRU_ERR_INVALID_ARG;
+  const void *vec16[] = {q, k_pages, v_pages};
+  for (const void *p : vec16)
+    if (!aligned(p, 16)) return RGLRU_ERR_INVALID_ARG;
+  if (!aligned(o, e) || !aligned(block_table, 4) || !aligned(lens, 4)) return RGLRU_ERR_INVALID_ARG;
+  if (need && (!workspace || workspace_bytes < need)) return RGLRU_ERR_WORKSPACE;
+  if (need && !aligned(workspace, 16)) return RGLRU_ERR_INVALID_ARG;
+  const size_t heads = static_cast<size_t>(num_pages) * page_size * Hkv, pool = heads * dh * (k_scales ? 1 : e);
+  const Rows outs[] = {flat(o, static_cast<size_t>(N) * Hq * dh * e),
+                       flat(need ? workspace : nullptr, need)};
+  const Rows ins[] = {heads_of(q, N, Hq, dh, q_stride, dt), flat(k_pages, pool), flat(v_pages, pool),
+                      flat(k_scales, heads), flat(v_scales, heads),
+                      flat(block_table, static_cast<size_t>(N) * max_pages * sizeof(int)),
+                      flat(lens, static_cast<size_t>(N) * sizeof(int))};
+  for (const Rows &w : outs)
+    for (const Rows &r : ins)
+      if (overlaps(w, r)) return RGLRU_ERR_INVALID_ARG;
+  return overlaps(outs[0], outs[1]) ? RGLRU_ERR_INVALID_ARG : RGLRU_OK;
+}
+
+rglru_status paged_attention(const void *q, const void *k_pages, const void *v_pages, const void *k_scales,
+                             const void *v_scales, const int *block_table, const int *lens, void *o, int N, int Hq,
+                             int Hkv, int dh, long long q_stride, int num_pages, int page_size, int max_pages,
+                             int window, int sinks, float scale, rglru_dtype dt, void *workspace,
+                             size_t workspace_bytes, void *stream) {
+  const rglru_status st = check_paged(N, Hq, Hkv, dh, page_size, max_pages, window, sinks, dt);
+  if (st != RGLRU_OK) return st;
+  const rglru::PagedPlan plan = plan_of(N, Hq, Hkv, page_size, max_pages, window, sinks, dt);
+  const size_t need = paged_bytes(plan, N, Hq, dh);
+  const rglru_status sp = check_paged_tensors(q, k_pages, v_pages, k_scales, v_scales, block_table, lens, o, N, Hq, Hkv,
+                                              dh, q_stride, num_pages, page_size, max_pages, scale, dt, workspace,
+                                              workspace_bytes, need);
+  if (sp != RGLRU_OK) return sp;
+  if (scale == 0.0f) scale = 1.0f / std::sqrt(static_cast<float>(dh));
+  const float c = scale * 1.4426950408889634f;
+  char *ws = static_cast<char *>(workspace);
+  rglru::PagedArgs a = {q,        k_pages, v_pages, block_table, lens,      o,         nullptr,
+                        nullptr,  N,       Hq,      Hkv,         dh,        q_stride,  num_pages,
+                        page_size, max_pages, window, sinks,     c,         max_floor(c), k_scales,  v_scales,
+                        nullptr,  0,       0,       0};
+  if (need) {
+    a.part = reinterpret_cast<float *>(ws);
+    a.stat = reinterpret_cast<float *>(ws + paged_part_bytes(plan, N, Hq, dh));
+  }
+  (void)hipGetLastError();
+  return hip_status(rglru::launch_paged_attention(a, plan, dt == RGLRU_BF16 ? kBF16 : kF32,
+                                                  static_cast<hipStream_t>(stream)));
+}
+
+// Attention over a shared prefix: the own tokens' sizes as in paged attention, and the prefix's.
+rglru_status check_prefix(int N, int Hq, int Hkv, int dh, int page_size, int prefix_pages, int max_pages, int window,
+                          int sinks) {
+  if (prefix_pages < 1) return RGLRU_ERR_INVALID_ARG;
+  const rglru_status st = check_paged(N, Hq, Hkv, dh, page_size, max_pages, window, sinks, RGLRU_BF16);
+  if (st != RGLRU_OK) return st;
+  if (static_cast<long long>(prefix_pages) * page_size >= kMaxTokens) return RGLRU_ERR_UNSUPPORTED;
+  return RGLRU_OK;
+}
+struct PrefixPlans {
+  rglru::PagedPlan shared, own;
+  size_t part_bytes, bytes;
+};
+PrefixPlans prefix_plans(int N, int Hq, int Hkv, int dh, int page_size, int prefix_pages, int max_pages, int window,
+                         int sinks) {
+  PrefixPlans p;
+  p.shared = rglru::prefix_plan(N, Hq, Hkv, static_cast<long long>(prefix_pages) * page_size);
+  p.own = plan_of(N, Hq, Hkv, page_size, max_pages, window, sinks, RGLRU_BF16);
+  const size_t rows = static_cast<size_t>(N) * (static_cast<size_t>(p.shared.splits) + p.own.splits) * Hq;
+  p.part_bytes = rglru::align_up(rows * dh * sizeof(float));
+  p.bytes = p.part_bytes + rglru::align_up(rows * 2 * sizeof(float));
+  return p;
 }
 
 }  // namespace
@@ -364,45 +429,68 @@ rglru_status rglru_paged_attention(const void *q, const void *k_pages, const voi
                                    int page_size, int max_pages, int window, int sinks,
                                    float scale, rglru_dtype dt, void *workspace,
                                    size_t workspace_bytes, void *stream) {
-  rglru_status st = check_paged(N, Hq, Hkv, dh, page_size, max_pages, window, sinks, dt);
+  return paged_attention(q, k_pages, v_pages, nullptr, nullptr, block_table, lens, o, N, Hq, Hkv, dh, q_stride,
+                         num_pages, page_size, max_pages, window, sinks, scale, dt, workspace, workspace_bytes, stream);
+}
+
+size_t rglru_paged_attention_e4m3_workspace_size(int N, int Hq, int Hkv, int dh, int page_size, int max_pages,
+                                                 int window, int sinks) {
+  return rglru_paged_attention_workspace_size(N, Hq, Hkv, dh, page_size, max_pages, window, sinks, RGLRU_BF16);
+}
+
+rglru_status rglru_paged_attention_e4m3(const void *q, const void *k_pages, const void *v_pages, const void *k_scales,
+                                        const void *v_scales, const int *block_table, const int *lens, void *o, int N,
+                                        int Hq, int Hkv, int dh, long long q_stride, int num_pages, int page_size,
+                                        int max_pages, int window, int sinks, float scale, void *workspace,
+                                        size_t workspace_bytes, void *stream) {
+  if (!k_scales || !v_scales) return RGLRU_ERR_INVALID_ARG;
+  return paged_attention(q, k_pages, v_pages, k_scales, v_scales, block_table, lens, o, N, Hq, Hkv, dh, q_stride,
+                         num_pages, page_size, max_pages, window, sinks, scale, RGLRU_BF16, workspace,
+                         workspace_bytes, stream);
+}
+
+size_t rglru_prefix_attention_workspace_size(int N, int Hq, int Hkv, int dh, int page_size, int prefix_pages,
+                                             int max_pages, int window, int sinks) {
+  if (check_prefix(N, Hq, Hkv, dh, page_size, prefix_pages, max_pages, window, sinks) != RGLRU_OK) return 0;
+  return prefix_plans(N, Hq, Hkv, dh, page_size, prefix_pages, max_pages, window, sinks).bytes;
+}
+
+rglru_status rglru_prefix_attention(const void *q, const void *k_pages, const void *v_pages, const void *k_scales,
+                                    const void *v_scales, const int *prefix_table, const int *prefix_len,
+                                    const int *block_table, const int *lens, void *o, int N, int Hq, int Hkv, int dh,
+                                    long long q_stride, int num_pages, int page_size, int prefix_pages, int max_pages,
+                                    int window, int sinks, float scale, rglru_dtype dt, void *workspace,
+                                    size_t workspace_bytes, void *stream) {
+  if (dt != RGLRU_BF16) return RGLRU_ERR_UNSUPPORTED;
+  const rglru_status st = check_prefix(N, Hq, Hkv, dh, page_size, prefix_pages, max_pages, window, sinks);
   if (st != RGLRU_OK) return st;
-  if (num_pages < 1 || !(scale == scale) || scale < 0.0f || std::isinf(scale))
-    return RGLRU_ERR_INVALID_ARG;
-  if (static_cast<long long>(num_pages) * page_size >= kMaxTokens) return RGLRU_ERR_UNSUPPORTED;
-  if (!q || !k_pages || !v_pages || !block_table || !lens || !o) return RGLRU_ERR_INVALID_ARG;
-  const size_t e = elem_bytes(dt);
-  if (!stride_ok(q_stride, Hq, dh) || q_stride * e % 16) return RGLRU_ERR_INVALID_ARG;
-  const void *vec16[] = {q, k_pages, v_pages};
-  for (const void *p : vec16)
-    if (!aligned(p, 16)) return RGLRU_ERR_INVALID_ARG;
-  if (!aligned(o, e) || !aligned(block_table, 4) || !aligned(lens, 4)) return RGLRU_ERR_INVALID_ARG;
-  const rglru::PagedPlan plan = plan_of(N, Hq, Hkv, page_size, max_pages, window, sinks, dt);
-  const size_t need = paged_bytes(plan, N, Hq, dh);
-  if (need && (!workspace || workspace_bytes < need)) return RGLRU_ERR_WORKSPACE;
-  if (need && !aligned(workspace, 16)) return RGLRU_ERR_INVALID_ARG;
-  const size_t pool = static_cast<size_t>(num_pages) * page_size * Hkv * dh * e;
-  const Rows outs[] = {flat(o, static_cast<size_t>(N) * Hq * dh * e),
-                       flat(need ? workspace : nullptr, need)};
-  const Rows ins[] = {heads_of(q, N, Hq, dh, q_stride, dt), flat(k_pages, pool), flat(v_pages, pool),
-                      flat(block_table, static_cast<size_t>(N) * max_pages * sizeof(int)),
-                      flat(lens, static_cast<size_t>(N) * sizeof(int))};
+  if (!prefix_table || !prefix_len || (k_scales == nullptr) != (v_scales == nullptr)) return RGLRU_ERR_INVALID_ARG;
+  if (!aligned(prefix_table, 4) || !aligned(prefix_len, 4)) return RGLRU_ERR_INVALID_ARG;
+  const PrefixPlans plan = prefix_plans(N, Hq, Hkv, dh, page_size, prefix_pages, max_pages, window, sinks);
+  const rglru_status sp = check_paged_tensors(q, k_pages, v_pages, k_scales, v_scales, block_table, lens, o, N, Hq, Hkv,
+                                              dh, q_stride, num_pages, page_size, max_pages, scale, RGLRU_BF16,
+                                              workspace, workspace_bytes, plan.bytes);
+  if (sp != RGLRU_OK) return sp;
+  const Rows outs[] = {flat(o, static_cast<size_t>(N) * Hq * dh * 2), flat(workspace, plan.bytes)};
+  const Rows ins[] = {flat(prefix_table, static_cast<size_t>(prefix_pages) * sizeof(int)), flat(prefix_len, sizeof(int))};
   for (const Rows &w : outs)
     for (const Rows &r : ins)
       if (overlaps(w, r)) return RGLRU_ERR_INVALID_ARG;
-  if (overlaps(outs[0], outs[1])) return RGLRU_ERR_INVALID_ARG;
   if (scale == 0.0f) scale = 1.0f / std::sqrt(static_cast<float>(dh));
   const float c = scale * 1.4426950408889634f;
-  char *ws = static_cast<char *>(workspace);
-  rglru::PagedArgs a = {q,        k_pages, v_pages, block_table, lens,      o,         nullptr,
-                        nullptr,  N,       Hq,      Hkv,         dh,        q_stride,  num_pages,
-                        page_size, max_pages, window, sinks,     c,         max_floor(c)};
-  if (need) {
-    a.part = reinterpret_cast<float *>(ws);
-    a.stat = reinterpret_cast<float *>(ws + paged_part_bytes(plan, N, Hq, dh));
-  }
+  const long long cap = static_cast<long long>(prefix_pages) * page_size;
+  float *const part = static_cast<float *>(workspace);
+  float *const stat = reinterpret_cast<float *>(static_cast<char *>(workspace) + plan.part_bytes);
+  const int parts = plan.shared.splits + plan.own.splits;
+  const rglru::PagedArgs own = {q,         k_pages,   v_pages, block_table, lens,     o,        part,
+                                stat,      N,         Hq,      Hkv,         dh,       q_stride, num_pages,
+                                page_size, max_pages, window,  sinks,       c,        max_floor(c), k_scales,
+                                v_scales,  prefix_len, cap,    parts,       plan.shared.splits};
+  const rglru::PrefixArgs a = {q,    k_pages,  v_pages, k_scales,  v_scales,  prefix_table, prefix_len, lens, o,
+                               part, stat,     N,       Hq,        Hkv,       q_stride,     cap,        num_pages,
+                               page_size, parts, window, sinks,    c,         max_floor(c)};
   (void)hipGetLastError();
-  return hip_status(rglru::launch_paged_attention(a, plan, dt == RGLRU_BF16 ? kBF16 : kF32,
-                                                  static_cast<hipStream_t>(stream)));
+  return hip_status(rglru::launch_prefix_attention(a, own, plan.shared, plan.own, static_cast<hipStream_t>(stream)));
 }
 
 }  // extern "C"

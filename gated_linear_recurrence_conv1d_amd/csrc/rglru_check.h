@@ -45,4 +45,31 @@ inline bool overlaps(const Rows &a, const Rows &b) {
 
 inline bool same(const Rows &a, const Rows &b) { return a.p == b.p && a.stride == b.stride; }
 
+// ---- operators on rows of heads
+constexpr long long kMaxStride = 1LL << 20;  // elements from token to token
+constexpr long long kMaxTokens = 0x7FFFFF00;  // token and cache row indices stay in an int
+
+inline Rows heads_of(const void *p, size_t rows, int heads, int dh, long long stride, rglru_dtype dt) {
+  const size_t e = elem_bytes(dt);
+  return {p, rows, static_cast<size_t>(heads) * dh * e, static_cast<size_t>(stride) * e};
+}
+
+inline Rows flat(const void *p, size_t bytes) { return {p, p ? size_t{1} : 0, bytes, bytes}; }
+
+// Sizes and types every operator on rows of heads shares.
+inline rglru_status check_heads(long long rows, int Hq, int Hkv, int dh, rglru_dtype dt) {
+  if (rows < 1 || Hq < 1 || Hkv < 1 || dh < 1) return RGLRU_ERR_INVALID_ARG;
+  if (dt != RGLRU_F32 && dt != RGLRU_BF16) return RGLRU_ERR_UNSUPPORTED;
+  if (Hq > 65535 || Hkv > 65535) return RGLRU_ERR_UNSUPPORTED;
+  return RGLRU_OK;
+}
+
+inline bool stride_ok(long long stride, int heads, int dh) {
+  return stride >= static_cast<long long>(heads) * dh;
+}
+
+// The kernels' running maximum starts here: below every score that matters, and finite in exp2
+// units.
+inline float max_floor(float c) { return -2.9e38f / (c > 1.0f ? c : 1.0f); }
+
 }  // namespace rglru

@@ -157,6 +157,12 @@ struct PagedArgs {
   int num_pages, page, max_pages, window, sinks;
   float c;      // scale * log2(e)
   float floor;  // the running maximum's start: below every score, floor * c finite
+  const void *k_scales, *v_scales;  // e8m0 [..][Hkv]: the cache is in e4m3 (rglru_e4m3.h); else NULL
+  // rows behind a shared prefix (launch_paged_parts): its length [1] and the most its table holds, the chunks' places
+  // in part and stat [N][parts][Hq], from first_part on
+  const int *prefix_len;
+  long long prefix_cap;
+  int parts, first_part;
 };
 struct PagedPlan {
   int chunk;   // tiles per workgroup
@@ -164,6 +170,80 @@ struct PagedPlan {
 };
 PagedPlan paged_plan(int N, int Hq, int Hkv, long long max_len, int window, int sinks, int io);
 hipError_t launch_paged_attention(const PagedArgs &a, const PagedPlan &p, int io, hipStream_t s);
+// Each row's own chunks behind a shared prefix, as O, m and l (bf16, or e4m3 with scales).
+hipError_t launch_paged_parts(const PagedArgs &a, const PagedPlan &p, hipStream_t s);
+
+// Attention over a shared prefix and each sequence's own tokens (bf16 cache, or e4m3 with scales); the parts' O and
+// (m, l) as in PagedArgs, those of the prefix first. The own tokens' part: `own`, with prefix_len and its places set.
+struct PrefixArgs {
+  const void *q, *k_pages, *v_pages, *k_scales, *v_scales;
+  const int *prefix_table, *prefix_len, *lens;
+  void *o;
+  float *part, *stat;
+  int N, Hq, Hkv;
+  long long q_stride, prefix_cap;
+  int num_pages, page, parts, window, sinks;
+  float c, floor;
+};
+PagedPlan prefix_plan(int N, int Hq, int Hkv, long long cap);
+hipError_t launch_prefix_attention(const PrefixArgs &a, const PagedArgs &own, const PagedPlan &p, const PagedPlan &po,
+                                   hipStream_t s);
+
+// Linear attention with a decay for each head (bf16; dk, dv in {64, 128, 256}); state [B][H][dk][dv] f32.
+struct LinearArgs {
+  const void *q, *k, *v;
+  const float *log_decay;  // [H], or [B][T][H] if gated
+  const int *lens;         // [B] or NULL
+  const float *s0;         // or NULL: zeros
+  void *o;
+  float *s_out;  // or NULL; may be s0
+  float *seg;    // [B][H][segs][dk][dv]: the segments' first states (segs > 1)
+  float *sums;   // [B][H][segs - 1]: their summed log2 decays
+  int B, T, Hk, H, dk, dv;
+  long long q_stride, k_stride, v_stride;
+  float scale;
+  bool gated;
+  int segs, seg_len;
+  int run;  // segments of a launch (set by the launcher)
+};
+struct LinearPlan {
+  int segs, seg_len;
+};
+LinearPlan linear_plan(int B, int T, int H, int dv);
+hipError_t launch_linear_attention(const LinearArgs &a, hipStream_t s);
+struct LinearStepArgs {
+  const void *q, *k, *v;
+  const float *log_decay;  // [H], or [N][H] if gated
+  const float *s_in;
+  float *s_out;  // may be s_in
+  void *o;
+  int N, Hk, H, dk, dv;
+  long long q_stride, k_stride, v_stride;
+  float scale;
+  bool gated;
+};
+hipError_t launch_linear_step(const LinearStepArgs &a, hipStream_t s);
+
+// A paged cache in e4m3 (rglru_e4m3.h), written and read back: dh in {64, 128, 256}, rows of 16-byte aligned heads.
+struct CacheWriteArgs {
+  const void *k, *v;
+  const long long *slots;  // outside [0, n_slots): the row is not written
+  void *k_pages, *v_pages, *k_scales, *v_scales;
+  int rows, Hkv;
+  long long k_stride, v_stride, n_slots;
+};
+struct CacheReadArgs {
+  const void *k_pages, *v_pages, *k_scales, *v_scales;
+  const int *table, *lens, *starts;  // starts: [B] or NULL (all 0)
+  void *k_out, *v_out;
+  int B, T, Hkv;
+  long long k_stride, v_stride;
+  int num_pages, page, max_pages;
+  bool zero_rest;  // rows behind a sequence's end: zeros, else left as they are
+};
+long long cache_read_blocks(int T, int Hkv, int dh);  // workgroups per sequence
+hipError_t launch_cache_quantize(const CacheWriteArgs &a, int dh, int io, hipStream_t s);
+hipError_t launch_cache_dequantize(const CacheReadArgs &a, int dh, int io, hipStream_t s);
 
 // Per-head RMS norm (weights NULL: none) and rotation of q and k; with slots also into the cache
 // (rows whose slot is not in [0, n_slots): not). Strides in elements from row to row.

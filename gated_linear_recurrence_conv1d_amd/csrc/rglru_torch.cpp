@@ -1,4 +1,4 @@
-// rglru_torch.cpp -- the binding's checks of the local attention block's tensors, and its calls of the C ABI
+// rglru_torch.cpp -- the binding's checks of the attention block's and the serving operators' tensors, and its calls of the C ABI
 // (include/rglru.h), as a CPython module. In Python the checks of a dozen tensors take longer than the
 // kernels of a decoding step (17 us against 4 for the norms of 64 tokens); here they are reads of tensor
 // fields, and new tensors are made without the arguments of torch.empty (0.5 us each instead of 1.2).
@@ -333,6 +333,210 @@ PyObject *paged_attention(PyObject *, PyObject *const *a, Py_ssize_t n) {
   });
 }
 
+// ---- serving
+constexpr c10::ScalarType kE4m3 = at::kFloat8_e4m3fn, kE8m0 = at::kFloat8_e8m0fnu;
+
+// An e4m3 cache's sizes, from k_pages.
+struct Pool {
+  int64_t pages[4], scales[3];
+};
+Pool pool_of(PyObject *k_pages) {
+  const at::Tensor &t = Call::tensor(k_pages, "k_pages");
+  if (t.dim() != 4) refuse(PyExc_ValueError, "k_pages: expected [pages, page, Hkv, dh], got " + text(t.sizes()));
+  Pool p;
+  for (int i = 0; i < 4; ++i) p.pages[i] = t.size(i);
+  for (int i = 0; i < 3; ++i) p.scales[i] = t.size(i);
+  return p;
+}
+struct Cache {
+  void *k, *v, *ks, *vs;
+};
+Cache cache_of(Call &c, const Pool &p, PyObject *const *a) {  // k_pages, v_pages, k_scales, v_scales
+  for (int i = 0; i < 4; ++i) Call::tensor(a[i], "cache");    // (none is optional)
+  return {c.flat(a[0], kE4m3, p.pages, "k_pages"), c.flat(a[1], kE4m3, p.pages, "v_pages"),
+          c.flat(a[2], kE8m0, p.scales, "k_scales"), c.flat(a[3], kE8m0, p.scales, "v_scales")};
+}
+
+// (k, v, slots, k_pages, v_pages, k_scales, v_scales, stream)
+PyObject *cache_quantize(PyObject *, PyObject *const *a, Py_ssize_t n) {
+  return guarded(n, 8, [&]() -> long {
+    Call c;
+    const at::Tensor &k = c.first(a[0], "k", 2);
+    const Sizes ks = k.sizes(), lead = ks.slice(0, ks.size() - 2);
+    const Pool p = pool_of(a[3]);
+    if (p.pages[2] != ks[ks.size() - 2] || p.pages[3] != ks[ks.size() - 1])
+      refuse(PyExc_ValueError, "k_pages: expected [pages, page, Hkv, dh] of k's heads, got " + text(p.pages));
+    long long sk, sv;
+    Call::tensor(a[1], "v");
+    Call::tensor(a[2], "slots");
+    void *pk = c.heads(a[0], ks, sk, "k"), *pv = c.heads(a[1], ks, sv, "v");
+    const long long *slots = static_cast<long long *>(c.flat(a[2], at::kLong, lead, "slots"));
+    const Cache m = cache_of(c, p, a + 3);
+    const int64_t rows = k.numel() / std::max<int64_t>(1, p.pages[2] * p.pages[3]);
+    return c.run(rglru_cache_quantize, pk, pv, slots, m.k, m.v, m.ks, m.vs, as_int(rows, "k"),
+                 as_int(p.pages[2], "k"), as_int(p.pages[3], "k"), sk, sv,
+                 static_cast<long long>(p.pages[0]) * p.pages[1], c.dtype(), arg_stream(a[7]));
+  });
+}
+
+// (k_pages, v_pages, k_scales, v_scales, block_table, lens, starts, k_out, v_out, zero_rest, stream)
+PyObject *cache_dequantize(PyObject *, PyObject *const *a, Py_ssize_t n) {
+  return guarded(n, 11, [&]() -> long {
+    Call c;
+    const at::Tensor &out = c.first(a[7], "k_out", 3), &table = Call::tensor(a[4], "block_table");
+    const Sizes os = out.sizes();
+    const Pool p = pool_of(a[0]);
+    if (os.size() != 4 || os[2] != p.pages[2] || os[3] != p.pages[3])
+      refuse(PyExc_ValueError, "k_out: expected [B, T, Hkv, dh] of the cache's heads, got shape " + text(os));
+    if (table.dim() != 2)
+      refuse(PyExc_ValueError, "block_table: expected [B, max_pages], got " + text(table.sizes()));
+    const int64_t tab[] = {os[0], table.size(1)}, per_seq[] = {os[0]};
+    long long sk, sv;
+    Call::tensor(a[5], "lens");
+    Call::tensor(a[8], "v_out");
+    const Cache m = cache_of(c, p, a);
+    const int *bt = static_cast<int *>(c.flat(a[4], at::kInt, tab, "block_table"));
+    const int *lens = static_cast<int *>(c.flat(a[5], at::kInt, per_seq, "lens"));
+    const int *starts = static_cast<int *>(c.flat(a[6], at::kInt, per_seq, "starts"));
+    void *ko = c.heads(a[7], os, sk, "k_out"), *vo = c.heads(a[8], os, sv, "v_out");
+    return c.run(rglru_cache_dequantize, m.k, m.v, m.ks, m.vs, bt, lens, starts, ko, vo, as_int(os[0], "k_out"),
+                 as_int(os[1], "k_out"), as_int(os[2], "k_out"), as_int(os[3], "k_out"), sk, sv,
+                 as_int(p.pages[0], "k_pages"), as_int(p.pages[1], "k_pages"), as_int(tab[1], "block_table"),
+                 a[9] == Py_True ? 1 : 0, c.dtype(), arg_stream(a[10]));
+  });
+}
+
+void want_bf16(const Call &c, const char *name) {
+  if (c.io() != at::kBFloat16)
+    refuse(PyExc_ValueError, std::string(name) + ": expected torch.bfloat16, got " + text(c.io()));
+}
+
+// (q, k_pages, v_pages, k_scales, v_scales, block_table, lens, o, window, sinks, scale, workspace, stream)
+PyObject *paged_attention_e4m3(PyObject *, PyObject *const *a, Py_ssize_t n) {
+  return guarded(n, 13, [&]() -> long {
+    Call c;
+    const at::Tensor &qt = c.first(a[0], "q", 3), &table = Call::tensor(a[5], "block_table");
+    want_bf16(c, "q");
+    if (qt.dim() != 3) refuse(PyExc_ValueError, "q: expected [N, Hq, dh], got shape " + text(qt.sizes()));
+    const Sizes qs = qt.sizes();
+    Pool p = pool_of(a[1]);
+    p.pages[3] = qs[2];
+    if (table.dim() != 2)
+      refuse(PyExc_ValueError, "block_table: expected [N, max_pages], got " + text(table.sizes()));
+    const int64_t tab[] = {qs[0], table.size(1)}, per_seq[] = {qs[0]};
+    long long sq;
+    void *q = c.heads(a[0], qs, sq, "q");
+    const Cache m = cache_of(c, p, a + 1);
+    const int *bt = static_cast<int *>(c.flat(a[5], at::kInt, tab, "block_table"));
+    const int *lens = static_cast<int *>(c.flat(a[6], at::kInt, per_seq, "lens"));
+    void *o = c.flat(a[7], c.io(), qs, "o");
+    size_t bytes;
+    void *ws = c.workspace(a[11], bytes);
+    return c.run(rglru_paged_attention_e4m3, q, m.k, m.v, m.ks, m.vs, bt, lens, o, as_int(qs[0], "q"),
+                 as_int(qs[1], "q"), as_int(p.pages[2], "k_pages"), as_int(qs[2], "q"), sq,
+                 as_int(p.pages[0], "k_pages"), as_int(p.pages[1], "k_pages"), as_int(tab[1], "block_table"),
+                 arg_int(a[8]), arg_int(a[9]), arg_float(a[10]), ws, bytes, arg_stream(a[12]));
+  });
+}
+
+// (q, k_pages, v_pages, k_scales, v_scales, prefix_table, prefix_len, block_table, lens, o, window, sinks, scale,
+//  workspace, stream)
+PyObject *prefix_attention(PyObject *, PyObject *const *a, Py_ssize_t n) {
+  return guarded(n, 15, [&]() -> long {
+    Call c;
+    const at::Tensor &qt = c.first(a[0], "q", 3), &table = Call::tensor(a[7], "block_table"),
+                     &prefix = Call::tensor(a[5], "prefix_table");
+    if (qt.dim() != 3) refuse(PyExc_ValueError, "q: expected [N, Hq, dh], got shape " + text(qt.sizes()));
+    const Sizes qs = qt.sizes();
+    Pool p = pool_of(a[1]);
+    p.pages[3] = qs[2];
+    if (table.dim() != 2)
+      refuse(PyExc_ValueError, "block_table: expected [N, max_pages], got " + text(table.sizes()));
+    if (prefix.dim() != 1)
+      refuse(PyExc_ValueError, "prefix_table: expected [prefix_pages], got " + text(prefix.sizes()));
+    const int64_t tab[] = {qs[0], table.size(1)}, per_seq[] = {qs[0]}, shared[] = {prefix.size(0)}, one[] = {1};
+    long long sq;
+    void *q = c.heads(a[0], qs, sq, "q");
+    if ((a[3] == Py_None) != (a[4] == Py_None)) refuse(PyExc_ValueError, "k_scales, v_scales: both or none");
+    const Cache m = a[3] == Py_None ? Cache{c.flat(a[1], c.io(), p.pages, "k_pages"),
+                                            c.flat(a[2], c.io(), p.pages, "v_pages"), nullptr, nullptr}
+                                    : cache_of(c, p, a + 1);
+    const int *pt = static_cast<int *>(c.flat(a[5], at::kInt, shared, "prefix_table"));
+    const int *pl = static_cast<int *>(c.flat(a[6], at::kInt, one, "prefix_len"));
+    const int *bt = static_cast<int *>(c.flat(a[7], at::kInt, tab, "block_table"));
+    const int *lens = static_cast<int *>(c.flat(a[8], at::kInt, per_seq, "lens"));
+    void *o = c.flat(a[9], c.io(), qs, "o");
+    size_t bytes;
+    void *ws = c.workspace(a[13], bytes);
+    return c.run(rglru_prefix_attention, q, m.k, m.v, m.ks, m.vs, pt, pl, bt, lens, o, as_int(qs[0], "q"),
+                 as_int(qs[1], "q"), as_int(p.pages[2], "k_pages"), as_int(qs[2], "q"), sq,
+                 as_int(p.pages[0], "k_pages"), as_int(p.pages[1], "k_pages"), as_int(shared[0], "prefix_table"),
+                 as_int(tab[1], "block_table"), arg_int(a[10]), arg_int(a[11]), arg_float(a[12]), c.dtype(), ws, bytes,
+                 arg_stream(a[14]));
+  });
+}
+
+// log_decay: [H], or one value of each row and head.
+const float *decays(Call &c, PyObject *o, Sizes lead, int64_t H, int &gated) {
+  const at::Tensor &t = Call::tensor(o, "log_decay");
+  Shape per_row(lead.begin(), lead.end());
+  per_row.push_back(H);
+  gated = t.dim() == 1 ? 0 : 1;
+  const int64_t per_head[] = {H};
+  return static_cast<float *>(c.flat(o, at::kFloat, gated ? Sizes(per_row) : Sizes(per_head), "log_decay"));
+}
+
+// (q, k, v, log_decay, lens, state, o, state_out, scale, workspace, stream)
+PyObject *linear_attention(PyObject *, PyObject *const *a, Py_ssize_t n) {
+  return guarded(n, 11, [&]() -> long {
+    Call c;
+    const at::Tensor &q = c.first(a[0], "q", 3), &v = Call::tensor(a[2], "v");
+    if (q.dim() != 4) refuse(PyExc_ValueError, "q: expected [B, T, Hk, dk], got shape " + text(q.sizes()));
+    if (v.dim() != 4) refuse(PyExc_ValueError, "v: expected [B, T, H, dv], got shape " + text(v.sizes()));
+    const Sizes qs = q.sizes();
+    const int64_t B = qs[0], T = qs[1], Hk = qs[2], dk = qs[3], H = v.size(2), dv = v.size(3);
+    const int64_t vs[] = {B, T, H, dv}, st[] = {B, H, dk, dv}, per_seq[] = {B};
+    long long sq, sk, sv;
+    Call::tensor(a[1], "k");
+    void *pq = c.heads(a[0], qs, sq, "q"), *pk = c.heads(a[1], qs, sk, "k"), *pv = c.heads(a[2], vs, sv, "v");
+    int gated;
+    const float *g = decays(c, a[3], qs.slice(0, 2), H, gated);
+    const int *lens = static_cast<int *>(c.flat(a[4], at::kInt, per_seq, "lens"));
+    const float *s0 = static_cast<float *>(c.flat(a[5], at::kFloat, st, "state"));
+    void *o = c.flat(a[6], c.io(), vs, "o");
+    float *so = static_cast<float *>(c.flat(a[7], at::kFloat, st, "state_out"));
+    size_t bytes;
+    void *ws = c.workspace(a[9], bytes);
+    return c.run(rglru_linear_attention, pq, pk, pv, g, lens, s0, o, so, as_int(B, "q"), as_int(T, "q"),
+                 as_int(Hk, "q"), as_int(H, "v"), as_int(dk, "q"), as_int(dv, "v"), sq, sk, sv, gated,
+                 arg_float(a[8]), c.dtype(), ws, bytes, arg_stream(a[10]));
+  });
+}
+
+// (q, k, v, log_decay, state, state_out, o, scale, stream)
+PyObject *linear_attention_step(PyObject *, PyObject *const *a, Py_ssize_t n) {
+  return guarded(n, 9, [&]() -> long {
+    Call c;
+    const at::Tensor &q = c.first(a[0], "q", 3), &v = Call::tensor(a[2], "v");
+    if (q.dim() != 3) refuse(PyExc_ValueError, "q: expected [N, Hk, dk], got shape " + text(q.sizes()));
+    if (v.dim() != 3) refuse(PyExc_ValueError, "v: expected [N, H, dv], got shape " + text(v.sizes()));
+    const Sizes qs = q.sizes();
+    const int64_t N = qs[0], Hk = qs[1], dk = qs[2], H = v.size(1), dv = v.size(2);
+    const int64_t vs[] = {N, H, dv}, st[] = {N, H, dk, dv};
+    long long sq, sk, sv;
+    Call::tensor(a[1], "k");
+    void *pq = c.heads(a[0], qs, sq, "q"), *pk = c.heads(a[1], qs, sk, "k"), *pv = c.heads(a[2], vs, sv, "v");
+    int gated;
+    const float *g = decays(c, a[3], qs.slice(0, 1), H, gated);
+    const float *s0 = static_cast<float *>(c.flat(a[4], at::kFloat, st, "state"));
+    float *so = static_cast<float *>(c.flat(a[5], at::kFloat, st, "state_out"));
+    void *o = c.flat(a[6], c.io(), vs, "o");
+    return c.run(rglru_linear_attention_step, pq, pk, pv, g, s0, so, o, as_int(N, "q"), as_int(Hk, "q"),
+                 as_int(H, "v"), as_int(dk, "q"), as_int(dv, "v"), sq, sk, sv, gated, arg_float(a[7]), c.dtype(),
+                 arg_stream(a[8]));
+  });
+}
+
 template <typename F> PyObject *made(F f) {
   try {
     return THPVariable_Wrap(f());
@@ -367,7 +571,10 @@ PyObject *empty_bytes(PyObject *, PyObject *const *a, Py_ssize_t n) {
   { #f, reinterpret_cast<PyCFunction>(reinterpret_cast<void (*)()>(f)), METH_FASTCALL, nullptr }
 PyMethodDef methods[] = {RGLRU_METHOD(qk_norm_rope),    RGLRU_METHOD(qk_norm_rope_backward),
                          RGLRU_METHOD(local_attention), RGLRU_METHOD(local_attention_backward),
-                         RGLRU_METHOD(paged_attention), RGLRU_METHOD(empty_as),
+                         RGLRU_METHOD(paged_attention), RGLRU_METHOD(cache_quantize),
+                         RGLRU_METHOD(cache_dequantize), RGLRU_METHOD(paged_attention_e4m3),
+                         RGLRU_METHOD(prefix_attention), RGLRU_METHOD(linear_attention),
+                         RGLRU_METHOD(linear_attention_step), RGLRU_METHOD(empty_as),
                          RGLRU_METHOD(empty_bytes),     {nullptr, nullptr, 0, nullptr}};
 PyModuleDef module = {PyModuleDef_HEAD_INIT, "_rglru_torch", nullptr, -1, methods, nullptr, nullptr, nullptr, nullptr};
 

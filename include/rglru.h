@@ -353,6 +353,111 @@ rglru_status rglru_paged_attention(const void *q, const void *k_pages, const voi
                                    float scale, rglru_dtype dt, void *workspace,
                                    size_t workspace_bytes, void *stream);
 
+/* ---- Serving: a paged cache in 8 bits, a prefix that sequences share, and linear attention.
+ * Conventions as for the attention block above. */
+
+/* Keys and values into a paged cache of e4m3 values (1 sign, 4 exponent and 3 fraction bits, largest 448) with a
+ * power-of-two scale for each (token, head):
+ *   s = max(2^-117, the smallest power of two with max_i |x_i| / s <= 448),  code_i = e4m3(x_i / s), to nearest even.
+ * The division is exact, so the codes are defined to the bit; code_i * s is exact in bf16 and fp32 (values from
+ * 1.9375 * 2^127 on read back as infinity). A row of a head that holds an infinity or a NaN gets the scale NaN: all of
+ * it reads back as NaN.
+ *  k, v [rows][Hkv][dh] dtype (f32 or bf16), *_stride elements from row to row, rows 16-byte aligned
+ *  slots [rows] int64: row r goes to row slots[r] of the cache (slot = page * page size + offset). A slot outside
+ *    [0, n_slots) writes nothing; rows of one call must not share a slot (if they do, what that slot holds is undefined)
+ *  k_pages, v_pages [n_slots][Hkv][dh] e4m3, 16-byte aligned; k_scales, v_scales [n_slots][Hkv] e8m0 (exponent + 127
+ *    in a byte, 255 is NaN); contiguous, in/out: rows that no slot names are left as they are
+ * dh in {64, 128, 256}, n_slots < 2^31 - 256. Outputs must not overlap the inputs or each other. */
+rglru_status rglru_cache_quantize(const void *k, const void *v, const long long *slots, void *k_pages, void *v_pages,
+                                  void *k_scales, void *v_scales, int rows, int Hkv, int dh, long long k_stride,
+                                  long long v_stride, long long n_slots, rglru_dtype dt, void *stream);
+
+/* The way back: row t of sequence b becomes token starts[b] + t (code * scale, exact; under scales below 2^-117, which
+ * are not written above, values below 2^-126 may come as 0), for the prompt's attention over what an earlier chunk has
+ * left in the cache.
+ *  k_pages .. v_scales [num_pages][page_size][Hkv][dh] and [num_pages][page_size][Hkv], as above
+ *  block_table [B][max_pages] int32, lens [B] int32: the tokens that a sequence has; starts [B] int32 or NULL (all 0)
+ *  k_out, v_out [B][T][Hkv][dh] dtype (f32 or bf16), out, *_stride elements from row to row (a sequence's rows are
+ *    T * stride apart from the next one's), rows 16-byte aligned
+ *  zero_rest  rows t >= lens[b] - starts[b]: zeros, or (0) left as they are
+ * A sequence whose start is negative or whose length is negative or over max_pages * page_size becomes NaN in all T
+ * rows; a token on a page outside [0, num_pages) becomes NaN. Nothing outside the pool is read. dh in {64, 128, 256}. */
+rglru_status rglru_cache_dequantize(const void *k_pages, const void *v_pages, const void *k_scales,
+                                    const void *v_scales, const int *block_table, const int *lens, const int *starts,
+                                    void *k_out, void *v_out, int B, int T, int Hkv, int dh, long long k_stride,
+                                    long long v_stride, int num_pages, int page_size, int max_pages, int zero_rest,
+                                    rglru_dtype dt, void *stream);
+
+/* rglru_paged_attention over that cache: k_pages, v_pages in e4m3 with k_scales, v_scales [num_pages][page_size][Hkv]
+ * in e8m0; q and o bf16. Everything else is the same; the cached values enter both contractions exactly. */
+size_t rglru_paged_attention_e4m3_workspace_size(int N, int Hq, int Hkv, int dh, int page_size, int max_pages,
+                                                 int window, int sinks);
+rglru_status rglru_paged_attention_e4m3(const void *q, const void *k_pages, const void *v_pages, const void *k_scales,
+                                        const void *v_scales, const int *block_table, const int *lens, void *o, int N,
+                                        int Hq, int Hkv, int dh, long long q_stride, int num_pages, int page_size,
+                                        int max_pages, int window, int sinks, float scale, void *workspace,
+                                        size_t workspace_bytes, void *stream);
+
+/* rglru_paged_attention for sequences that share a prefix, whose keys and values the cache holds once and which is read
+ * once for all of them. Sequence n's tokens are the prefix_len[0] of the prefix and then lens[n] of its own, the new
+ * one the last of them; token u of the prefix lies in row u % page_size of page prefix_table[u / page_size], own token
+ * j (position prefix_len[0] + j) in page block_table[n][j / page_size]. With L = prefix_len[0] + lens[n], position u is
+ * visible if u >= L - window or u < sinks.
+ *  q [N][Hq][dh] bf16, q_stride elements from row to row, 16-byte aligned rows; o [N][Hq][dh] bf16, contiguous, out
+ *  k_pages, v_pages [num_pages][page_size][Hkv][dh] bf16, or e4m3 with k_scales, v_scales [num_pages][page_size][Hkv]
+ *    in e8m0 (both or neither NULL)
+ *  prefix_table [prefix_pages], prefix_len [1], block_table [N][max_pages], lens [N] int32, on the device
+ *  workspace  at least rglru_prefix_attention_workspace_size() bytes
+ * L = 0: o = 0. A prefix length that is negative or over prefix_pages * page_size makes every row NaN; a row whose own
+ * length is negative or over max_pages * page_size, or that needs a page outside [0, num_pages), becomes NaN. Nothing
+ * outside the pool is read. An infinite or NaN k or v reaches the rows that see it and no others. Softmax and both
+ * contractions accumulate in fp32, the probabilities enter the second one as bf16 hi + lo. Sums are taken in a fixed
+ * order: results are bitwise reproducible. Supported: dt = RGLRU_BF16, dh in {64, 128, 256}, Hq % Hkv == 0, any
+ * page_size >= 1, prefix_pages, max_pages and num_pages times page_size below 2^31 - 256. */
+size_t rglru_prefix_attention_workspace_size(int N, int Hq, int Hkv, int dh, int page_size, int prefix_pages,
+                                             int max_pages, int window, int sinks);
+rglru_status rglru_prefix_attention(const void *q, const void *k_pages, const void *v_pages, const void *k_scales,
+                                    const void *v_scales, const int *prefix_table, const int *prefix_len,
+                                    const int *block_table, const int *lens, void *o, int N, int Hq, int Hkv, int dh,
+                                    long long q_stride, int num_pages, int page_size, int prefix_pages, int max_pages,
+                                    int window, int sinks, float scale, rglru_dtype dt, void *workspace,
+                                    size_t workspace_bytes, void *stream);
+
+/* Causal linear attention with a decay for each head: the gated recurrence with a matrix for a state,
+ *   S_t = exp(g_t) S_{t-1} + k_t v_t^T,   o_t = scale S_t^T q_t,
+ * over prompts (in chunks, on the matrix cores), from a state and to a state. Value head h reads query and key head
+ * h / (H / Hk). Forward only, for serving.
+ *  q, k [B][T][Hk][dk], v [B][T][H][dv] bf16, *_stride elements from token to token (a multiple of 8; a sequence's
+ *    tokens are T * stride apart from the next one's), 16-byte aligned
+ *  log_decay f32: gated = 0: [H], g_t constant; else [B][T][H]. Meant to be <= 0; below -104 (-inf: the state is
+ *    forgotten) it counts as -104, whose exponential is 0 in fp32
+ *  lens [B] int32 or NULL (all T); values are taken into [0, T]. Rows t >= lens[b]: o = 0, and nothing in those rows of
+ *    q, k, v and log_decay is used (they may hold anything)
+ *  s0 [B][H][dk][dv] f32 or NULL (zeros); s_out the same or NULL, out: S after the last token (s0 if there is none); may
+ *    be s0 itself
+ *  o [B][T][H][dv] bf16, contiguous, out
+ *  scale > 0, or 0 for 1/sqrt(dk)
+ *  workspace  at least rglru_linear_attention_workspace_size() bytes (NULL if that is 0)
+ * The state, all sums and all decays are fp32. Operands of the contractions that are not inputs enter as sums of bf16
+ * terms: the decayed scores and the state as two (about 16 bits), the decayed values that form the state as three (24
+ * bits). Sums are taken in a fixed order: results are bitwise reproducible. An infinite or NaN input reaches the rows
+ * from its own token on. Outputs must not overlap the inputs (but for s_out = s0) or each other. Supported: dt =
+ * RGLRU_BF16, dk, dv in {64, 128, 256}, H % Hk == 0, strides <= 2^20. */
+size_t rglru_linear_attention_workspace_size(int B, int T, int Hk, int H, int dk, int dv);
+rglru_status rglru_linear_attention(const void *q, const void *k, const void *v, const float *log_decay,
+                                    const int *lens, const float *s0, void *o, float *s_out, int B, int T, int Hk,
+                                    int H, int dk, int dv, long long q_stride, long long k_stride, long long v_stride,
+                                    int gated, float scale, rglru_dtype dt, void *workspace, size_t workspace_bytes,
+                                    void *stream);
+
+/* One token of the same recurrence for N independent sequences: q, k [N][Hk][dk], v [N][H][dv] (rows as above),
+ * log_decay [H], or [N][H] if gated; s_in, s_out [N][H][dk][dv] f32 (s_out may be s_in: in place); o [N][H][dv]. fp32
+ * throughout. With s_in = rglru_linear_attention's s_out it continues that prompt. */
+rglru_status rglru_linear_attention_step(const void *q, const void *k, const void *v, const float *log_decay,
+                                         const float *s_in, float *s_out, void *o, int N, int Hk, int H, int dk, int dv,
+                                         long long q_stride, long long k_stride, long long v_stride, int gated,
+                                         float scale, rglru_dtype dt, void *stream);
+
 /* Bytes of device workspace rglru_backward needs for this shape (0 when the shape is invalid).
  * About 4 B (bf16) or 8 B (fp32) of pre-activations, the same again of gate gradients and 4 B of
  * conv-output gradient per element of x, plus chunk summaries and partial sums. */

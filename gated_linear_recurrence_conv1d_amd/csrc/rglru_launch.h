@@ -204,7 +204,8 @@ struct LinearArgs {
   float scale;
   bool gated;
   int segs, seg_len;
-  int run;  // segments of a launch (set by the launcher)
+  int run;       // segments of a launch, and
+  bool chained;  // whether seg holds what each segment starts from (both set by the launcher)
 };
 struct LinearPlan {
   int segs, seg_len;

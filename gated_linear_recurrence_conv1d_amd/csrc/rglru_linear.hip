@@ -9,17 +9,18 @@
 // strong decays only underflow.
 //
 // linear_fwd: a workgroup walks the chunks of one (sequence, head, slice of up to 128 values, segment); each wave
-// keeps S for 32 of the values (dk x 32 in accumulators). Per chunk, on 32x32x16 MFMAs:
-//   P^T = K Q^T, its three causal 32x32 tiles shared among the waves, decayed, and handed round in LDS as the next
+// keeps S for 16 of the values (dk x 16 in accumulators). Per chunk, on 16x16x32 MFMAs:
+//   P^T = K Q^T, its ten causal 16x16 tiles shared among the waves, decayed, and handed round in LDS as the next
 //     product's operand;
-//   O^T = S^T Q^T: S is the operand straight from its accumulators, as Q takes its k index in their row order;
+//   O^T = S^T Q^T: S is the operand straight from its accumulators, as Q lies in their row order;
 //   O^T += V^T P^T and S += K^T (w V), V and K read from LDS transposed, V once for both.
 // S and P enter as bf16 hi + lo and w V as three bf16 terms (8 + 8 + 8 bits): the state is an fp32 result and o is
 // then within the rounding of its own type; with one term each, o would be off by as much again for each of them.
 //
-// With few (sequence, head, slice)s the prompt is cut into segments: linear_fwd<.., STATE> first forms each
-// segment's own state (K and V only), linear_carry chains them (from a copy of the first state: the last one may go
-// where that is), and linear_fwd starts each segment from its state.
+// With few (sequence, head, slice)s the prompt is cut into segments: linear_state first forms each segment's own state (K
+// and V only), and linear_fwd starts each segment from the chain of those before it: up to kFew segments it forms the
+// chain itself (they are read 1.5 times on average; at B8 T2048 H16 with 4, 9.5 us of a launch less), else linear_carry
+// has done so in place.
 #include "rglru_attn.h"
 #include "rglru_grid.h"
 #include "rglru_launch.h"
@@ -33,6 +34,7 @@ using namespace attn;
 namespace {
 
 constexpr int kC = 64;              // tokens per chunk
+constexpr int kFew = 4;             // segments that are chained where they are needed
 constexpr float kLeast = -104.0f;   // exp of it is 0 in fp32: a smaller log decay (-inf: forget) counts as this
 
 // Inclusive running sum over the 64 lanes.
@@ -60,6 +62,12 @@ __device__ __forceinline__ u32x4_t split(float (&x)[8]) {
   }
   return h;
 }
+__device__ __forceinline__ u32x4_t rounded(const float (&x)[8]) {
+  u32x4_t h;
+#pragma unroll
+  for (int i = 0; i < 4; ++i) h[i] = pack_bf16x2(x[2 * i], x[2 * i + 1]);
+  return h;
+}
 
 typedef __attribute__((address_space(3))) uint16_t lds_u16_t;
 
@@ -72,239 +80,440 @@ __device__ __forceinline__ bool not_finite(u32x4_t v) {
   return top[0] >= 0x7F80 || top[1] >= 0x7F80;
 }
 
-__device__ __forceinline__ f32x16_t mfma(u32x4_t a, u32x4_t b, f32x16_t c) {
-  return __builtin_amdgcn_mfma_f32_32x32x16_bf16(__builtin_bit_cast(bf16x8_t, a), __builtin_bit_cast(bf16x8_t, b), c, 0,
+__device__ __forceinline__ f32x4_t mfma(u32x4_t a, u32x4_t b, f32x4_t c) {
+  return __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8_t, a), __builtin_bit_cast(bf16x8_t, b), c, 0,
                                                  0, 0);
 }
 
 }  // namespace
 
-// STATE: only the state at the segment's end from a zero one (into the next one's a.seg), and the segment's summed g (a.sums).
-template <int DK, int DVS, bool STATE>
-__global__ __launch_bounds__(DVS * 2, DK == 256 ? 1 : 2) void linear_fwd(LinearArgs a) {
-  constexpr int NW = DVS / 32;
-  typedef Blk<DK, NW> KB;
-  typedef Blk<DVS, NW> VB;
-  constexpr int kQB = 2 * KB::kBytes, kVB = 2 * VB::kBytes;  // 64 rows
-  // the product's operands as lanes read them: [tile][step][lane], tiles (t0, s0), (t1, s0), (t1, s1), hi then lo
-  constexpr int kPB = 3 * 2 * 64 * 16;
-  __shared__ __attribute__((aligned(1024))) unsigned char smem[(STATE ? 1 : 2) * kQB + kVB + (STATE ? 0 : 2 * kPB)];
-  __shared__ __attribute__((aligned(16))) float sb[NW][3][kC];  // each wave's own: b, scale exp(b), exp(b_63 - b)
+// 64 rows of DH bf16 in LDS, 64 bytes apart beyond their length, the 16-byte chunk c of each 64 bytes of row r at c ^
+// turn(r): the 16 rows at one chunk of a pass, and 8 rows at 2 neighbouring chunks of another, fall on different banks,
+// and the steps along a row are constant offsets. Lanes are c = lane % 16, g = lane / 16.
+template <int DH, int NT> struct Rows64 {
+  static constexpr unsigned kStride = 2 * DH + 64, kBytes = kC * kStride;
+  static constexpr int kCPR = DH / 8, kN = kC * kCPR / NT;  // 16-byte chunks per row; per thread
+  static constexpr int kRows = NT / kCPR;                   // rows that one of the threads' chunks covers
+  // the chunks of rows `base` .. from memory, rows from `rows` on as zeros
+  // (here and in put the thread's terms are formed anew: kept through the walk, they take its registers)
+  __device__ __forceinline__ static void load(u32x4_t (&x)[kN], const bf16_t *base, unsigned row_bytes, int rows, int tid) {
+    asm volatile("" : "+v"(tid));
+    const auto src = __builtin_amdgcn_make_buffer_rsrc(
+        const_cast<bf16_t *>(wave_uniform(base)), static_cast<short>(0),
+        rows > 0 ? static_cast<int>(row_bytes * static_cast<unsigned>(min(rows, kC) - 1)) + DH * 2 : 0, kRawWord3);
+    const unsigned at = static_cast<unsigned>(tid / kCPR) * row_bytes + (tid % kCPR) * 16;
+#pragma unroll
+    for (int i = 0; i < kN; ++i)
+      x[i] = __builtin_bit_cast(u32x4_t, __builtin_amdgcn_raw_buffer_load_b128(src, at + i * kRows * row_bytes, 0, 0));
+  }
+  __device__ __forceinline__ static int turn(int r) { return 2 * ((r >> 2) & 1) + ((r >> 3) & 1); }
+  __device__ __forceinline__ static unsigned chunk(int r, int c) {  // of row r, its place
+    return r * kStride + (c >> 2) * 64 + (((c & 3) ^ turn(r)) * 16);
+  }
+  // thread's chunk i is of row tid / kCPR + kRows i: its turn comes again after 16 rows
+  static constexpr int kPar = kRows < 16 ? 16 / kRows : 1;
+  __device__ __forceinline__ static void put(const u32x4_t (&x)[kN], unsigned lds, int tid) {
+    asm volatile("" : "+v"(tid));
+#pragma unroll
+    for (int i = 0; i < kN; ++i) {
+      const int p = i % kPar;
+      *(lds_u32x4_t *)static_cast<uintptr_t>(lds + chunk(tid / kCPR + kRows * p, tid % kCPR) + (i - p) * kRows * kStride) =
+          x[i];
+    }
+  }
+  // put with the order of two accumulators' rows in each 32 values: chunk g has 4 g .. 4 g + 3 and 16 + 4 g .. 16 + 4 g + 3
+  __device__ __forceinline__ static void put_paired(const u32x4_t (&x)[kN], unsigned lds, int tid) {
+    asm volatile("" : "+v"(tid));
+    const int r = tid / kCPR, c = tid % kCPR, to = (c & ~3) + 2 * (c & 1);
+#pragma unroll
+    for (int i = 0; i < kN; ++i) {
+      const int p = i % kPar;
+      const unsigned at = lds + (i - p) * kRows * kStride + 8 * ((c >> 1) & 1);
+      *(lds_u32x2_t *)static_cast<uintptr_t>(at + chunk(r + kRows * p, to)) = u32x2_t{x[i][0], x[i][1]};
+      *(lds_u32x2_t *)static_cast<uintptr_t>(at + chunk(r + kRows * p, to + 1)) = u32x2_t{x[i][2], x[i][3]};
+    }
+  }
+  // operand, row c of the 16 at `lds`, k = what lies at values 32 st + 8 g ..
+  __device__ __forceinline__ static unsigned row_lane(int lane) { return chunk(lane & 15, lane >> 4); }
+  __device__ __forceinline__ static u32x4_t rows(unsigned lds, unsigned l, int st) {
+    return *(lds_u32x4_t *)static_cast<uintptr_t>(l + lds + 64 * st);
+  }
+  // the same of rows as they came, k in the paired order
+  struct PairLane {
+    unsigned at[2];
+  };
+  __device__ __forceinline__ static PairLane pair_lane(int lane) {
+    const int r = lane & 15, g = lane >> 4;
+    return {{chunk(r, g >> 1) + 8 * (g & 1), chunk(r, 2 + (g >> 1)) + 8 * (g & 1)}};
+  }
+  __device__ __forceinline__ static u32x4_t pairs(unsigned lds, const PairLane &l, int st) {
+    const u32x2_t a = *(lds_u32x2_t *)static_cast<uintptr_t>(l.at[0] + lds + 64 * st),
+                  b = *(lds_u32x2_t *)static_cast<uintptr_t>(l.at[1] + lds + 64 * st);
+    return u32x4_t{a[0], a[1], b[0], b[1]};
+  }
+  // operand, column 16 j + c, k = rows 32 st + 4 g .. and 32 st + 16 + 4 g ..: two accumulators' row order
+  struct ColLane {
+    unsigned at[2];
+  };
+  __device__ __forceinline__ static ColLane col_lane(int lane) {
+    const int r = 4 * (lane >> 4) + ((lane & 15) >> 2), c = (lane & 3) >> 1;
+    return {{chunk(r, c) + 8 * (lane & 1), chunk(r, 2 + c) + 8 * (lane & 1)}};
+  }
+  __device__ __forceinline__ static u32x4_t cols(unsigned lds, unsigned l, int st) {
+    const uint2 x = __builtin_bit_cast(uint2, __builtin_amdgcn_ds_read_tr16_b64_v4i16(
+                                                  (lds_i16x4_t *)static_cast<uintptr_t>(l + lds + 32 * st * kStride)));
+    const uint2 y = __builtin_bit_cast(
+        uint2, __builtin_amdgcn_ds_read_tr16_b64_v4i16(
+                   (lds_i16x4_t *)static_cast<uintptr_t>(l + lds + (32 * st + 16) * kStride)));
+    return u32x4_t{x.x, x.y, y.x, y.y};
+  }
+  __device__ __forceinline__ static u32x4_t cols(unsigned lds, const ColLane &l, int st, int j) {
+    return cols(lds + 64 * (j >> 1), l.at[j & 1], st);
+  }
+  // one value, for the few that are read alone
+  __device__ __forceinline__ static float value(unsigned lds, int r, int d) {
+    return bf16_to_f32(*(lds_u16_t *)static_cast<uintptr_t>(lds + chunk(r, d >> 3) + 2 * (d & 7)));
+  }
+};
+
+// The decayed scores in LDS, as lanes read them: operand of (16 tokens j, 32 earlier ones p <= j / 2), hi then lo.
+constexpr unsigned kScores = 6 * 64 * 16;
+__device__ __forceinline__ constexpr unsigned scores_of(int j, int p) { return (j < 2 ? j : 2 * j - 2 + p) * 1024; }
+
+// O^T += V^T P^T of each 16 tokens' own 32, one token at a time, in fp32. (The lane's terms are formed here: kept, they
+// would take registers from the walk, which hardly ever comes here.)
+template <typename VB> __device__ __forceinline__ void own_tokens(f32x4_t (&O)[4], unsigned ldv, unsigned ldp, int w, int lane) {
+  asm volatile("" : "+v"(lane));
+  const int c = lane & 15, g = lane >> 4;
+#pragma unroll
+  for (int j = 0; j < 4; ++j)
+    for (int s = 0; s < 16 * (1 + (j & 1)); ++s) {
+      const unsigned at = ldp + scores_of(j, j >> 1) + (c + 16 * ((s >> 2) & 3)) * 16 + 8 * (s >> 4) + 2 * (s & 3);
+      const float p = bf16_to_f32(*(lds_u16_t *)static_cast<uintptr_t>(at)) +
+                      bf16_to_f32(*(lds_u16_t *)static_cast<uintptr_t>(at + kScores));
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        const float x = p * VB::value(ldv, 32 * (j >> 1) + s, 16 * w + 4 * g + e);
+        if (s <= 16 * (j & 1) + c) O[j][e] += x;
+      }
+    }
+}
+
+// This workgroup's (sequence, head, slice, segment), and where its tokens are.
+template <int DK, int DVS> struct Place {
+  int b, seg, h, slice, len, t_lo, t_hi, t_end;
+  size_t tok, head;
+  const bf16_t *k, *v;
+  const float *g;
+  size_t g_stride;
+  __device__ __forceinline__ bool find(const LinearArgs &a) {
+    // Heads of one key head, and their slices, one after another: they read the same q and k. Workgroups go to the 8
+    // dies (each with an L2 of its own) in turn, so each die takes one run of them.
+    const int nsl = a.dv / DVS, per = a.H * nsl * a.run, eighth = per * a.B >> 3;
+    int id = block_of(blockIdx.y);
+    if (id < eighth * 8) id = (id & 7) * eighth + (id >> 3);
+    b = uni(id / per);
+    if (b >= a.B) return false;
+    const int r0 = id - b * per;
+    seg = uni(r0 / (a.H * nsl));
+    const int r1 = r0 - seg * a.H * nsl;
+    h = uni(r1 / nsl);
+    slice = r1 - h * nsl;
+    len = clamp_len(a.lens, b, a.T);
+    t_lo = seg * a.seg_len;
+    t_hi = min(a.T, t_lo + a.seg_len);
+    t_end = min(len, t_hi);
+    tok = static_cast<size_t>(b) * a.T;
+    head = static_cast<size_t>(b) * a.H + h;
+    k = static_cast<const bf16_t *>(a.k) + tok * a.k_stride + static_cast<size_t>(key_head(a)) * DK;
+    v = static_cast<const bf16_t *>(a.v) + tok * a.v_stride + static_cast<size_t>(h) * a.dv + slice * DVS;
+    g = a.gated ? a.log_decay + tok * a.H + h : a.log_decay + h;
+    g_stride = a.gated ? a.H : 0;
+    return true;
+  }
+  __device__ __forceinline__ int key_head(const LinearArgs &a) const { return uni(h / (a.H / a.Hk)); }
+  // log decay of token t + lane (behind the segment's last one: any)
+  __device__ __forceinline__ float decay(int t, int lane) const {
+    return g[static_cast<size_t>(min(t + lane, t_end - 1)) * g_stride];
+  }
+  // the running sum of log2 decays, from what decay() has loaded
+  __device__ __forceinline__ float running(float x, int t, int lane) const {
+    return wave_sum_up(t + lane < t_end ? log2_decay(x) : 0.0f);
+  }
+};
+
+// V's operand of 32 tokens, each times its weight, as three bf16 terms.
+struct Weighted {
+  u32x4_t hi, mid, lo;
+};
+__device__ __forceinline__ Weighted weighted(u32x4_t v, const float *w, int st, int g) {
+  float x[8];
+#pragma unroll
+  for (int e = 0; e < 8; ++e)
+    x[e] = (e & 1 ? bf16hi(v[e >> 1]) : bf16lo(v[e >> 1])) * w[32 * st + 16 * (e >> 2) + 4 * g + (e & 3)];
+  Weighted r;
+  r.hi = split(x);
+  r.mid = split(x);
+  r.lo = rounded(x);
+  return r;
+}
+
+// S += K^T (w V) of 64 tokens, four of S's tiles at a time.
+template <int DK, typename KB> __device__ __forceinline__ void add_outer(f32x4_t (&S)[DK / 16], const u32x4_t (&v)[2],
+                                                                         const float *w, unsigned ldk,
+                                                                         const typename KB::ColLane &kl, int g) {
+#pragma unroll
+  for (int st = 0; st < 2; ++st) {
+    const Weighted x = weighted(v[st], w, st, g);
+#pragma unroll
+    for (int n = 0; n < DK / 64; ++n) {
+      f32x4_t *const s = S + 4 * n;
+      u32x4_t kt[4];
+#pragma unroll
+      for (int i = 0; i < 4; ++i) kt[i] = KB::cols(ldk, kl, st, 4 * n + i);
+#pragma unroll
+      for (int i = 0; i < 4; ++i) s[i] = mfma(kt[i], x.hi, s[i]);
+#pragma unroll
+      for (int i = 0; i < 4; ++i) s[i] = mfma(kt[i], x.mid, s[i]);
+#pragma unroll
+      for (int i = 0; i < 4; ++i) s[i] = mfma(kt[i], x.lo, s[i]);
+    }
+  }
+}
+
+// A wave's share of a state to memory and from it: dk = 16 i + 4 g + e of tile i, value c of the 16 from p on. (The
+// lane's terms are formed here: kept from one call for the other, they take registers from the walk.)
+template <int DK> __device__ __forceinline__ void store_state(const f32x4_t (&S)[DK / 16], float *p, int dv) {
+  int lane = threadIdx.x & 63;
+  asm volatile("" : "+v"(lane));
+  float *const at = p + 4 * (lane >> 4) * dv + (lane & 15);
+#pragma unroll
+  for (int i = 0; i < DK / 16; ++i)
+#pragma unroll
+    for (int e = 0; e < 4; ++e) at[static_cast<size_t>(16 * i + e) * dv] = S[i][e];
+}
+template <int DK> __device__ __forceinline__ void load_state(f32x4_t (&S)[DK / 16], const float *p, int dv) {
+  int lane = threadIdx.x & 63;
+  asm volatile("" : "+v"(lane));
+  const float *const at = p + 4 * (lane >> 4) * dv + (lane & 15);
+#pragma unroll
+  for (int i = 0; i < DK / 16; ++i)
+#pragma unroll
+    for (int e = 0; e < 4; ++e) S[i][e] = at[static_cast<size_t>(16 * i + e) * dv];
+}
+
+// Threads of a workgroup, a wave for 16 values; waves a SIMD that the registers have to leave room for.
+constexpr int threads_of(int DVS) { return DVS * 4; }
+constexpr int waves_of(int DK, int DVS) { return (DK == 256 ? 1 : 2) * (DVS / 64); }
+
+// The state of a segment's own tokens at its end (to the next one's a.seg), and its summed g (a.sums). Chunks from the
+// last one back: once what follows has decayed by 2^-150 in all, which is 0 in fp32, no earlier token counts.
+template <int DK, int DVS>
+__global__ __launch_bounds__(threads_of(DVS), waves_of(DK, DVS)) void linear_state(LinearArgs a) {
+  constexpr int NT = threads_of(DVS);
+  typedef Rows64<DK, NT> KB;
+  typedef Rows64<DVS, NT> VB;
+  __shared__ __attribute__((aligned(16))) unsigned char smem[KB::kBytes + VB::kBytes];
+  __shared__ __attribute__((aligned(16))) float sw[DVS / 16][kC];  // each wave's own
+  const int tid = threadIdx.x, lane = tid & 63, w = uni(tid >> 6), g = lane >> 4;
+  const unsigned ldk = lds_addr(smem), ldv = ldk + KB::kBytes;
+  Place<DK, DVS> at;
+  if (!at.find(a)) return;
+  const unsigned krb = static_cast<unsigned>(a.k_stride) * 2, vrb = static_cast<unsigned>(a.v_stride) * 2;
+  f32x4_t S[DK / 16];
+#pragma unroll
+  for (int i = 0; i < DK / 16; ++i) S[i] = f32x4_t{};
+  float later = 0.0f;  // summed log2 decays of the chunks done
+  u32x4_t kx[KB::kN], vx[VB::kN];
+  float gx = 0.0f;
+  auto load = [&](int t) {
+    KB::load(kx, at.k + static_cast<size_t>(t) * a.k_stride, krb, at.t_end - t, tid);
+    VB::load(vx, at.v + static_cast<size_t>(t) * a.v_stride, vrb, at.t_end - t, tid);
+    gx = at.decay(t, lane);
+  };
+  const int n = at.t_end > at.t_lo ? (at.t_end - at.t_lo + kC - 1) / kC : 0;
+  if (n) load(at.t_lo + (n - 1) * kC);
+  const typename KB::ColLane kc = KB::col_lane(lane);
+  const unsigned vc = ldv + 64 * (w >> 1) + (w & 1 ? VB::col_lane(lane).at[1] : VB::col_lane(lane).at[0]);
+  for (int i = n - 1; i >= 0 && !(later <= -150.0f); --i) {
+    KB::put(kx, ldk, tid);
+    VB::put(vx, ldv, tid);
+    const float bt = at.running(gx, at.t_lo + i * kC, lane);
+    const float b_end = __int_as_float(__builtin_amdgcn_readlane(__float_as_int(bt), 63));
+    sw[w][lane] = __builtin_amdgcn_exp2f(b_end - bt + later);
+    later += b_end;
+    lds_barrier();
+    if (i) load(at.t_lo + (i - 1) * kC);
+    u32x4_t v[2];
+#pragma unroll
+    for (int st = 0; st < 2; ++st) v[st] = VB::cols(0, vc, st);
+    add_outer<DK, KB>(S, v, sw[w], ldk, kc, g);
+    lds_barrier();  // everyone is done with the chunk
+  }
+  if (tid == 0 && at.slice == 0) a.sums[at.head * (a.segs - 1) + at.seg] = later;
+  store_state<DK>(S, a.seg + (at.head * a.segs + at.seg + 1) * static_cast<size_t>(DK) * a.dv + at.slice * DVS + 16 * w,
+                  a.dv);
+}
+
+template <int DK, int DVS>
+__global__ __launch_bounds__(threads_of(DVS), waves_of(DK, DVS)) void linear_fwd(LinearArgs a) {
+  constexpr int NW = DVS / 16, NT = threads_of(DVS);
+  typedef Rows64<DK, NT> KB;
+  typedef Rows64<DVS, NT> VB;
+  __shared__ __attribute__((aligned(16))) unsigned char smem[2 * KB::kBytes + VB::kBytes + 2 * kScores];
+  __shared__ __attribute__((aligned(16))) float mb[kC], me[kC], mw[kC];  // b, scale exp(b), exp(b_63 - b)
+  __shared__ float mkeep;                                                // exp(b_63)
   const int tid = threadIdx.x, lane = tid & 63, w = uni(tid >> 6);
-  const int lrow = lane & 31, half = lane >> 5;
-  const unsigned ldk = lds_addr(smem), ldv = ldk + kQB, ldq = ldv + kVB, ldp = ldq + kQB;
-  const int id = block_of(blockIdx.y);
-  const int nsl = a.dv / DVS, per = a.H * nsl * a.run;
-  // (heads of one key head, and their slices, one after another: they read the same q and k)
-  const int b = uni(id / per);
-  if (b >= a.B) return;
-  const int r0 = id - b * per, seg = uni(r0 / (a.H * nsl)), r1 = r0 - seg * a.H * nsl;
-  const int h = uni(r1 / nsl), slice = r1 - h * nsl;
-  const int kh = uni(h / (a.H / a.Hk));
-  const int T = a.T, len = clamp_len(a.lens, b, T);
-  const int t_lo = seg * a.seg_len, t_hi = min(T, t_lo + a.seg_len), t_end = min(len, t_hi);
-  const size_t tok = static_cast<size_t>(b) * T;
-  const bf16_t *const q_ = static_cast<const bf16_t *>(a.q) + tok * a.q_stride + static_cast<size_t>(kh) * DK;
-  const bf16_t *const k_ = static_cast<const bf16_t *>(a.k) + tok * a.k_stride + static_cast<size_t>(kh) * DK;
-  const bf16_t *const v_ = static_cast<const bf16_t *>(a.v) + tok * a.v_stride + static_cast<size_t>(h) * a.dv +
-                           slice * DVS;
-  const float *const g_ = a.gated ? a.log_decay + tok * a.H + h : a.log_decay + h;
-  const size_t g_stride = a.gated ? a.H : 0;
+  const int c = lane & 15, g = lane >> 4;
+  const unsigned ldk = lds_addr(smem), ldv = ldk + KB::kBytes, ldq = ldv + VB::kBytes, ldp = ldq + KB::kBytes;
+  Place<DK, DVS> at;
+  if (!at.find(a)) return;
+  const bf16_t *const q_ = static_cast<const bf16_t *>(a.q) + at.tok * a.q_stride +
+                           static_cast<size_t>(at.key_head(a)) * DK;
   const unsigned qrb = static_cast<unsigned>(a.q_stride) * 2, krb = static_cast<unsigned>(a.k_stride) * 2,
                  vrb = static_cast<unsigned>(a.v_stride) * 2;
-  const typename KB::Lane ql = KB::load_lane(w, lane, qrb), kl = KB::load_lane(w, lane, krb);
-  const typename VB::Lane vl = VB::load_lane(w, lane, vrb);
-
-  // the state, dk = 32 i + 8 (e / 4) + 4 half + e % 4 of tile i, value 32 w + lane % 32 of the slice
-  f32x16_t S[DK / 32];
-  const size_t head = static_cast<size_t>(b) * a.H + h, dkv = static_cast<size_t>(DK) * a.dv;
-  const int col = slice * DVS + 32 * w + lrow;
-  {
-    const float *from = STATE ? nullptr : a.segs == 1 ? a.s0 : a.seg;
-    if (from) from += (head * a.segs + seg) * dkv + col;
-#pragma unroll
-    for (int i = 0; i < DK / 32; ++i)
-#pragma unroll
-      for (int e = 0; e < 16; ++e)
-        S[i][e] = from ? from[static_cast<size_t>(32 * i + 8 * (e >> 2) + 4 * half + (e & 3)) * a.dv] : 0.0f;
-  }
-  float total = 0.0f;
-  const unsigned krow = KB::row_lane(lane), kcol = KB::col_lane(lane), vcol = VB::col_lane(lane);
-  bf16_t *const o_ = static_cast<bf16_t *>(a.o) + (tok * a.H + h) * a.dv + slice * DVS + 32 * w;
-  const size_t o_stride = static_cast<size_t>(a.H) * a.dv;
-  float *const mb = sb[w][0], *const me = sb[w][1], *const mw = sb[w][2];
-
-  auto load_chunk = [&](int t) {
-#pragma unroll
-    for (int hb = 0; hb < 2; ++hb) {  // 32 rows each; rows from len on read zero
-      const int u = t + 32 * hb, rows = len - u;
-      const size_t at = rows > 0 ? u : 0;
-      const auto sk = KB::rsrc(k_ + at * a.k_stride, krb, rows), sv = VB::rsrc(v_ + at * a.v_stride, vrb, rows);
-#pragma unroll
-      for (int i = 0; i < KB::kLPW; ++i) KB::load(sk, krb, i, w, kl, ldk + hb * KB::kBytes);
-#pragma unroll
-      for (int i = 0; i < VB::kLPW; ++i) VB::load(sv, vrb, i, w, vl, ldv + hb * VB::kBytes);
-      if constexpr (!STATE) {
-        const auto sq = KB::rsrc(q_ + at * a.q_stride, qrb, rows);
-#pragma unroll
-        for (int i = 0; i < KB::kLPW; ++i) KB::load(sq, qrb, i, w, ql, ldq + hb * KB::kBytes);
-      }
-    }
+  u32x4_t qx[KB::kN], kx[KB::kN], vx[VB::kN];
+  float gx = 0.0f;  // (the first wave's)
+  auto load = [&](int t) {
+    KB::load(kx, at.k + static_cast<size_t>(t) * a.k_stride, krb, at.t_end - t, tid);
+    if (w == 0) gx = at.decay(t, lane);
   };
-  auto load_decay = [&](int t) { return t + lane < t_end ? log2_decay(g_[static_cast<size_t>(t + lane) * g_stride]) : 0.0f; };
+  auto load_qv = [&](int t) {
+    KB::load(qx, q_ + static_cast<size_t>(t) * a.q_stride, qrb, at.t_end - t, tid);
+    VB::load(vx, at.v + static_cast<size_t>(t) * a.v_stride, vrb, at.t_end - t, tid);
+  };
+  f32x4_t S[DK / 16];
+  const size_t dkv = static_cast<size_t>(DK) * a.dv;
+  const int col = at.slice * DVS + 16 * w;
+  if (const float *from = a.chained ? a.seg + (at.head * a.segs + at.seg) * dkv : a.s0 ? a.s0 + at.head * dkv : nullptr) {
+    load_state<DK>(S, from + col, a.dv);
+  } else {
+#pragma unroll
+    for (int i = 0; i < DK / 16; ++i) S[i] = f32x4_t{};
+  }
+  for (int j = 0; !a.chained && j < at.seg; ++j) {
+    const float keep = __builtin_amdgcn_exp2f(uniform_load(a.sums, at.head * (a.segs - 1) + j));
+    f32x4_t own[DK / 16];
+    load_state<DK>(own, a.seg + (at.head * a.segs + j + 1) * dkv + col, a.dv);
+#pragma unroll
+    for (int i = 0; i < DK / 16; ++i) S[i] = S[i] * keep + own[i];
+  }
+  if (at.t_lo < at.t_end) {
+    load(at.t_lo);
+    load_qv(at.t_lo);
+  }
+  bf16_t *const o_ = static_cast<bf16_t *>(a.o) + (at.tok * a.H + at.h) * a.dv + col;
+  const size_t o_stride = static_cast<size_t>(a.H) * a.dv;
+  const typename KB::ColLane kc = KB::col_lane(lane);
+  const typename KB::PairLane kr = KB::pair_lane(lane);
+  const unsigned vc = ldv + 64 * (w >> 1) + (w & 1 ? VB::col_lane(lane).at[1] : VB::col_lane(lane).at[0]);
+  const unsigned qr = ldq + KB::row_lane(lane), pl = ldp + lane * 16;
+  if (w == 0) {  // of the scores' operands, the tokens behind the 16 of an even j: never written again
+#pragma unroll
+    for (int j = 0; j < 4; j += 2)
+#pragma unroll
+      for (int x = 0; x < 2; ++x)
+        *(lds_u32x2_t *)static_cast<uintptr_t>(pl + scores_of(j, j >> 1) + 8 + x * kScores) = u32x2_t{};
+  }
 
-  if (t_lo < t_end) load_chunk(t_lo);
-  float g_next = t_lo < t_end ? load_decay(t_lo) : 0.0f;
-  for (int t = t_lo; t < t_end; t += kC) {
-    // ---- the chunk's running sum of log2 decays, each wave for itself
-    const float bt = wave_sum_up(g_next);
-    const float b_end = __int_as_float(__builtin_amdgcn_readlane(__float_as_int(bt), 63));
-    mb[lane] = bt;
-    me[lane] = __builtin_amdgcn_exp2f(bt) * a.scale;
-    mw[lane] = __builtin_amdgcn_exp2f(b_end - bt);
-    if constexpr (STATE) total += b_end;
-    __builtin_amdgcn_s_waitcnt(0x0F70);  // vmcnt(0): this wave's rows landed
+  for (int t = at.t_lo; t < at.t_end; t += kC) {
+    KB::put(kx, ldk, tid);
+    KB::put_paired(qx, ldq, tid);
+    VB::put(vx, ldv, tid);
+    if (w == 0) {
+      const float bt = at.running(gx, t, lane);
+      const float b_end = __int_as_float(__builtin_amdgcn_readlane(__float_as_int(bt), 63));
+      mb[lane] = bt;
+      me[lane] = __builtin_amdgcn_exp2f(bt) * a.scale;
+      mw[lane] = __builtin_amdgcn_exp2f(b_end - bt);
+      if (lane == 0) mkeep = __builtin_amdgcn_exp2f(b_end);
+    }
     lds_barrier();
-    g_next = t + kC < t_end ? load_decay(t + kC) : 0.0f;
-    f32x16_t O[2];  // O^T: value 32 w + 8 (e / 4) + 4 half + e % 4 of the slice, token 32 tile + lane % 32
-    if constexpr (!STATE) {
-      // ---- P^T
-      for (int tile = w; tile < 3; tile += NW) {
-        const int tt = tile > 0 ? 1 : 0, ss = tile > 1 ? 1 : 0;
-        f32x16_t p = f32x16_t{};
-        unsigned ka = ldk + ss * KB::kBytes + krow, qa = ldq + tt * KB::kBytes + krow;
-        asm volatile("" : "+v"(ka), "+v"(qa));
+    if (t + kC < at.t_end) load(t + kC);
+    // ---- P^T: tile of tokens 16 j .. against 16 i ..
+    for (int n = w; n < 10; n += NW) {
+      const int j = n < 1 ? 0 : n < 3 ? 1 : n < 6 ? 2 : 3, i = n - j * (j + 1) / 2;
+      f32x4_t p = f32x4_t{};
+      const unsigned k0 = ldk + 16 * i * KB::kStride, q0 = qr + 16 * j * KB::kStride;
 #pragma unroll
-        for (int d = 0; d < KB::kKS; ++d)
-          p = __builtin_amdgcn_mfma_f32_32x32x16_bf16(KB::rows(ka, d), KB::rows(qa, d), p, 0, 0, 0);
-        const float btt = mb[32 * tt + lrow];
+      for (int d = 0; d < DK / 32; ++d) p = mfma(KB::pairs(k0, kr, d), KB::rows(0, q0, d), p);
+      const float btt = mb[16 * j + c];
+      const f32x4_t bs = *reinterpret_cast<const f32x4_t *>(&mb[16 * i + 4 * g]);
+      float x[4];
 #pragma unroll
-        for (int st = 0; st < 2; ++st) {
-          float x[8];
-#pragma unroll
-          for (int e = 0; e < 8; ++e) {
-            const int s = 16 * st + 8 * (e >> 2) + 4 * half + (e & 3);
-            const float f = p[8 * st + e] * a.scale * __builtin_amdgcn_exp2f(btt - mb[32 * ss + s]);
-            x[e] = tt > ss || s <= lrow ? f : 0.0f;
-          }
-          const unsigned at = ldp + ((tile * 2 + st) * 64 + lane) * 16;
-          *(lds_u32x4_t *)static_cast<uintptr_t>(at) = split(x);
-          *(lds_u32x4_t *)static_cast<uintptr_t>(at + kPB) = split(x);
-        }
+      for (int e = 0; e < 4; ++e) {
+        const float f = p[e] * a.scale * __builtin_amdgcn_exp2f(btt - bs[e]);
+        x[e] = i < j || 4 * g + e <= c ? f : 0.0f;
       }
-      lds_barrier();
-      // ---- O^T = S^T Q^T, rows scaled by scale exp(b_t)
-      O[0] = O[1] = f32x16_t{};
-      unsigned qa[2][2];  // row 32 tile + lane % 32: its chunk for values 4 half .. of 8 and of the next 8
-      const int rq = lane & 31;
-#pragma unroll
-      for (int tt = 0; tt < 2; ++tt)
-#pragma unroll
-        for (int x = 0; x < 2; ++x) {
-          qa[tt][x] = ldq + tt * KB::kBytes + rq * KB::kRowBytes + ((x ^ KB::swz(rq)) * 16) + 8 * half;
-          asm volatile("" : "+v"(qa[tt][x]));
-        }
-#pragma unroll
-      for (int i = 0; i < DK / 32; ++i)
-#pragma unroll
-        for (int st = 0; st < 2; ++st) {
-          float x[8];
-#pragma unroll
-          for (int e = 0; e < 8; ++e) x[e] = S[i][8 * st + e];
-          const u32x4_t hi = split(x), lo = split(x);
-#pragma unroll
-          for (int tt = 0; tt < 2; ++tt) {
-            const unsigned step = 32u * (2 * i + st);
-            const u32x2_t q0 = *(lds_u32x2_t *)static_cast<uintptr_t>(qa[tt][0] ^ step),
-                          q1 = *(lds_u32x2_t *)static_cast<uintptr_t>(qa[tt][1] ^ step);
-            const u32x4_t qv = {q0[0], q0[1], q1[0], q1[1]};
-            O[tt] = mfma(hi, qv, O[tt]);
-            O[tt] = mfma(lo, qv, O[tt]);
-          }
-        }
-#pragma unroll
-      for (int tt = 0; tt < 2; ++tt) O[tt] *= me[32 * tt + lrow];
+      const u32x2_t hi = {pack_bf16x2(x[0], x[1]), pack_bf16x2(x[2], x[3])};
+      const u32x2_t lo = {pack_bf16x2(x[0] - bf16lo(hi[0]), x[1] - bf16hi(hi[0])),
+                          pack_bf16x2(x[2] - bf16lo(hi[1]), x[3] - bf16hi(hi[1]))};
+      const unsigned to = pl + scores_of(j, i >> 1) + 8 * (i & 1);
+      *(lds_u32x2_t *)static_cast<uintptr_t>(to) = hi;
+      *(lds_u32x2_t *)static_cast<uintptr_t>(to + kScores) = lo;
     }
-    // ---- S decays; then O^T += V^T P^T and S += K^T (w V), 16 tokens at a time
-    const float keep = __builtin_amdgcn_exp2f(b_end);
+    // ---- O^T = S^T Q^T, rows scaled by scale exp(b_t): value 16 w + 4 g + e, token 16 j + c
+    f32x4_t O[4];
 #pragma unroll
-    for (int i = 0; i < DK / 32; ++i) S[i] *= keep;
-    unsigned va = ldv + vcol, ka = ldk + kcol;
-    asm volatile("" : "+v"(va), "+v"(ka));
+    for (int j = 0; j < 4; ++j) O[j] = f32x4_t{};
 #pragma unroll
-    for (int st = 0; st < 4; ++st) {
-      const u32x4_t v = __builtin_bit_cast(u32x4_t, VB::cols(va, st, w));
-      if constexpr (!STATE) {
-        // a token's own tile: 0 * v is not 0 where a later token's v is infinite or NaN, those go one by one
-        const bool odd = __any(not_finite(v));
+    for (int n = 0; n < DK / 32; ++n) {
+      float f[8];
 #pragma unroll
-        for (int tt = st >> 1; tt < 2; ++tt) {
-          const unsigned at = ldp + (((tt + (st >> 1)) * 2 + (st & 1)) * 64 + lane) * 16;
-          if (tt == st >> 1 && odd) {
-            const unsigned vrows = ldv + tt * VB::kBytes, prow = ldp + ((2 * tt * 2 + (st & 1)) * 64 + lrow) * 16;
-            for (int s = 0; s < 16; ++s) {
-              const unsigned pa = prow + ((s >> 2) & 1) * 512 + ((s & 3) + 4 * (s >> 3)) * 2;
-              const float p = bf16_to_f32(*(lds_u16_t *)static_cast<uintptr_t>(pa)) +
-                              bf16_to_f32(*(lds_u16_t *)static_cast<uintptr_t>(pa + kPB));
-              const int row = 16 * (st & 1) + s;
+      for (int e = 0; e < 8; ++e) f[e] = S[2 * n + (e >> 2)][e & 3];
+      const u32x4_t hi = split(f), lo = rounded(f);
+      u32x4_t q[4];
 #pragma unroll
-              for (int e = 0; e < 16; ++e) {
-                const int d = 32 * w + 8 * (e >> 2) + 4 * half + (e & 3);
-                const unsigned va1 = vrows + row * VB::kRowBytes + (((d >> 3) ^ VB::swz(row)) * 16) + (d & 7) * 2;
-                const float x = p * bf16_to_f32(*(lds_u16_t *)static_cast<uintptr_t>(va1));
-                if (row <= lrow) O[tt][e] += x;
-              }
-            }
-            continue;
-          }
-          O[tt] = mfma(v, *(lds_u32x4_t *)static_cast<uintptr_t>(at), O[tt]);
-          O[tt] = mfma(v, *(lds_u32x4_t *)static_cast<uintptr_t>(at + kPB), O[tt]);
-        }
-      }
-      float x[8];
+      for (int j = 0; j < 4; ++j) q[j] = KB::rows(16 * j * KB::kStride, qr, n);
 #pragma unroll
-      for (int e = 0; e < 8; ++e)
-        x[e] = (e & 1 ? bf16hi(v[e >> 1]) : bf16lo(v[e >> 1])) * mw[16 * st + 8 * (e >> 2) + 4 * half + (e & 3)];
-      const u32x4_t hi = split(x), mid = split(x), lo = split(x);
+      for (int j = 0; j < 4; ++j) O[j] = mfma(hi, q[j], O[j]);
 #pragma unroll
-      for (int i = 0; i < DK / 32; ++i) {
-        const u32x4_t kt = __builtin_bit_cast(u32x4_t, KB::cols(ka, st, i));
-        S[i] = mfma(kt, hi, S[i]);
-        S[i] = mfma(kt, mid, S[i]);
-        S[i] = mfma(kt, lo, S[i]);
-      }
+      for (int j = 0; j < 4; ++j) O[j] = mfma(lo, q[j], O[j]);
     }
-    if constexpr (!STATE) {
 #pragma unroll
-      for (int tt = 0; tt < 2; ++tt) {
-        const int row = t + 32 * tt + lrow;
-        if (row < t_hi) {
+    for (int j = 0; j < 4; ++j) O[j] *= me[16 * j + c];
+    u32x4_t v[2];
 #pragma unroll
-          for (int g = 0; g < 4; ++g) {
-            u32x2_t x = {pack_bf16x2(O[tt][4 * g], O[tt][4 * g + 1]), pack_bf16x2(O[tt][4 * g + 2], O[tt][4 * g + 3])};
-            if (row >= len) x = u32x2_t{};
-            *reinterpret_cast<u32x2_t *>(o_ + row * o_stride + 8 * g + 4 * half) = x;
-          }
-        }
+    for (int st = 0; st < 2; ++st) v[st] = VB::cols(0, vc, st);
+    // (not with the keys: registers would be spilled, and a spilled load is waited for)
+    if (t + kC < at.t_end) load_qv(t + kC);
+    lds_barrier();  // the scores are there
+    // ---- O^T += V^T P^T. Where a v is infinite or NaN, 0 times it is not 0: each token's own 32 are left out here
+    // and go one by one
+    const bool odd = __any(not_finite(v[0]) || not_finite(v[1]));
+    const unsigned own = odd ? 0u : ~0u;
+#pragma unroll
+    for (int st = 0; st < 2; ++st)
+#pragma unroll
+      for (int j = 2 * st; j < 4; ++j) {
+        const unsigned from = pl + scores_of(j, st);
+        const u32x4_t x = st == j >> 1 ? v[st] & own : v[st];
+        O[j] = mfma(x, *(lds_u32x4_t *)static_cast<uintptr_t>(from), O[j]);
+        O[j] = mfma(x, *(lds_u32x4_t *)static_cast<uintptr_t>(from + kScores), O[j]);
       }
+    if (odd) own_tokens<VB>(O, ldv, ldp, w, lane);
+    int cr = c;
+    asm volatile("" : "+v"(cr));  // (addresses of rows formed here, as above)
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      const int row = t + 16 * j + cr;
+      u32x2_t x = {pack_bf16x2(O[j][0], O[j][1]), pack_bf16x2(O[j][2], O[j][3])};
+      if (row >= at.len) x = u32x2_t{};
+      if (row < at.t_hi) *reinterpret_cast<u32x2_t *>(o_ + row * o_stride + 4 * g) = x;
     }
+    // ---- S decays, and takes the chunk's tokens
+    const float keep = mkeep;
+#pragma unroll
+    for (int i = 0; i < DK / 16; ++i) S[i] *= keep;
+    add_outer<DK, KB>(S, v, mw, ldk, kc, g);
     lds_barrier();  // everyone is done with the chunk
-    if (t + kC < t_end) load_chunk(t + kC);
   }
-  if constexpr (!STATE) {
-    // rows behind the sequence, from the first whole chunk on
-    const int z0 = t_lo < t_end ? t_lo + (t_end - t_lo + kC - 1) / kC * kC : t_lo;
-    for (long long i = z0 * 4LL + lane; i < t_hi * 4LL; i += 64)
-      *reinterpret_cast<u32x4_t *>(o_ + static_cast<size_t>(i >> 2) * o_stride + 8 * static_cast<int>(i & 3)) = u32x4_t{};
-    if (!a.s_out || seg != a.segs - 1) return;
-  } else if (tid == 0 && slice == 0) {
-    a.sums[head * (a.segs - 1) + seg] = total;
-  }
-  float *const to = (STATE ? a.seg + (head * a.segs + seg + 1) * dkv : a.s_out + head * dkv) + col;
-#pragma unroll
-  for (int i = 0; i < DK / 32; ++i)
-#pragma unroll
-    for (int e = 0; e < 16; ++e) to[static_cast<size_t>(32 * i + 8 * (e >> 2) + 4 * half + (e & 3)) * a.dv] = S[i][e];
+  // rows behind the sequence, from the first whole chunk on
+  const int z0 = at.t_lo < at.t_end ? at.t_lo + (at.t_end - at.t_lo + kC - 1) / kC * kC : at.t_lo;
+  for (long long i = z0 * 2LL + lane; i < at.t_hi * 2LL; i += 64)
+    *reinterpret_cast<u32x4_t *>(o_ + static_cast<size_t>(i >> 1) * o_stride + 8 * static_cast<int>(i & 1)) = u32x4_t{};
+  if (!a.s_out || at.seg != a.segs - 1) return;
+  store_state<DK>(S, a.s_out + at.head * dkv + col, a.dv);
 }
 
 // Segments' own states to the states they end with, S_j = exp(sum of g) S_{j-1} + own, in place; the first one's from
@@ -410,9 +619,13 @@ template <int DK, int DVS> hipError_t launch(LinearArgs a, hipStream_t s) {
   if (a.segs > 1) {
     a.run = a.segs - 1;
     const long long g = rows * a.run;
-    linear_fwd<DK, DVS, true><<<dim3(grid_x(g), grid_rows(g)), DVS * 2, 0, s>>>(a);
+    linear_state<DK, DVS><<<dim3(grid_x(g), grid_rows(g)), threads_of(DVS), 0, s>>>(a);
     const hipError_t e = hipGetLastError();
     if (e != hipSuccess) return e;
+    // (where the last state goes over the first one, the segments need a copy of that)
+    a.chained = a.segs > kFew || (a.s0 && a.s_out == a.s0);
+  }
+  if (a.chained) {
     const long long c = (static_cast<long long>(a.B) * a.H * DK * (a.dv / 4) + 255) / 256;
     linear_carry<<<dim3(grid_x(c), grid_rows(c)), 256, 0, s>>>(a);
     const hipError_t f = hipGetLastError();
@@ -420,7 +633,7 @@ template <int DK, int DVS> hipError_t launch(LinearArgs a, hipStream_t s) {
   }
   a.run = a.segs;
   const long long g = rows * a.run;
-  linear_fwd<DK, DVS, false><<<dim3(grid_x(g), grid_rows(g)), DVS * 2, 0, s>>>(a);
+  linear_fwd<DK, DVS><<<dim3(grid_x(g), grid_rows(g)), threads_of(DVS), 0, s>>>(a);
   return hipGetLastError();
 }
 

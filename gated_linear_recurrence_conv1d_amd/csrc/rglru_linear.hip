@@ -416,8 +416,23 @@ __global__ __launch_bounds__(threads_of(DVS), waves_of(DK, DVS)) void linear_fwd
         *(lds_u32x2_t *)static_cast<uintptr_t>(pl + scores_of(j, j >> 1) + 8 + x * kScores) = u32x2_t{};
   }
 
+  // o of a chunk goes to memory through q's place, in whole rows, where the two have rows of one length (each thread's
+  // 16 bytes, before its wave puts the next q there)
+  constexpr bool kThrough = DK == DVS;
+  auto store_rows = [&](int t0) {
+    int x = tid;
+    asm volatile("" : "+v"(x));
+#pragma unroll
+    for (int i = 0; i < VB::kN; ++i) {
+      const int r = x / VB::kCPR + VB::kRows * i, row = t0 + r;
+      u32x4_t y = *(lds_u32x4_t *)static_cast<uintptr_t>(ldq + VB::chunk(r, x % VB::kCPR));
+      if (row >= at.len) y = u32x4_t{};
+      if (row < at.t_hi) *reinterpret_cast<u32x4_t *>(o_ - 16 * w + row * o_stride + 8 * (x % VB::kCPR)) = y;
+    }
+  };
   for (int t = at.t_lo; t < at.t_end; t += kC) {
     KB::put(kx, ldk, tid);
+    if (kThrough && t > at.t_lo) store_rows(t - kC);
     KB::put_paired(qx, ldq, tid);
     VB::put(vx, ldv, tid);
     if (w == 0) {
@@ -498,8 +513,12 @@ __global__ __launch_bounds__(threads_of(DVS), waves_of(DK, DVS)) void linear_fwd
     for (int j = 0; j < 4; ++j) {
       const int row = t + 16 * j + cr;
       u32x2_t x = {pack_bf16x2(O[j][0], O[j][1]), pack_bf16x2(O[j][2], O[j][3])};
-      if (row >= at.len) x = u32x2_t{};
-      if (row < at.t_hi) *reinterpret_cast<u32x2_t *>(o_ + row * o_stride + 4 * g) = x;
+      if constexpr (kThrough) {
+        *(lds_u32x2_t *)static_cast<uintptr_t>(ldq + VB::chunk(16 * j + cr, 2 * w + (g >> 1)) + 8 * (g & 1)) = x;
+      } else {
+        if (row >= at.len) x = u32x2_t{};
+        if (row < at.t_hi) *reinterpret_cast<u32x2_t *>(o_ + row * o_stride + 4 * g) = x;
+      }
     }
     // ---- S decays, and takes the chunk's tokens
     const float keep = mkeep;
@@ -510,6 +529,7 @@ __global__ __launch_bounds__(threads_of(DVS), waves_of(DK, DVS)) void linear_fwd
   }
   // rows behind the sequence, from the first whole chunk on
   const int z0 = at.t_lo < at.t_end ? at.t_lo + (at.t_end - at.t_lo + kC - 1) / kC * kC : at.t_lo;
+  if (kThrough && z0 > at.t_lo) store_rows(z0 - kC);
   for (long long i = z0 * 2LL + lane; i < at.t_hi * 2LL; i += 64)
     *reinterpret_cast<u32x4_t *>(o_ + static_cast<size_t>(i >> 1) * o_stride + 8 * static_cast<int>(i & 1)) = u32x4_t{};
   if (!a.s_out || at.seg != a.segs - 1) return;

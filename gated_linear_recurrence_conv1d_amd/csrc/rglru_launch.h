@@ -158,7 +158,7 @@ struct PagedArgs {
   float c;      // scale * log2(e)
   float floor;  // the running maximum's start: below every score, floor * c finite
   const void *k_scales, *v_scales;  // e8m0 [..][Hkv]: the cache is in e4m3 (rglru_e4m3.h); else NULL
-  // rows behind a shared prefix (launch_paged_parts): its length [1] and the most its table holds, the chunks' places
+  // rows behind a shared prefix (launch_prefix_attention): its length [1] and the most its table holds, the chunks' places
   // in part and stat [N][parts][Hq], from first_part on
   const int *prefix_len;
   long long prefix_cap;
@@ -170,8 +170,6 @@ struct PagedPlan {
 };
 PagedPlan paged_plan(int N, int Hq, int Hkv, long long max_len, int window, int sinks, int io);
 hipError_t launch_paged_attention(const PagedArgs &a, const PagedPlan &p, int io, hipStream_t s);
-// Each row's own chunks behind a shared prefix, as O, m and l (bf16, or e4m3 with scales).
-hipError_t launch_paged_parts(const PagedArgs &a, const PagedPlan &p, hipStream_t s);
 
 // Attention over a shared prefix and each sequence's own tokens (bf16 cache, or e4m3 with scales); the parts' O and
 // (m, l) as in PagedArgs, those of the prefix first. The own tokens' part: `own`, with prefix_len and its places set.

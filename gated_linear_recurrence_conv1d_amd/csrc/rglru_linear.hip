@@ -373,10 +373,10 @@ __global__ __launch_bounds__(threads_of(DVS), waves_of(DK, DVS)) void linear_fwd
   const unsigned qrb = static_cast<unsigned>(a.q_stride) * 2, krb = static_cast<unsigned>(a.k_stride) * 2,
                  vrb = static_cast<unsigned>(a.v_stride) * 2;
   u32x4_t qx[KB::kN], kx[KB::kN], vx[VB::kN];
-  float gx = 0.0f;  // (the first wave's)
+  float gx = 0.0f;  // (the last wave's)
   auto load = [&](int t) {
     KB::load(kx, at.k + static_cast<size_t>(t) * a.k_stride, krb, at.t_end - t, tid);
-    if (w == 0) gx = at.decay(t, lane);
+    if (w == NW - 1) gx = at.decay(t, lane);
   };
   auto load_qv = [&](int t) {
     KB::load(qx, q_ + static_cast<size_t>(t) * a.q_stride, qrb, at.t_end - t, tid);
@@ -435,7 +435,7 @@ __global__ __launch_bounds__(threads_of(DVS), waves_of(DK, DVS)) void linear_fwd
     if (kThrough && t > at.t_lo) store_rows(t - kC);
     KB::put_paired(qx, ldq, tid);
     VB::put(vx, ldv, tid);
-    if (w == 0) {
+    if (w == NW - 1) {  // (the first ones have two tiles of scores)
       const float bt = at.running(gx, t, lane);
       const float b_end = __int_as_float(__builtin_amdgcn_readlane(__float_as_int(bt), 63));
       mb[lane] = bt;
@@ -445,6 +445,26 @@ __global__ __launch_bounds__(threads_of(DVS), waves_of(DK, DVS)) void linear_fwd
     }
     lds_barrier();
     if (t + kC < at.t_end) load(t + kC);
+    // ---- O^T = S^T Q^T, rows scaled by scale exp(b_t): value 16 w + 4 g + e, token 16 j + c
+    f32x4_t O[4];
+#pragma unroll
+    for (int j = 0; j < 4; ++j) O[j] = f32x4_t{};
+#pragma unroll
+    for (int n = 0; n < DK / 32; ++n) {
+      float f[8];
+#pragma unroll
+      for (int e = 0; e < 8; ++e) f[e] = S[2 * n + (e >> 2)][e & 3];
+      const u32x4_t hi = split(f), lo = rounded(f);
+      u32x4_t q[4];
+#pragma unroll
+      for (int j = 0; j < 4; ++j) q[j] = KB::rows(16 * j * KB::kStride, qr, n);
+#pragma unroll
+      for (int j = 0; j < 4; ++j) O[j] = mfma(hi, q[j], O[j]);
+#pragma unroll
+      for (int j = 0; j < 4; ++j) O[j] = mfma(lo, q[j], O[j]);
+    }
+#pragma unroll
+    for (int j = 0; j < 4; ++j) O[j] *= me[16 * j + c];
     // ---- P^T: tile of tokens 16 j .. against 16 i ..
     for (int n = w; n < 10; n += NW) {
       const int j = n < 1 ? 0 : n < 3 ? 1 : n < 6 ? 2 : 3, i = n - j * (j + 1) / 2;
@@ -467,26 +487,6 @@ __global__ __launch_bounds__(threads_of(DVS), waves_of(DK, DVS)) void linear_fwd
       *(lds_u32x2_t *)static_cast<uintptr_t>(to) = hi;
       *(lds_u32x2_t *)static_cast<uintptr_t>(to + kScores) = lo;
     }
-    // ---- O^T = S^T Q^T, rows scaled by scale exp(b_t): value 16 w + 4 g + e, token 16 j + c
-    f32x4_t O[4];
-#pragma unroll
-    for (int j = 0; j < 4; ++j) O[j] = f32x4_t{};
-#pragma unroll
-    for (int n = 0; n < DK / 32; ++n) {
-      float f[8];
-#pragma unroll
-      for (int e = 0; e < 8; ++e) f[e] = S[2 * n + (e >> 2)][e & 3];
-      const u32x4_t hi = split(f), lo = rounded(f);
-      u32x4_t q[4];
-#pragma unroll
-      for (int j = 0; j < 4; ++j) q[j] = KB::rows(16 * j * KB::kStride, qr, n);
-#pragma unroll
-      for (int j = 0; j < 4; ++j) O[j] = mfma(hi, q[j], O[j]);
-#pragma unroll
-      for (int j = 0; j < 4; ++j) O[j] = mfma(lo, q[j], O[j]);
-    }
-#pragma unroll
-    for (int j = 0; j < 4; ++j) O[j] *= me[16 * j + c];
     u32x4_t v[2];
 #pragma unroll
     for (int st = 0; st < 2; ++st) v[st] = VB::cols(0, vc, st);

@@ -98,35 +98,63 @@ __device__ __forceinline__ void prefix_row(const PrefixArgs &a, const bf16_t *q,
   }
 }
 
+constexpr unsigned kPartRow = 36 * 4;  // 32 values of a row on their way out, 16 bytes apart against conflicts
+
+// What a workgroup of the prefix has in LDS: two blocks of K and V, then each wave's rows on their way out; each wave's
+// first visible token; keys whose page is none, by block and wave.
+template <int DH> struct PrefixLds {
+  static constexpr unsigned kIn = 2 * Blk<DH>::kSlot, kOut = kOwn * kPartRow;
+  __attribute__((aligned(1024))) unsigned char slots[kIn > kOut ? kIn : kOut];
+  int least[kWg];
+  unsigned bads[2][kWg];
+};
+
+// The prefix's part: id is the workgroup's (chunk, key/value head, 128 rows).
 template <typename C, int DH>
-__global__ __launch_bounds__(64 * kWg, 2) void prefix_fwd(PrefixArgs a, int chunk) {
+__device__ __forceinline__ void prefix_rows(const PrefixArgs &a, int chunk, int id, PrefixLds<DH> &mem) {
   typedef Blk<DH> K;
   constexpr bool kCode = sizeof(C) == 1;
-  __shared__ __attribute__((aligned(1024))) unsigned char smem[2 * K::kSlot];
-  __shared__ int least[kWg];
+  auto &smem = mem.slots;
+  auto &least = mem.least;
+  auto &bads = mem.bads;
   const int tid = threadIdx.x, lane = tid & 63, w = uni(tid >> 6);
   const unsigned lds = lds_addr(smem);
   const int lrow = lane & 31, half = lane >> 5;
   const int G = a.Hq / a.Hkv;
   const long long R = static_cast<long long>(a.N) * G;  // rows of a key/value head
   const int tiles = static_cast<int>((R + kOwn - 1) / kOwn);
-  const int id = block_of(blockIdx.y);  // row tiles first: the workgroups of one chunk are near each other
+  // (row tiles first: the workgroups of one chunk are near each other)
   const int sp = uni(id / (tiles * a.Hkv)), rest = id - sp * tiles * a.Hkv;
   const int kvh = uni(rest / tiles), tile = rest - kvh * tiles;
   const int P = prefix_of(a.prefix_len, a.prefix_cap);
   const int blocks = (P + kBlk - 1) / kBlk, b0 = sp * chunk, b1 = min(blocks, b0 + chunk);
   if (b0 >= b1) return;  // (also without a prefix and with a bad length)
   // this lane's row
-  const long long r = static_cast<long long>(tile) * kOwn + 32 * w + lrow;
-  const long long rc = r < R ? r : R - 1;
-  const int n = static_cast<int>(rc / G), h = kvh * G + static_cast<int>(rc - static_cast<long long>(n) * G);
-  // tokens before w0 are behind the row's window (lens may be anything: the join refuses what is no length)
-  const int w0 = static_cast<int>(min(max(static_cast<long long>(P) + a.lens[n] - a.window, 0LL), 0x7FFFFFFFLL));
-  const bf16_t *const q = static_cast<const bf16_t *>(a.q) + static_cast<size_t>(n) * a.q_stride +
-                          static_cast<size_t>(h) * DH;
+  struct Row {
+    int n, h;
+    bool on;     // is one
+    size_t part;  // where its part goes
+  };
+  auto my_row = [&](int l) {
+    const int r = tile * kOwn + 32 * w + (l & 31);  // (R is below 2^30)
+    Row x;
+    x.on = r < R;
+    const int rc = x.on ? r : static_cast<int>(R) - 1;
+    x.n = rc / G;
+    x.h = kvh * G + rc - x.n * G;
+    x.part = (static_cast<size_t>(x.n) * a.parts + sp) * a.Hq + x.h;
+    return x;
+  };
+  int w0;  // tokens before it are behind the row's window (lens may be anything: the join refuses what is no length)
   bf16x8_t qf[K::kKS];
+  {
+    const Row x = my_row(lane);
+    w0 = static_cast<int>(min(max(static_cast<long long>(P) + a.lens[x.n] - a.window, 0LL), 0x7FFFFFFFLL));
+    const bf16_t *const q = static_cast<const bf16_t *>(a.q) + static_cast<size_t>(x.n) * a.q_stride +
+                            static_cast<size_t>(x.h) * DH;
 #pragma unroll
-  for (int s = 0; s < K::kKS; ++s) qf[s] = load_bf16x8(q + 16 * s + 8 * half);
+    for (int s = 0; s < K::kKS; ++s) qf[s] = load_bf16x8(q + 16 * s + 8 * half);
+  }
   int wmin = w0, wmax = w0;
 #pragma unroll
   for (int o = 1; o < 32; o <<= 1) {
@@ -141,12 +169,12 @@ __global__ __launch_bounds__(64 * kWg, 2) void prefix_fwd(PrefixArgs a, int chun
   // blocks that no row sees are left out: after the sinks' up to the first window's
   const int sink_end = (a.sinks + kBlk - 1) / kBlk, win = first / kBlk;
   auto next_of = [&](int b) { return uni(b >= sink_end && b < win ? win : b); };
-  const size_t stat_at = (static_cast<size_t>(n) * a.parts + sp) * a.Hq + h;
   const int i0 = next_of(b0);
   if (i0 >= b1) {  // nothing: l = 0, and O is not read
-    if (half == 0 && r < R) {
-      a.stat[2 * stat_at] = a.floor;
-      a.stat[2 * stat_at + 1] = 0.0f;
+    const Row x = my_row(lane);
+    if (half == 0 && x.on) {
+      a.stat[2 * x.part] = a.floor;
+      a.stat[2 * x.part + 1] = 0.0f;
     }
     return;
   }
@@ -154,28 +182,26 @@ __global__ __launch_bounds__(64 * kWg, 2) void prefix_fwd(PrefixArgs a, int chun
   const size_t row_bytes = static_cast<size_t>(a.Hkv) * DH * sizeof(C);
   const char *const kp = static_cast<const char *>(a.k_pages) + static_cast<size_t>(kvh) * DH * sizeof(C);
   const char *const vp = static_cast<const char *>(a.v_pages) + static_cast<size_t>(kvh) * DH * sizeof(C);
-  // pool row of key u (past the prefix: of its last key; on a page outside the pool: row 0, and `bad`)
-  auto row_of = [&](int u, bool &bad) {
-    u = min(u, P - 1);
-    const int t = u / a.page, page = a.prefix_table[t];
-    bad = page < 0 || page >= a.num_pages;
-    return bad ? 0 : page * a.page + (u - t * a.page);
-  };
-  // A block's rows are looked up a block before they are loaded, and loaded a block before they are used.
+  // A block's rows are looked up a block before they are loaded, and loaded a block before they are used. (What the
+  // table gives is looked at when it is needed: at once, it would be waited for, and with it all loads before it.)
   // bf16: a lane looks up key lane % 32, and its row is handed to the lanes that load it.
   // e4m3: a thread has DH / 8 codes of key tid / 8.
-  int key_row = 0, bad_key = 0;
+  int key_page = 0, key_at = 0;  // of the key looked up, its page and place there
   constexpr int kCW = kCode ? DH / 32 : 1;  // words
   uint32_t ck[kCW], cv[kCW];
   unsigned sk = 0, sv = 0;
   const int crow = tid >> 3, cpart = tid & 7;
   auto look_up = [&](int b) {
-    bool bad;
-    key_row = row_of(b * kBlk + (kCode ? crow : lrow), bad);
-    bad_key = bad;
+    const int u = min(b * kBlk + (kCode ? crow : lrow), P - 1);  // (past the prefix: its last key)
+    const int t = u / a.page;
+    key_page = a.prefix_table[t];
+    key_at = u - t * a.page;
   };
+  auto bad_key = [&]() { return key_page < 0 || key_page >= a.num_pages; };
+  auto key_row = [&]() { return bad_key() ? 0 : key_page * a.page + key_at; };  // the pool's; for a bad page row 0
   auto load_codes = [&]() {
-    const char *const kr = kp + key_row * row_bytes + cpart * (DH / 8), *const vr = vp + (kr - kp);
+    const int row = key_row();
+    const char *const kr = kp + row * row_bytes + cpart * (DH / 8), *const vr = vp + (kr - kp);
 #pragma unroll
     for (int i = 0; i < kCW; i += 4) {
       if constexpr (kCW >= 4) {
@@ -194,7 +220,7 @@ __global__ __launch_bounds__(64 * kWg, 2) void prefix_fwd(PrefixArgs a, int chun
         }
       }
     }
-    const size_t at = static_cast<size_t>(key_row) * a.Hkv + kvh;
+    const size_t at = static_cast<size_t>(row) * a.Hkv + kvh;
     sk = static_cast<const uint8_t *>(a.k_scales)[at];
     sv = static_cast<const uint8_t *>(a.v_scales)[at];
   };
@@ -213,10 +239,11 @@ __global__ __launch_bounds__(64 * kWg, 2) void prefix_fwd(PrefixArgs a, int chun
     }
   };
   auto load_rows = [&](unsigned slot) {
+    const int mine = key_row();
 #pragma unroll
     for (int ii = 0; ii < K::kLPW; ++ii) {
       const int row = (w + kWg * ii) * K::kRPI + lane / K::kCPR;
-      const size_t at = static_cast<size_t>(__shfl(key_row, row, 64)) * row_bytes +
+      const size_t at = static_cast<size_t>(__shfl(mine, row, 64)) * row_bytes +
                         static_cast<unsigned>(((lane % K::kCPR) ^ K::swz(row)) * 16);
       const unsigned dst = static_cast<unsigned>(uni(slot + (w + kWg * ii) * 1024));
       dma_16b_from(kp + at, dst);
@@ -224,9 +251,8 @@ __global__ __launch_bounds__(64 * kWg, 2) void prefix_fwd(PrefixArgs a, int chun
     }
   };
   // bad keys of the block looked up last, bit by bit (e4m3: of the 8 that this wave looked up, for all waves)
-  __shared__ unsigned bads[2][kWg];
   auto bad_bits = [&]() {
-    const unsigned long long x = __ballot(bad_key);
+    const unsigned long long x = __ballot(bad_key());
     if constexpr (!kCode) return static_cast<unsigned>(x);
     unsigned bits = 0;
 #pragma unroll
@@ -367,34 +393,74 @@ __global__ __launch_bounds__(64 * kWg, 2) void prefix_fwd(PrefixArgs a, int chun
   halves(l, lo, hi);
   const float lt = lo + hi;
   float worst = 0.0f;
-  float *const out = a.part + stat_at * DH;
+  int again = lane;
+  asm volatile("" : "+v"(again));  // the row is formed anew: kept, it takes registers from the walk
+  const Row me = my_row(again);
+  // through LDS, 32 values of the wave's 32 rows at a time: whole lines to memory (lane by lane, 32 bytes of each)
+  lds_barrier();  // everyone is done with the slots
+  const unsigned mine = lds + w * 32 * kPartRow;
+  const int sub = again >> 3;  // this lane stores 16 bytes of rows sub, 8 + sub, ..
+  const size_t at = me.on ? me.part : static_cast<size_t>(-1);
+  float *to[4];
 #pragma unroll
-  for (int j = 0; j < K::kDT; ++j)
+  for (int k = 0; k < 4; ++k) {
+    const long long part = __shfl(static_cast<long long>(at), 8 * k + sub, 64);
+    to[k] = part < 0 ? nullptr : a.part + part * DH + 4 * (again & 7);
+  }
+#pragma unroll
+  for (int j = 0; j < K::kDT; ++j) {
 #pragma unroll
     for (int g = 0; g < 4; ++g) {
-      f32x4_t x;
+      u32x4_t x;
 #pragma unroll
       for (int e = 0; e < 4; ++e) {
-        x[e] = acc[j][4 * g + e];
-        worst = fmaf(0.0f, x[e], worst);  // NaN if any is not finite
+        worst = fmaf(0.0f, acc[j][4 * g + e], worst);  // NaN if any is not finite
+        x[e] = __float_as_uint(acc[j][4 * g + e]);
       }
-      if (r < R) *reinterpret_cast<f32x4_t *>(out + 32 * j + 8 * g + 4 * half) = x;
+      *(lds_u32x4_t *)static_cast<uintptr_t>(mine + (again & 31) * kPartRow + 32 * g + 16 * half) = x;
     }
-  if (half == 0 && r < R) {
-    a.stat[2 * stat_at] = m;
-    a.stat[2 * stat_at + 1] = lt;
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+      const u32x4_t x = *(lds_u32x4_t *)static_cast<uintptr_t>(mine + (8 * k + sub) * kPartRow + 16 * (again & 7));
+      if (to[k]) *reinterpret_cast<u32x4_t *>(to[k] + 32 * j) = x;
+    }
   }
-  const unsigned long long rows = __ballot(r < R && !(worst == 0.0f) && lt < __builtin_inff());
+  if (half == 0 && me.on) {
+    a.stat[2 * me.part] = m;
+    a.stat[2 * me.part + 1] = lt;
+  }
+  const unsigned long long rows = __ballot(me.on && !(worst == 0.0f) && lt < __builtin_inff());
   unsigned odd = static_cast<unsigned>(rows | (rows >> 32));
   if (odd) __builtin_amdgcn_s_waitcnt(0x0F70);  // this wave's stores are done before it stores those rows again
   while (odd) {
     const int x = __builtin_ctz(odd);
     odd &= odd - 1;
-    const int nx = __shfl(n, x, 64), hx = __shfl(h, x, 64), wx = __shfl(w0, x, 64);
-    const size_t at = (static_cast<size_t>(nx) * a.parts + sp) * a.Hq + hx;
-    prefix_row<C, DH>(a, static_cast<const bf16_t *>(a.q) + static_cast<size_t>(nx) * a.q_stride +
-                             static_cast<size_t>(hx) * DH,
-                      kvh, b0 * kBlk, min(P, b1 * kBlk), wx, a.part + at * DH, a.stat + 2 * at, lane);
+    const Row y = my_row(x);
+    prefix_row<C, DH>(a, static_cast<const bf16_t *>(a.q) + static_cast<size_t>(y.n) * a.q_stride +
+                             static_cast<size_t>(y.h) * DH,
+                      kvh, b0 * kBlk, min(P, b1 * kBlk), __shfl(w0, x, 64), a.part + y.part * DH, a.stat + 2 * y.part, lane);
+  }
+}
+
+// Both parts in one launch, the prefix's workgroups first: those are bound by their products and the vector work
+// between them, the own tokens' by memory, and those fill the CUs that the longer ones leave.
+template <typename C, int DH, bool UNI>
+__global__ __launch_bounds__(64 * kWg, 2) void prefix_fwd(PrefixArgs a, PagedArgs own, int chunk, int own_chunk, int own_splits,
+                                                          int shared_groups, int own_groups) {
+  __shared__ union Both {
+    __device__ Both() {}
+    PrefixLds<DH> prefix;
+    PagedLds<DH> paged;
+  } lds;
+  const int id = block_of(blockIdx.y);
+  const bool mine = id >= shared_groups;
+  const int i = mine ? id - shared_groups : id;
+  if (mine && i >= own_groups) return;
+  if (mine) {
+    const int cols = own.N * own_splits, y = i / cols;
+    paged_rows<bf16_t, C, DH, UNI, true>(own, own_chunk, own_splits, i - y * cols, y, lds.paged);
+  } else {
+    prefix_rows<C, DH>(a, chunk, i, lds.prefix);
   }
 }
 
@@ -414,19 +480,32 @@ __global__ __launch_bounds__(256) void prefix_join(PrefixArgs a, PagedArgs own, 
   const int shared = bad ? 0 : ((P + kBlk - 1) / kBlk + chunk - 1) / chunk;
   const int used = shared + (wk.nt + own_chunk - 1) / own_chunk;
   float m = a.floor, l = 0.0f, acc[V] = {};
-  for (int s = w; s < used; s += 4) {
-    const size_t r = (static_cast<size_t>(n) * a.parts + (s < shared ? s : own.first_part + s - shared)) * a.Hq + h;
-    const float2 st = *reinterpret_cast<const float2 *>(a.stat + 2 * r);
-    if (st.y == 0.0f) continue;  // the row sees nothing there
-    const float mn = fmaxf(m, st.x);
-    const float fo = __builtin_amdgcn_exp2f((m - mn) * a.c), fn = __builtin_amdgcn_exp2f((st.x - mn) * a.c);
-    m = mn;
-    l = fmaf(st.y, fn, l * fo);
+  constexpr int kAt = 4;  // parts in flight
+  for (int s0 = w; s0 < used; s0 += 4 * kAt) {
+    float2 st[kAt];
+    float x[kAt][V];
 #pragma unroll
-    for (int i = 0; i < V; ++i) acc[i] = fmaf(a.part[r * DH + lane + 64 * i], fn, acc[i] * fo);
+    for (int j = 0; j < kAt; ++j) {
+      const int s = min(s0 + 4 * j, used - 1);
+      const size_t r = (static_cast<size_t>(n) * a.parts + (s < shared ? s : own.first_part + s - shared)) * a.Hq + h;
+      st[j] = *reinterpret_cast<const float2 *>(a.stat + 2 * r);
+#pragma unroll
+      for (int i = 0; i < V; ++i) x[j][i] = a.part[r * DH + lane * V + i];
+    }
+#pragma unroll
+    for (int j = 0; j < kAt; ++j) {
+      // (l = 0: the row sees nothing there, and O may hold anything)
+      if (s0 + 4 * j >= used || st[j].y == 0.0f) continue;
+      const float mn = fmaxf(m, st[j].x);
+      const float fo = __builtin_amdgcn_exp2f((m - mn) * a.c), fn = __builtin_amdgcn_exp2f((st[j].x - mn) * a.c);
+      m = mn;
+      l = fmaf(st[j].y, fn, l * fo);
+#pragma unroll
+      for (int i = 0; i < V; ++i) acc[i] = fmaf(x[j][i], fn, acc[i] * fo);
+    }
   }
 #pragma unroll
-  for (int i = 0; i < V; ++i) ro[w][lane + 64 * i] = acc[i];
+  for (int i = 0; i < V; ++i) ro[w][lane * V + i] = acc[i];
   if (lane == 0) {
     rl[w] = l;
     rm[w] = m;
@@ -448,12 +527,14 @@ __global__ __launch_bounds__(256) void prefix_join(PrefixArgs a, PagedArgs own, 
   }
 }
 
-// Blocks per chunk of the prefix, and the most chunks it can have.
+// Blocks per chunk of the prefix, and the most chunks it can have. At least 4 blocks, as each chunk leaves an O of all
+// rows to write and read again (N64 Hq16 dh256 P1999: 36.5 us, with 2 blocks 41, with 8 44.5); 2 where the rows are few
+// and the chunks' number is the time (N6 Hq10 dh256 P700: 14.8 us, with 4 16.6).
 PagedPlan prefix_plan(int N, int Hq, int Hkv, long long cap) {
   const long long tiles = (static_cast<long long>(N) * (Hq / Hkv) + kOwn - 1) / kOwn * Hkv;
   const long long blocks = (cap + kBlk - 1) / kBlk;
   constexpr long long kTarget = 512;  // workgroups: two fit a CU at a time
-  const long long chunk = std::max<long long>((blocks * tiles + kTarget - 1) / kTarget, 2);
+  const long long chunk = std::max<long long>((blocks * tiles + kTarget - 1) / kTarget, tiles > 2 ? 4 : 2);
   PagedPlan p;
   p.chunk = static_cast<int>(std::min<long long>(chunk, 1 << 28));
   p.splits = static_cast<int>(std::max<long long>((blocks + p.chunk - 1) / p.chunk, 1));
@@ -464,12 +545,18 @@ namespace {
 
 template <typename C, int DH>
 hipError_t launch(const PrefixArgs &a, const PagedArgs &own, const PagedPlan &p, const PagedPlan &po, hipStream_t s) {
-  const long long tiles = (static_cast<long long>(a.N) * (a.Hq / a.Hkv) + kOwn - 1) / kOwn;
-  const long long groups = tiles * a.Hkv * p.splits;
-  prefix_fwd<C, DH><<<dim3(grid_x(groups), grid_rows(groups)), 64 * kWg, 0, s>>>(a, p.chunk);
-  hipError_t e = hipGetLastError();
-  if (e != hipSuccess) return e;
-  e = launch_paged_parts(own, po, s);
+  const int G = a.Hq / a.Hkv;
+  const long long tiles = (static_cast<long long>(a.N) * G + kOwn - 1) / kOwn;
+  const long long shared = tiles * a.Hkv * p.splits;
+  const long long mine = static_cast<long long>(a.N) * po.splits * a.Hkv * ((G + 15) / 16), all = shared + mine;
+  const dim3 grid(grid_x(all), grid_rows(all));
+  if (a.page % 16 == 0)
+    prefix_fwd<C, DH, true><<<grid, 64 * kWg, 0, s>>>(a, own, p.chunk, po.chunk, po.splits, static_cast<int>(shared),
+                                                      static_cast<int>(mine));
+  else
+    prefix_fwd<C, DH, false><<<grid, 64 * kWg, 0, s>>>(a, own, p.chunk, po.chunk, po.splits, static_cast<int>(shared),
+                                                       static_cast<int>(mine));
+  const hipError_t e = hipGetLastError();
   if (e != hipSuccess) return e;
   const long long rows = static_cast<long long>(a.N) * a.Hq;
   prefix_join<DH><<<dim3(grid_x(rows), grid_rows(rows)), 256, 0, s>>>(a, own, p.chunk, po.chunk);

@@ -167,7 +167,7 @@ __device__ __forceinline__ void prefix_rows(const PrefixArgs &a, int chunk, int 
   lds_barrier();
   const int first = min(min(least[0], least[1]), min(least[2], least[3]));
   // blocks that no row sees are left out: after the sinks' up to the first window's
-  const int sink_end = (a.sinks + kBlk - 1) / kBlk, win = first / kBlk;
+  const int sink_end = (min(a.sinks, P) + kBlk - 1) / kBlk, win = first / kBlk;
   auto next_of = [&](int b) { return uni(b >= sink_end && b < win ? win : b); };
   const int i0 = next_of(b0);
   if (i0 >= b1) {  // nothing: l = 0, and O is not read
@@ -522,7 +522,7 @@ __global__ __launch_bounds__(256) void prefix_join(PrefixArgs a, PagedArgs own, 
     float o = 0.0f;
 #pragma unroll
     for (int k = 0; k < 4; ++k) o = fmaf(ro[k][d], f[k], o);
-    o = bad ? __builtin_nanf("") : P + raw == 0 ? 0.0f : o / lt;
+    o = bad ? __builtin_nanf("") : (P | raw) == 0 ? 0.0f : o / lt;
     static_cast<bf16_t *>(a.o)[static_cast<size_t>(id) * DH + d] = f32_to_bf16(o);
   }
 }

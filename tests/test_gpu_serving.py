@@ -338,6 +338,17 @@ def test_prefix_scores_far_apart():
         check(got, o, attention_bound(o, mag, most, dh, P + 50), "o")
 
 
+@pytest.mark.parametrize("S", [2 ** 31 - 1, 2 ** 31 - 32, 130])
+def test_prefix_all_sinks(S):
+    """More sinks than tokens: everything is visible, whatever the window."""
+    rng = np.random.default_rng(36)
+    P, lens, page = 200, [1, 40, 0], 16
+    q, cache, pools, pt, table = prefix_inputs(rng, "bf16", P, lens, 4, 2, 64, page)
+    got = run_prefix(q, cache, pt, P, table, lens, 5, S)
+    o, mag, most = sv.prefix_attention(num(q), *pools, pt, P, table, lens, 5, S)
+    check(got, o, attention_bound(o, mag, most, 64, P + 40), "o")
+
+
 @pytest.mark.parametrize("kind", ["bf16", "e4m3"])
 @pytest.mark.parametrize("page", [16, 12])
 @pytest.mark.parametrize("dh", [64, 128, 256])
@@ -481,6 +492,23 @@ def test_linear_attention(B, T, Hk, H, dk, dv, lens, gated, start):
     rg.rglru_linear_attention(q, k, v, g, o2 := torch.empty_like(o), s0, None, dl, workspace=torch.empty(
         max(1, rg.rglru_linear_attention_workspace_size(B, T, Hk, H, dk, dv)), dtype=torch.uint8, device=DEV))
     assert torch.equal(o, o2)
+
+
+@pytest.mark.parametrize("T", [520, 800, 1100, 1300, 2500])  # 2, 3, 4, 5 and 9 segments, the last ones not full
+def test_linear_segments(T):
+    """Segments whose decays let nothing, a part or all of the ones before them through, and sequences that end in the
+    first, in a middle and in the last one."""
+    rng = np.random.default_rng(T)
+    B, Hk, H, dk, dv = 3, 1, 4, 64, 64
+    q, k, v, g, s0 = linear_inputs(rng, B, T, Hk, H, dk, dv, True, True)
+    g *= torch.tensor([1e-3, 0.1, 3.0, 60.0], device=DEV)
+    g[:, T // 2, 1] = -float("inf")
+    lens = [T, T // 2, 40]
+    o, s = rg.linear_attention(q, k, v, g, s0, ints(lens))
+    linear_check(o, s, q, k, v, g, s0, lens)
+    mine = s0.clone()
+    o2, _ = rg.linear_attention(q, k, v, g, mine, ints(lens), state_out=mine)
+    assert torch.equal(o, o2) and torch.equal(s, mine)
 
 
 def test_linear_decays_of_all_strengths():

@@ -6,7 +6,8 @@
 //   o_t = scale (sum_{s <= t} exp(b_t - b_s) <q_t, k_s> v_s + exp(b_t) S^T q_t)
 //   S'  = exp(b_63) S + sum_s exp(b_63 - b_s) k_s v_s^T
 // All exponents are differences of one running sum taken before the exponential, so nothing is divided by a decay and
-// strong decays only underflow.
+// strong decays only underflow. Tokens that forget the state are counted beside that sum, not in it: the weights of the
+// tokens behind them stay as exact as their own decays are.
 //
 // linear_fwd: a workgroup walks the chunks of one (sequence, head, slice of up to 128 values, segment); each wave
 // keeps S for 16 of the values (dk x 16 in accumulators). Per chunk, on 16x16x32 MFMAs:
@@ -35,7 +36,8 @@ namespace {
 
 constexpr int kC = 64;              // tokens per chunk
 constexpr int kFew = 4;             // segments that are chained where they are needed
-constexpr float kLeast = -104.0f;   // exp of it is 0 in fp32: a smaller log decay (-inf: forget) counts as this
+constexpr float kLeast = -104.0f;   // exp of it is 0 in fp32: a smaller log decay (-inf) forgets the state
+constexpr float kGone = -150.0f;    // exp2 of it is 0 in fp32
 
 // Inclusive running sum over the 64 lanes.
 __device__ __forceinline__ float wave_sum_up(float v) {
@@ -48,8 +50,6 @@ __device__ __forceinline__ float wave_sum_up(float v) {
   v = add(v, __builtin_amdgcn_update_dpp(0, __float_as_int(v), 0x143, 0xC, 0xF, false));  // row_bcast:31
   return v;
 }
-
-__device__ __forceinline__ float log2_decay(float g) { return (g < kLeast ? kLeast : g) * kLn2Inv; }
 
 // 8 fp32 values as bf16 terms: x = hi + mid (+ lo), each the rounding of what is left.
 __device__ __forceinline__ u32x4_t split(float (&x)[8]) {
@@ -70,6 +70,7 @@ __device__ __forceinline__ u32x4_t rounded(const float (&x)[8]) {
 }
 
 typedef __attribute__((address_space(3))) uint16_t lds_u16_t;
+typedef int i32x4_t __attribute__((ext_vector_type(4)));
 
 // Whether any of 8 bf16 values is infinite or NaN: as integers without their sign, those are the largest.
 __device__ __forceinline__ bool not_finite(u32x4_t v) {
@@ -199,6 +200,16 @@ template <typename VB> __device__ __forceinline__ void own_tokens(f32x4_t (&O)[4
     }
 }
 
+// Of a chunk's tokens up to the lane's one, and of all: the summed log2 decays of those that do not forget the state, and
+// the number of those that do.
+struct Sums {
+  float b, b_end;
+  int f, f_end;
+  // what is left of the lane's token after the chunk, with 2^later to come; of the state before it
+  __device__ __forceinline__ float kept(float later) const { return f == f_end ? __builtin_amdgcn_exp2f(b_end - b + later) : 0.0f; }
+  __device__ __forceinline__ float before() const { return f == 0 ? __builtin_amdgcn_exp2f(b) : 0.0f; }
+};
+
 // This workgroup's (sequence, head, slice, segment), and where its tokens are.
 template <int DK, int DVS> struct Place {
   int b, seg, h, slice, len, t_lo, t_hi, t_end;
@@ -236,9 +247,16 @@ template <int DK, int DVS> struct Place {
   __device__ __forceinline__ float decay(int t, int lane) const {
     return g[static_cast<size_t>(min(t + lane, t_end - 1)) * g_stride];
   }
-  // the running sum of log2 decays, from what decay() has loaded
-  __device__ __forceinline__ float running(float x, int t, int lane) const {
-    return wave_sum_up(t + lane < t_end ? log2_decay(x) : 0.0f);
+  // the running sums, from what decay() has loaded
+  __device__ __forceinline__ Sums running(float x, int t, int lane) const {
+    const bool live = t + lane < t_end, forgets = live && x < kLeast;
+    const unsigned long long all = __ballot(forgets);
+    Sums r;
+    r.b = wave_sum_up(live && !forgets ? x * kLn2Inv : 0.0f);
+    r.f = __builtin_amdgcn_mbcnt_hi(static_cast<unsigned>(all >> 32), __builtin_amdgcn_mbcnt_lo(static_cast<unsigned>(all), forgets));
+    r.b_end = __int_as_float(__builtin_amdgcn_readlane(__float_as_int(r.b), 63));
+    r.f_end = __popcll(all);
+    return r;
   }
 };
 
@@ -335,13 +353,12 @@ __global__ __launch_bounds__(threads_of(DVS), waves_of(DK, DVS)) void linear_sta
   if (n) load(at.t_lo + (n - 1) * kC);
   const typename KB::ColLane kc = KB::col_lane(lane);
   const unsigned vc = ldv + 64 * (w >> 1) + (w & 1 ? VB::col_lane(lane).at[1] : VB::col_lane(lane).at[0]);
-  for (int i = n - 1; i >= 0 && !(later <= -150.0f); --i) {
+  for (int i = n - 1; i >= 0 && !(later <= kGone); --i) {
     KB::put(kx, ldk, tid);
     VB::put(vx, ldv, tid);
-    const float bt = at.running(gx, at.t_lo + i * kC, lane);
-    const float b_end = __int_as_float(__builtin_amdgcn_readlane(__float_as_int(bt), 63));
-    sw[w][lane] = __builtin_amdgcn_exp2f(b_end - bt + later);
-    later += b_end;
+    const Sums sums = at.running(gx, at.t_lo + i * kC, lane);
+    sw[w][lane] = sums.kept(later);
+    later = sums.f_end ? kGone : later + sums.b_end;
     lds_barrier();
     if (i) load(at.t_lo + (i - 1) * kC);
     u32x4_t v[2];
@@ -361,8 +378,10 @@ __global__ __launch_bounds__(threads_of(DVS), waves_of(DK, DVS)) void linear_fwd
   typedef Rows64<DK, NT> KB;
   typedef Rows64<DVS, NT> VB;
   __shared__ __attribute__((aligned(16))) unsigned char smem[2 * KB::kBytes + VB::kBytes + 2 * kScores];
-  __shared__ __attribute__((aligned(16))) float mb[kC], me[kC], mw[kC];  // b, scale exp(b), exp(b_63 - b)
-  __shared__ float mkeep;                                                // exp(b_63)
+  // b, the number that forget, scale exp(b), exp(b_63 - b); exp(b_63)
+  __shared__ __attribute__((aligned(16))) float mb[kC], me[kC], mw[kC];
+  __shared__ __attribute__((aligned(16))) int mf[kC];
+  __shared__ float mkeep;
   const int tid = threadIdx.x, lane = tid & 63, w = uni(tid >> 6);
   const int c = lane & 15, g = lane >> 4;
   const unsigned ldk = lds_addr(smem), ldv = ldk + KB::kBytes, ldq = ldv + VB::kBytes, ldp = ldq + KB::kBytes;
@@ -436,12 +455,12 @@ __global__ __launch_bounds__(threads_of(DVS), waves_of(DK, DVS)) void linear_fwd
     KB::put_paired(qx, ldq, tid);
     VB::put(vx, ldv, tid);
     if (w == NW - 1) {  // (the first ones have two tiles of scores)
-      const float bt = at.running(gx, t, lane);
-      const float b_end = __int_as_float(__builtin_amdgcn_readlane(__float_as_int(bt), 63));
-      mb[lane] = bt;
-      me[lane] = __builtin_amdgcn_exp2f(bt) * a.scale;
-      mw[lane] = __builtin_amdgcn_exp2f(b_end - bt);
-      if (lane == 0) mkeep = __builtin_amdgcn_exp2f(b_end);
+      const Sums sums = at.running(gx, t, lane);
+      mb[lane] = sums.b;
+      mf[lane] = sums.f;
+      me[lane] = sums.before() * a.scale;
+      mw[lane] = sums.kept(0.0f);
+      if (lane == 63) mkeep = sums.before();
     }
     lds_barrier();
     if (t + kC < at.t_end) load(t + kC);
@@ -473,12 +492,14 @@ __global__ __launch_bounds__(threads_of(DVS), waves_of(DK, DVS)) void linear_fwd
 #pragma unroll
       for (int d = 0; d < DK / 32; ++d) p = mfma(KB::pairs(k0, kr, d), KB::rows(0, q0, d), p);
       const float btt = mb[16 * j + c];
+      const int ftt = mf[16 * j + c];
       const f32x4_t bs = *reinterpret_cast<const f32x4_t *>(&mb[16 * i + 4 * g]);
+      const i32x4_t fs = *reinterpret_cast<const i32x4_t *>(&mf[16 * i + 4 * g]);
       float x[4];
 #pragma unroll
       for (int e = 0; e < 4; ++e) {
         const float f = p[e] * a.scale * __builtin_amdgcn_exp2f(btt - bs[e]);
-        x[e] = i < j || 4 * g + e <= c ? f : 0.0f;
+        x[e] = (i < j || 4 * g + e <= c) && fs[e] == ftt ? f : 0.0f;
       }
       const u32x2_t hi = {pack_bf16x2(x[0], x[1]), pack_bf16x2(x[2], x[3])};
       const u32x2_t lo = {pack_bf16x2(x[0] - bf16lo(hi[0]), x[1] - bf16hi(hi[0])),
@@ -592,7 +613,7 @@ template <int COLS> __global__ __launch_bounds__(256) void linear_step(LinearSte
     ks[tid] = bf16_to_f32(k[tid]);
   }
   const float g = a.log_decay[a.gated ? row : h];
-  const float keep = __builtin_amdgcn_exp2f(log2_decay(g));
+  const float keep = g < kLeast ? 0.0f : __builtin_amdgcn_exp2f(g * kLn2Inv);
   const u32x2_t vw = *reinterpret_cast<const u32x2_t *>(static_cast<const bf16_t *>(a.v) + n * a.v_stride +
                                                         static_cast<size_t>(h) * a.dv + at);
   const f32x4_t v = {bf16lo(vw[0]), bf16hi(vw[0]), bf16lo(vw[1]), bf16hi(vw[1])};

@@ -429,8 +429,8 @@ rglru_status rglru_prefix_attention(const void *q, const void *k_pages, const vo
  * h / (H / Hk). Forward only, for serving.
  *  q, k [B][T][Hk][dk], v [B][T][H][dv] bf16, *_stride elements from token to token (a multiple of 8; a sequence's
  *    tokens are T * stride apart from the next one's), 16-byte aligned
- *  log_decay f32: gated = 0: [H], g_t constant; else [B][T][H]. Meant to be <= 0; below -104 (-inf: the state is
- *    forgotten) it counts as -104, whose exponential is 0 in fp32
+ *  log_decay f32: gated = 0: [H], g_t constant; else [B][T][H]. Meant to be <= 0; below -104, where its
+ *    exponential is 0 in fp32 (-inf), the state is forgotten
  *  lens [B] int32 or NULL (all T); values are taken into [0, T]. Rows t >= lens[b]: o = 0, and nothing in those rows of
  *    q, k, v and log_decay is used (they may hold anything)
  *  s0 [B][H][dk][dv] f32 or NULL (zeros); s_out the same or NULL, out: S after the last token (s0 if there is none); may
@@ -441,7 +441,8 @@ rglru_status rglru_prefix_attention(const void *q, const void *k_pages, const vo
  * The state, all sums and all decays are fp32. Operands of the contractions that are not inputs enter as sums of bf16
  * terms: the decayed scores and the state as two (about 16 bits), the decayed values that form the state as three (24
  * bits). A decay over several tokens of a chunk of 64 is taken from the difference of two of the chunk's running sums of
- * log decays, and relatively off by up to 2^-23 times their size (2^-13 behind six tokens that forget the state). Sums are taken in a fixed order: results are bitwise reproducible. An infinite or NaN input reaches no row before
+ * log decays (without those below -104, which are counted), and relatively off by up to 2^-23 times their size. Sums are
+ * taken in a fixed order: results are bitwise reproducible. An infinite or NaN input reaches no row before
  * its own token, and the rows from there on until what it is in has decayed by 2^-150 (from then on it may or may not).
  * Outputs must not overlap the inputs (but for s_out = s0) or each other. Supported: dt = RGLRU_BF16, dk, dv in {64, 128,
  * 256}, H % Hk == 0, strides <= 2^20. */

@@ -531,6 +531,25 @@ def test_linear_decays_of_all_strengths():
     assert torch.allclose(s2[:, 2], s[:, 2], rtol=1e-5, atol=1e-5)
 
 
+@pytest.mark.parametrize("T", [200, 1100])
+def test_linear_forgetting_is_exact(T):
+    """Many tokens that forget the state (documents in one row): the others' weights are as exact as without them, so
+    the running sums that count are those of the other tokens alone."""
+    rng = np.random.default_rng(T)
+    B, H, dk, dv = 2, 3, 64, 128
+    q, k, v, g, s0 = linear_inputs(rng, B, T, 1, H, dk, dv, True, True)
+    others = g.clone()
+    for b in range(B):
+        for t in rng.choice(T, T // 7, replace=False):
+            g[b, t] = torch.tensor([-float("inf"), -1e9, -104.5], device=DEV)
+            others[b, t] = 0
+    o, s = rg.linear_attention(q, k, v, g, s0)
+    ro, rs, ao, as_ = sv.linear_attention(num(q), num(k), num(v), num(g), num(s0))
+    es = (2 * T + 200 + 16 * chunk_sums(others, B, T, H)) * W24
+    check(s, rs, es * as_, "state")
+    check(o, ro, ((es + (dk + 64) * W24 + 2.0 ** -16) * ao + U * np.abs(ro)) * (1 + U), "o")
+
+
 @pytest.mark.parametrize("bad", [float("nan"), float("inf")])
 @pytest.mark.parametrize("dk,dv", [(64, 64), (128, 256), (256, 128)])
 def test_linear_bad_inputs_reach_later_rows_only(bad, dk, dv):

@@ -696,10 +696,11 @@ hipError_t launch_linear_attention(const LinearArgs &a, hipStream_t s) {
 }
 
 hipError_t launch_linear_step(const LinearStepArgs &a, hipStream_t s) {
-  // few rows: narrow slices, so that more workgroups share them
-  const long long rows = static_cast<long long>(a.N) * a.H;
-  if (a.dv == 64 || rows * (a.dv / 64) <= 1024) return rows * (a.dv / 64) > 256 ? launch<64>(a, s) : launch<32>(a, s);
-  return a.dv == 128 ? launch<128>(a, s) : launch<256>(a, s);
+  // 64 values for a workgroup (dk128 dv256, 4096 rows: 210 us, with 128 values 218, with 256 233, with 32 224); 32 while
+  // that leaves the chip short of workgroups, the sooner the longer each one is (dk128 dv128: 16 rows 3.1 us, with 64
+  // values 3.4, 512 rows 13.4 and 11.4; dk256 dv256: 32 rows 5.2 and 7.9, 512 rows 42 and 41)
+  const long long groups = static_cast<long long>(a.N) * a.H * (a.dv / 64);
+  return groups <= 2 * a.dk ? launch<32>(a, s) : launch<64>(a, s);
 }
 
 }  // namespace rglru

@@ -208,7 +208,7 @@ struct LinearArgs {
 struct LinearPlan {
   int segs, seg_len;
 };
-LinearPlan linear_plan(int B, int T, int H, int dv);
+LinearPlan linear_plan(int B, int T, int H, int dk, int dv);
 hipError_t launch_linear_attention(const LinearArgs &a, hipStream_t s);
 struct LinearStepArgs {
   const void *q, *k, *v;

@@ -641,12 +641,16 @@ template <int COLS> __global__ __launch_bounds__(256) void linear_step(LinearSte
   }
 }
 
-// Segments of a prompt: as many as give the chip two workgroups a CU, of four chunks at least.
-LinearPlan linear_plan(int B, int T, int H, int dv) {
-  const long long groups = static_cast<long long>(B) * H * (dv == 64 ? 1 : dv / 128);
+// Segments of a prompt: 256 workgroups, one a CU, where a workgroup's state has 16384 values or more (more segments are
+// more states to form: B1 T32768 H16 dk256 dv256 503 us, with 512 workgroups 559; B8 T2048 H16 dk128 dv128 98 and 102),
+// else 512 (B6 T4096 H16 dk64 dv128 103 us, with 256 118); 320 leave some CUs twice the others' work (744, 99, 123). Of
+// two chunks at least (B1 T2048 H8 dk128 dv128 31 us, with four 38.6, with one 35; T128 12, with one 15.8).
+LinearPlan linear_plan(int B, int T, int H, int dk, int dv) {
+  const int dvs = dv == 64 ? 64 : 128;
+  const long long groups = static_cast<long long>(B) * H * (dv / dvs);
   const int chunks = (T + kC - 1) / kC;
-  long long segs = std::max<long long>(512 / groups, 1);
-  segs = std::min<long long>(segs, std::max(chunks / 4, 1));
+  long long segs = std::max<long long>((dk * dvs < 16384 ? 512 : 256) / groups, 1);
+  segs = std::min<long long>(segs, std::max(chunks / 2, 1));
   LinearPlan p;
   p.seg_len = static_cast<int>((chunks + segs - 1) / segs) * kC;
   p.segs = (T + p.seg_len - 1) / p.seg_len;

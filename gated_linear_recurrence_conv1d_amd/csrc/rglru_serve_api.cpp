@@ -142,7 +142,7 @@ size_t rglru_linear_attention_workspace_size(int B, int T, int Hk, int H, int dk
   if (check_prompt(B, T, Hk, H, dk, dv, static_cast<long long>(Hk) * dk, static_cast<long long>(Hk) * dk,
                    static_cast<long long>(H) * dv, 0.0f, RGLRU_BF16) != RGLRU_OK)
     return 0;
-  return linear_bytes(rglru::linear_plan(B, T, H, dv), B, H, dk, dv);
+  return linear_bytes(rglru::linear_plan(B, T, H, dk, dv), B, H, dk, dv);
 }
 
 rglru_status rglru_linear_attention(const void *q, const void *k, const void *v, const float *log_decay,
@@ -157,7 +157,7 @@ rglru_status rglru_linear_attention(const void *q, const void *k, const void *v,
   for (const void *p : vec16)
     if (!aligned(p, 16)) return RGLRU_ERR_INVALID_ARG;
   if (!aligned(log_decay, 4) || !aligned(lens, 4)) return RGLRU_ERR_INVALID_ARG;
-  const rglru::LinearPlan plan = rglru::linear_plan(B, T, H, dv);
+  const rglru::LinearPlan plan = rglru::linear_plan(B, T, H, dk, dv);
   const size_t need = linear_bytes(plan, B, H, dk, dv);
   if (need && (!workspace || workspace_bytes < need)) return RGLRU_ERR_WORKSPACE;
   if (need && !aligned(workspace, 16)) return RGLRU_ERR_INVALID_ARG;

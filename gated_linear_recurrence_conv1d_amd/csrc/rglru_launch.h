@@ -195,18 +195,19 @@ struct LinearArgs {
   const float *s0;         // or NULL: zeros
   void *o;
   float *s_out;  // or NULL; may be s0
-  float *seg;    // [B][H][segs][dk][dv]: the segments' first states (segs > 1)
-  float *sums;   // [B][H][segs - 1]: their summed log2 decays
+  float *seg;    // [B][H][states + 1][dk][dv]: room for s0, then the states of parts of segments (states > 0)
+  float *sums;   // [B][H][states]: their summed log2 decays
   int B, T, Hk, H, dk, dv;
   long long q_stride, k_stride, v_stride;
   float scale;
   bool gated;
   int segs, seg_len;
-  int run;       // segments of a launch, and
-  bool chained;  // whether seg holds what each segment starts from (both set by the launcher)
+  int sub, states;  // parts of a segment whose states are formed alone; of all segments but the last
+  int run;          // segments or parts of a launch, and
+  bool chained;     // whether seg holds what each segment starts from (both set by the launcher)
 };
 struct LinearPlan {
-  int segs, seg_len;
+  int segs, seg_len, sub, states;
 };
 LinearPlan linear_plan(int B, int T, int H, int dk, int dv);
 hipError_t launch_linear_attention(const LinearArgs &a, hipStream_t s);

@@ -18,10 +18,10 @@
 // S and P enter as bf16 hi + lo and w V as three bf16 terms (8 + 8 + 8 bits): the state is an fp32 result and o is
 // then within the rounding of its own type; with one term each, o would be off by as much again for each of them.
 //
-// With few (sequence, head, slice)s the prompt is cut into segments: linear_state first forms each segment's own state (K
-// and V only), and linear_fwd starts each segment from the chain of those before it: up to kFew segments it forms the
-// chain itself (they are read 1.5 times on average; at B8 T2048 H16 with 4, 9.5 us of a launch less), else linear_carry
-// has done so in place.
+// With few (sequence, head, slice)s the prompt is cut into segments: linear_state first forms the states of their own
+// tokens (K and V only; of a segment whole, or of parts of it), and linear_fwd starts each segment from the chain of those
+// before it: up to kFew states it forms the chain itself (at B8 T2048 H16 9.5 us of a launch less), else linear_carry has
+// done so in place.
 #include "rglru_attn.h"
 #include "rglru_grid.h"
 #include "rglru_launch.h"
@@ -35,7 +35,7 @@ using namespace attn;
 namespace {
 
 constexpr int kC = 64;              // tokens per chunk
-constexpr int kFew = 4;             // segments that are chained where they are needed
+constexpr int kFew = 4;             // states that are chained where they are needed
 constexpr float kLeast = -104.0f;   // exp of it is 0 in fp32: a smaller log decay (-inf) forgets the state
 constexpr float kGone = -150.0f;    // exp2 of it is 0 in fp32
 
@@ -324,7 +324,7 @@ template <int DK> __device__ __forceinline__ void load_state(f32x4_t (&S)[DK / 1
 constexpr int threads_of(int DVS) { return DVS * 4; }
 constexpr int waves_of(int DK, int DVS) { return (DK == 256 ? 1 : 2) * (DVS / 64); }
 
-// The state of a segment's own tokens at its end (to the next one's a.seg), and its summed g (a.sums). Chunks from the
+// The state of the own tokens of a segment, or of a part of one, at its end (to the next one's a.seg), and its summed g (a.sums). Chunks from the
 // last one back: once what follows has decayed by 2^-150 in all, which is 0 in fp32, no earlier token counts.
 template <int DK, int DVS>
 __global__ __launch_bounds__(threads_of(DVS), waves_of(DK, DVS)) void linear_state(LinearArgs a) {
@@ -367,8 +367,8 @@ __global__ __launch_bounds__(threads_of(DVS), waves_of(DK, DVS)) void linear_sta
     add_outer<DK, KB>(S, v, sw[w], ldk, kc, g);
     lds_barrier();  // everyone is done with the chunk
   }
-  if (tid == 0 && at.slice == 0) a.sums[at.head * (a.segs - 1) + at.seg] = later;
-  store_state<DK>(S, a.seg + (at.head * a.segs + at.seg + 1) * static_cast<size_t>(DK) * a.dv + at.slice * DVS + 16 * w,
+  if (tid == 0 && at.slice == 0) a.sums[at.head * a.states + at.seg] = later;
+  store_state<DK>(S, a.seg + (at.head * (a.states + 1) + at.seg + 1) * static_cast<size_t>(DK) * a.dv + at.slice * DVS + 16 * w,
                   a.dv);
 }
 
@@ -404,16 +404,17 @@ __global__ __launch_bounds__(threads_of(DVS), waves_of(DK, DVS)) void linear_fwd
   f32x4_t S[DK / 16];
   const size_t dkv = static_cast<size_t>(DK) * a.dv;
   const int col = at.slice * DVS + 16 * w;
-  if (const float *from = a.chained ? a.seg + (at.head * a.segs + at.seg) * dkv : a.s0 ? a.s0 + at.head * dkv : nullptr) {
+  const int before = at.seg * a.sub;  // states before the segment
+  if (const float *from = a.chained ? a.seg + (at.head * (a.states + 1) + before) * dkv : a.s0 ? a.s0 + at.head * dkv : nullptr) {
     load_state<DK>(S, from + col, a.dv);
   } else {
 #pragma unroll
     for (int i = 0; i < DK / 16; ++i) S[i] = f32x4_t{};
   }
-  for (int j = 0; !a.chained && j < at.seg; ++j) {
-    const float keep = __builtin_amdgcn_exp2f(uniform_load(a.sums, at.head * (a.segs - 1) + j));
+  for (int j = 0; !a.chained && j < before; ++j) {
+    const float keep = __builtin_amdgcn_exp2f(uniform_load(a.sums, at.head * a.states + j));
     f32x4_t own[DK / 16];
-    load_state<DK>(own, a.seg + (at.head * a.segs + j + 1) * dkv + col, a.dv);
+    load_state<DK>(own, a.seg + (at.head * (a.states + 1) + j + 1) * dkv + col, a.dv);
 #pragma unroll
     for (int i = 0; i < DK / 16; ++i) S[i] = S[i] * keep + own[i];
   }
@@ -566,8 +567,8 @@ __global__ __launch_bounds__(256) void linear_carry(LinearArgs a) {
   if (head >= static_cast<size_t>(a.B) * a.H) return;
   const size_t at = (i - head * quads) * 4;
   f32x4_t s = a.s0 ? *reinterpret_cast<const f32x4_t *>(a.s0 + head * dkv + at) : f32x4_t{};
-  const int n = a.segs - 1;
-  float *const own = a.seg + head * a.segs * dkv + at;
+  const int n = a.states;
+  float *const own = a.seg + head * (n + 1) * dkv + at;
   *reinterpret_cast<f32x4_t *>(own) = s;
   constexpr int kFly = 4;
   for (int j0 = 0; j0 < n; j0 += kFly) {
@@ -649,11 +650,22 @@ LinearPlan linear_plan(int B, int T, int H, int dk, int dv) {
   const int dvs = dv == 64 ? 64 : 128;
   const long long groups = static_cast<long long>(B) * H * (dv / dvs);
   const int chunks = (T + kC - 1) / kC;
-  long long segs = std::max<long long>((dk * dvs < 16384 ? 512 : 256) / groups, 1);
+  const int target = dk * dvs < 16384 ? 512 : 256;
+  long long segs = std::max<long long>(target / groups, 1);
   segs = std::min<long long>(segs, std::max(chunks / 2, 1));
+  const int in_seg = static_cast<int>((chunks + segs - 1) / segs);
   LinearPlan p;
-  p.seg_len = static_cast<int>((chunks + segs - 1) / segs) * kC;
+  // the states of few segments in parts, where forming them leaves CUs idle and the chain of them stays short (B8 T2048
+  // H16 dk128 dv128, decays of heads: 101 us, whole 107; B16 T1024 H8 dk256 dv128 88 and 91; but B1 T2048 H8 dk128 dv128
+  // with 30 states 37, with 15 31)
+  const long long before = std::max((chunks + in_seg - 1) / in_seg - 1, 1);
+  const int sub = static_cast<int>(std::max<long long>(
+      std::min<long long>({target / (before * groups), kFew / before, in_seg}), 1));
+  const int in_state = (in_seg + sub - 1) / sub;
+  p.sub = (in_seg + in_state - 1) / in_state;
+  p.seg_len = p.sub * in_state * kC;
   p.segs = (T + p.seg_len - 1) / p.seg_len;
+  p.states = (p.segs - 1) * p.sub;
   return p;
 }
 
@@ -661,14 +673,17 @@ namespace {
 
 template <int DK, int DVS> hipError_t launch(LinearArgs a, hipStream_t s) {
   const long long rows = static_cast<long long>(a.B) * a.H * (a.dv / DVS);
-  if (a.segs > 1) {
-    a.run = a.segs - 1;
+  if (a.states) {
+    const int seg_len = a.seg_len;
+    a.run = a.states;
+    a.seg_len /= a.sub;
     const long long g = rows * a.run;
     linear_state<DK, DVS><<<dim3(grid_x(g), grid_rows(g)), threads_of(DVS), 0, s>>>(a);
     const hipError_t e = hipGetLastError();
     if (e != hipSuccess) return e;
     // (where the last state goes over the first one, the segments need a copy of that)
-    a.chained = a.segs > kFew || (a.s0 && a.s_out == a.s0);
+    a.chained = a.states > kFew || (a.s0 && a.s_out == a.s0);
+    a.seg_len = seg_len;
   }
   if (a.chained) {
     const long long c = (static_cast<long long>(a.B) * a.H * DK * (a.dv / 4) + 255) / 256;

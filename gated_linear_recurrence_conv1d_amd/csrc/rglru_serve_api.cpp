@@ -67,11 +67,11 @@ rglru_status check_prompt(int B, int T, int Hk, int H, int dk, int dv, long long
 
 // The segments' states, then their decays.
 size_t seg_bytes(const rglru::LinearPlan &p, int B, int H, int dk, int dv) {
-  return rglru::align_up(static_cast<size_t>(B) * H * p.segs * dk * dv * sizeof(float));
+  return rglru::align_up(static_cast<size_t>(B) * H * (p.states + 1) * dk * dv * sizeof(float));
 }
 size_t linear_bytes(const rglru::LinearPlan &p, int B, int H, int dk, int dv) {
-  if (p.segs == 1) return 0;
-  return seg_bytes(p, B, H, dk, dv) + rglru::align_up(static_cast<size_t>(B) * H * (p.segs - 1) * sizeof(float));
+  if (!p.states) return 0;
+  return seg_bytes(p, B, H, dk, dv) + rglru::align_up(static_cast<size_t>(B) * H * p.states * sizeof(float));
 }
 
 }  // namespace
@@ -180,7 +180,8 @@ rglru_status rglru_linear_attention(const void *q, const void *k, const void *v,
   }
   a.B = B, a.T = T, a.Hk = Hk, a.H = H, a.dk = dk, a.dv = dv;
   a.q_stride = q_stride, a.k_stride = k_stride, a.v_stride = v_stride;
-  a.scale = scale, a.gated = gated != 0, a.segs = plan.segs, a.seg_len = plan.seg_len;
+  a.scale = scale, a.gated = gated != 0, a.segs = plan.segs, a.sub = plan.sub, a.states = plan.states;
+  a.seg_len = plan.seg_len;
   (void)hipGetLastError();
   return hip_status(rglru::launch_linear_attention(a, static_cast<hipStream_t>(stream)));
 }

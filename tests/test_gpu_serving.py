@@ -494,7 +494,7 @@ def test_linear_attention(B, T, Hk, H, dk, dv, lens, gated, start):
     assert torch.equal(o, o2)
 
 
-@pytest.mark.parametrize("T", [250, 512, 520, 800, 1100, 1300, 2500])  # 2, 4, 3, 5, 9, 7 and 20 segments
+@pytest.mark.parametrize("T", [250, 512, 520, 800, 1100, 1300, 2500])  # 2 to 20 segments, states of parts
 def test_linear_segments(T):
     """Segments whose decays let nothing, a part or all of the ones before them through, and sequences that end in the
     first, in a middle and in the last one."""

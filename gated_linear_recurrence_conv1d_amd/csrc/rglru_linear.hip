@@ -22,6 +22,12 @@
 // tokens (K and V only; of a segment whole, or of parts of it), and linear_fwd starts each segment from the chain of those
 // before it: up to kFew states it forms the chain itself (at B8 T2048 H16 9.5 us of a launch less), else linear_carry has
 // done so in place.
+//
+// B8 T2048 H16 dk128 dv128: 24 us of states and 86; B1 T65536 H8 dk128 dv256: 30, 9 of the chain and 283 (607 MB in all,
+// 125 us at a copy's rate). A wave's chunk has 97 matrix instructions (59 without the lower terms) and 605 vector ones,
+// half of them the splitting into terms. With one workgroup on each CU matrix units are busy for 30% of the time, vector
+// units for 47%, LDS for 36%; two waves a SIMD hardly hide one behind the other, and the rest is waiting at the three
+// barriers. With two workgroups a CU the waits overlap, but the states of twice the segments cost as much.
 #include "rglru_attn.h"
 #include "rglru_grid.h"
 #include "rglru_launch.h"
@@ -89,8 +95,8 @@ __device__ __forceinline__ f32x4_t mfma(u32x4_t a, u32x4_t b, f32x4_t c) {
 }  // namespace
 
 // 64 rows of DH bf16 in LDS, 64 bytes apart beyond their length, the 16-byte chunk c of each 64 bytes of row r at c ^
-// turn(r): the 16 rows at one chunk of a pass, and 8 rows at 2 neighbouring chunks of another, fall on different banks,
-// and the steps along a row are constant offsets. Lanes are c = lane % 16, g = lane / 16.
+// turn(r): what is read at once falls on different banks (16 rows at one chunk, 8 rows at 2 neighbouring chunks, 8 rows at
+// one and the 8 others at its neighbour), and the steps along a row are constant offsets. Lanes are c = lane % 16, g = lane / 16.
 template <int DH, int NT> struct Rows64 {
   static constexpr unsigned kStride = 2 * DH + 64, kBytes = kC * kStride;
   static constexpr int kCPR = DH / 8, kN = kC * kCPR / NT;  // 16-byte chunks per row; per thread
@@ -107,7 +113,7 @@ template <int DH, int NT> struct Rows64 {
     for (int i = 0; i < kN; ++i)
       x[i] = __builtin_bit_cast(u32x4_t, __builtin_amdgcn_raw_buffer_load_b128(src, at + i * kRows * row_bytes, 0, 0));
   }
-  __device__ __forceinline__ static int turn(int r) { return 2 * ((r >> 2) & 1) + ((r >> 3) & 1); }
+  __device__ __forceinline__ static int turn(int r) { return (2 * ((r >> 2) & 1)) ^ (3 * ((r >> 3) & 1)); }
   __device__ __forceinline__ static unsigned chunk(int r, int c) {  // of row r, its place
     return r * kStride + (c >> 2) * 64 + (((c & 3) ^ turn(r)) * 16);
   }
@@ -586,8 +592,9 @@ __global__ __launch_bounds__(256) void linear_carry(LinearArgs a) {
   }
 }
 
-// One token: workgroup = (sequence, head, `cols` of the values), the state read and written once. A row of the slice
-// is cols / 4 lanes' 16 bytes; rows are dealt to the lane groups, whose shares of o meet in LDS.
+// One token: workgroup = (sequence, head, COLS of the values), the state read and written once. A row of the slice
+// is COLS / 4 lanes' 16 bytes; rows are dealt to the lane groups, whose shares of o meet in LDS. Bound by memory: 4096
+// states of dk128 dv256 in 210 us (1.07 GB, 5.1 TB/s: a plain copy's rate), 8 of dk128 dv128 in 3.7 us.
 template <int COLS> __global__ __launch_bounds__(256) void linear_step(LinearStepArgs a) {
   constexpr int kLanes = COLS / 4, kGroups = 256 / kLanes, kFly = 8;
   __shared__ float qs[256], ks[256];

@@ -16,6 +16,12 @@
 // bf16), so that both contractions see plain bf16 and one conversion serves 128 rows.
 // A window may have left a part of the prefix for some rows and not for others: masked entries get P = 0, and where
 // 0 * V is not 0 (a V that is infinite or NaN) the row is done again key by key.
+//
+// N256 Hq8 Hkv2 dh128 P32000 in e4m3, up to 400 own tokens: 77 us and 9.3 us of joining. A block of 32 keys has 24 matrix
+// instructions a wave (768 cycles; P's lower half is a third of them) and 700 cycles of vector work, half of it in 16
+// exponentials, and takes 1420: with the two waves that a SIMD's registers hold, the one hardly hides behind the other.
+// Softmax of a block between the matrix instructions of the one before (79 us) or of all three stages (188, spilled)
+// gained nothing. N64 Hq16 dh256 P1999 in bf16: 30 us and 6.8 us, most of it each chunk's latency and its O (17 MB).
 #include "rglru_attn.h"
 #include "rglru_e4m3.h"
 #include "rglru_grid.h"

@@ -35,7 +35,7 @@ using namespace attn;
 
 namespace {
 
-constexpr int kAhead = 3;  // MFMA steps that LDS operands are read ahead
+constexpr int kAhead = 2;  // MFMA steps that LDS operands are read ahead (3: 3% slower in e4m3 at dh128, else the same)
 
 // dma_16b from an address per lane: 64 lanes x 16 bytes to LDS at lds_base + 16 lane.
 __device__ __forceinline__ void dma_16b_from(const void *p, unsigned lds_base) {
@@ -125,7 +125,7 @@ __device__ __forceinline__ void prefix_rows(const PrefixArgs &a, int chunk, int 
   auto &bads = mem.bads;
   const int tid = threadIdx.x, lane = tid & 63, w = uni(tid >> 6);
   const unsigned lds = lds_addr(smem);
-  const int lrow = lane & 31, half = lane >> 5;
+  const int half = lane >> 5;
   const int G = a.Hq / a.Hkv;
   const long long R = static_cast<long long>(a.N) * G;  // rows of a key/value head
   const int tiles = static_cast<int>((R + kOwn - 1) / kOwn);
@@ -196,9 +196,14 @@ __device__ __forceinline__ void prefix_rows(const PrefixArgs &a, int chunk, int 
   constexpr int kCW = kCode ? DH / 32 : 1;  // words
   uint32_t ck[kCW], cv[kCW];
   unsigned sk = 0, sv = 0;
-  const int crow = tid >> 3, cpart = tid & 7;
+  // (the thread's terms are formed where they are needed: kept, they take registers from the walk)
+  auto mine_of = [&]() {
+    int x = threadIdx.x;
+    asm volatile("" : "+v"(x));
+    return x;
+  };
   auto look_up = [&](int b) {
-    const int u = min(b * kBlk + (kCode ? crow : lrow), P - 1);  // (past the prefix: its last key)
+    const int u = min(b * kBlk + (kCode ? mine_of() >> 3 : mine_of() & 31), P - 1);  // (past the prefix: its last key)
     const int t = u / a.page;
     key_page = a.prefix_table[t];
     key_at = u - t * a.page;
@@ -207,7 +212,7 @@ __device__ __forceinline__ void prefix_rows(const PrefixArgs &a, int chunk, int 
   auto key_row = [&]() { return bad_key() ? 0 : key_page * a.page + key_at; };  // the pool's; for a bad page row 0
   auto load_codes = [&]() {
     const int row = key_row();
-    const char *const kr = kp + row * row_bytes + cpart * (DH / 8), *const vr = vp + (kr - kp);
+    const char *const kr = kp + row * row_bytes + (mine_of() & 7) * (DH / 8), *const vr = vp + (kr - kp);
 #pragma unroll
     for (int i = 0; i < kCW; i += 4) {
       if constexpr (kCW >= 4) {
@@ -232,6 +237,7 @@ __device__ __forceinline__ void prefix_rows(const PrefixArgs &a, int chunk, int 
   };
   auto put = [&](const uint32_t *codes, unsigned b, unsigned dst) {
     const float s = __uint_as_float(b << 23);
+    const int me = mine_of(), crow = me >> 3, cpart = me & 7;
 #pragma unroll
     for (int i = 0; i < kCW / 2; ++i) {  // a 16-byte chunk of 8 values
       u32x4_t v;
@@ -339,9 +345,10 @@ __device__ __forceinline__ void prefix_rows(const PrefixArgs &a, int chunk, int 
     }
     const bool full = U + kBlk <= P && (U >= wmax || U + kBlk <= a.sinks) && bad == 0;
     if (!full) {
+      const int first = 4 * ((mine_of() >> 5) & 1);
 #pragma unroll
       for (int e = 0; e < 16; ++e) {
-        const int k = 8 * (e >> 2) + 4 * half + (e & 3), u = U + k;
+        const int k = 8 * (e >> 2) + first + (e & 3), u = U + k;
         const bool on = u < P && (u >= w0 || u < a.sinks);
         s[e] = !on ? -__builtin_inff() : (bad >> k) & 1 ? __builtin_nanf("") : s[e];
       }
@@ -450,8 +457,9 @@ __device__ __forceinline__ void prefix_rows(const PrefixArgs &a, int chunk, int 
 
 // Both parts in one launch, the prefix's workgroups first: those are bound by their products and the vector work
 // between them, the own tokens' by memory, and those fill the CUs that the longer ones leave.
+// Three workgroups a CU at dh 128 (at dh 64 four): the prefix's are two, so that own tokens run beside them.
 template <typename C, int DH, bool UNI>
-__global__ __launch_bounds__(64 * kWg, 2) void prefix_fwd(PrefixArgs a, PagedArgs own, int chunk, int own_chunk, int own_splits,
+__global__ __launch_bounds__(64 * kWg, DH == 128 ? 3 : 2) void prefix_fwd(PrefixArgs a, PagedArgs own, int chunk, int own_chunk, int own_splits,
                                                           int shared_groups, int own_groups) {
   __shared__ union Both {
     __device__ Both() {}
@@ -534,8 +542,8 @@ __global__ __launch_bounds__(256) void prefix_join(PrefixArgs a, PagedArgs own, 
 }
 
 // Blocks per chunk of the prefix, and the most chunks it can have. At least 4 blocks, as each chunk leaves an O of all
-// rows to write and read again (N64 Hq16 dh256 P1999: 36.5 us, with 2 blocks 41, with 8 44.5); 2 where the rows are few
-// and the chunks' number is the time (N6 Hq10 dh256 P700: 14.8 us, with 4 16.6).
+// rows to write and read again (N64 Hq16 dh256 P1999: 33.2 us, with 2 blocks 37.4, with 8 34.1); 2 where the rows are few
+// and a chunk's length is the time (N6 Hq10 dh256 P700: 13.2 us, with 4 15.7).
 PagedPlan prefix_plan(int N, int Hq, int Hkv, long long cap) {
   const long long tiles = (static_cast<long long>(N) * (Hq / Hkv) + kOwn - 1) / kOwn * Hkv;
   const long long blocks = (cap + kBlk - 1) / kBlk;

@@ -63,6 +63,7 @@ __device__ __forceinline__ u32x4_t split(float (&x)[8]) {
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
     h[i] = pack_bf16x2(x[2 * i], x[2 * i + 1]);
+    asm("" : "+v"(h[i]));  // (else the lower value is rounded a second time for the difference)
     x[2 * i] -= bf16lo(h[i]);
     x[2 * i + 1] -= bf16hi(h[i]);
   }

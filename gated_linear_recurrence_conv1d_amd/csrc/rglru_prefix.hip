@@ -377,7 +377,8 @@ __device__ __forceinline__ void prefix_rows(const PrefixArgs &a, int chunk, int 
     for (int e = 0; e < 16; e += 2) {
       const float x = __builtin_amdgcn_exp2f((s[e] - m) * a.c), y = __builtin_amdgcn_exp2f((s[e + 1] - m) * a.c);
       l += x + y;
-      const uint32_t hw = pack_bf16x2(x, y);
+      uint32_t hw = pack_bf16x2(x, y);
+      asm("" : "+v"(hw));  // (else x is rounded a second time for the difference)
       p[e >> 3][(e >> 1) & 3] = hw;
       pl[e >> 3][(e >> 1) & 3] = pack_bf16x2(x - bf16lo(hw), y - bf16hi(hw));
     }

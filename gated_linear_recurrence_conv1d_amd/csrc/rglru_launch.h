@@ -182,9 +182,11 @@ struct PrefixArgs {
   long long q_stride, prefix_cap;
   int num_pages, page, parts, window, sinks;
   float c, floor;
+  unsigned page_factor;  // division by page (both set by the launcher)
+  int page_shift;
 };
 PagedPlan prefix_plan(int N, int Hq, int Hkv, long long cap);
-hipError_t launch_prefix_attention(const PrefixArgs &a, const PagedArgs &own, const PagedPlan &p, const PagedPlan &po,
+hipError_t launch_prefix_attention(PrefixArgs a, const PagedArgs &own, const PagedPlan &p, const PagedPlan &po,
                                    hipStream_t s);
 
 // Linear attention with a decay for each head (bf16; dk, dv in {64, 128, 256}); state [B][H][dk][dv] f32.

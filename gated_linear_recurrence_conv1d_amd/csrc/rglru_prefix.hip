@@ -17,11 +17,11 @@
 // A window may have left a part of the prefix for some rows and not for others: masked entries get P = 0, and where
 // 0 * V is not 0 (a V that is infinite or NaN) the row is done again key by key.
 //
-// N256 Hq8 Hkv2 dh128 P32000 in e4m3, up to 400 own tokens: 77 us and 9.3 us of joining. A block of 32 keys has 24 matrix
-// instructions a wave (768 cycles; P's lower half is a third of them) and 700 cycles of vector work, half of it in 16
-// exponentials, and takes 1420: with the two waves that a SIMD's registers hold, the one hardly hides behind the other.
-// Softmax of a block between the matrix instructions of the one before (79 us) or of all three stages (188, spilled)
-// gained nothing. N64 Hq16 dh256 P1999 in bf16: 30 us and 6.8 us, most of it each chunk's latency and its O (17 MB).
+// N256 Hq8 Hkv2 dh128 P32000 in e4m3, up to 400 own tokens: 72 us and 9.4 us of joining. Matrix units are busy for 30% of
+// the time (a third of it P's lower halves), vector units for nearly 50% (a quarter of it the exponentials), and with the
+// two or three waves that a SIMD's registers hold, the one hardly hides behind the other. The softmax of a block between
+// the matrix instructions of the one before, or of all three stages, gained nothing (79 us for then 77, and 188, spilled).
+// N64 Hq16 dh256 P1999 in bf16: 27 us and 6.7 us, most of it each chunk's latency and its O (17 MB).
 #include "rglru_attn.h"
 #include "rglru_e4m3.h"
 #include "rglru_grid.h"
@@ -185,7 +185,7 @@ __device__ __forceinline__ void prefix_rows(const PrefixArgs &a, int chunk, int 
     return;
   }
 
-  const size_t row_bytes = static_cast<size_t>(a.Hkv) * DH * sizeof(C);
+  const unsigned row_bytes = static_cast<unsigned>(a.Hkv) * DH * sizeof(C);
   const char *const kp = static_cast<const char *>(a.k_pages) + static_cast<size_t>(kvh) * DH * sizeof(C);
   const char *const vp = static_cast<const char *>(a.v_pages) + static_cast<size_t>(kvh) * DH * sizeof(C);
   // A block's rows are looked up a block before they are loaded, and loaded a block before they are used. (What the
@@ -204,7 +204,7 @@ __device__ __forceinline__ void prefix_rows(const PrefixArgs &a, int chunk, int 
   };
   auto look_up = [&](int b) {
     const int u = min(b * kBlk + (kCode ? mine_of() >> 3 : mine_of() & 31), P - 1);  // (past the prefix: its last key)
-    const int t = u / a.page;
+    const int t = static_cast<int>(__umulhi(2u * u, a.page_factor) >> a.page_shift);  // u / page
     key_page = a.prefix_table[t];
     key_at = u - t * a.page;
   };
@@ -212,7 +212,8 @@ __device__ __forceinline__ void prefix_rows(const PrefixArgs &a, int chunk, int 
   auto key_row = [&]() { return bad_key() ? 0 : key_page * a.page + key_at; };  // the pool's; for a bad page row 0
   auto load_codes = [&]() {
     const int row = key_row();
-    const char *const kr = kp + row * row_bytes + (mine_of() & 7) * (DH / 8), *const vr = vp + (kr - kp);
+    const char *const kr = kp + static_cast<size_t>(static_cast<unsigned>(row)) * row_bytes + (mine_of() & 7) * (DH / 8),
+               *const vr = vp + (kr - kp);
 #pragma unroll
     for (int i = 0; i < kCW; i += 4) {
       if constexpr (kCW >= 4) {
@@ -255,7 +256,7 @@ __device__ __forceinline__ void prefix_rows(const PrefixArgs &a, int chunk, int 
 #pragma unroll
     for (int ii = 0; ii < K::kLPW; ++ii) {
       const int row = (w + kWg * ii) * K::kRPI + lane / K::kCPR;
-      const size_t at = static_cast<size_t>(__shfl(mine, row, 64)) * row_bytes +
+      const size_t at = static_cast<size_t>(static_cast<unsigned>(__shfl(mine, row, 64))) * row_bytes +
                         static_cast<unsigned>(((lane % K::kCPR) ^ K::swz(row)) * 16);
       const unsigned dst = static_cast<unsigned>(uni(slot + (w + kWg * ii) * 1024));
       dma_16b_from(kp + at, dst);
@@ -276,7 +277,7 @@ __device__ __forceinline__ void prefix_rows(const PrefixArgs &a, int chunk, int 
   f32x16_t acc[K::kDT];  // O^T
 #pragma unroll
   for (int j = 0; j < K::kDT; ++j) acc[j] = f32x16_t{};
-  float m = a.floor, l = 0.0f;
+  float m = a.floor, mc = m * a.c, l = 0.0f;
   int b = i0, bn = next_of(i0 + 1);  // this block and the next one
   look_up(b);
   unsigned bad_now = bad_bits(), bad_next = 0;
@@ -365,17 +366,19 @@ __device__ __forceinline__ void prefix_rows(const PrefixArgs &a, int chunk, int 
     mx = fmaxf(fmaxf(lo, hi), a.floor);
     const bool raise = (mx - m) * a.c > 8.0f;
     if (__any(raise)) {
-      const float mn = raise ? mx : m;
-      const float corr = __builtin_amdgcn_exp2f((m - mn) * a.c);
+      const float corr = raise ? __builtin_amdgcn_exp2f(mc - mx * a.c) : 1.0f;
       l *= corr;
-      m = mn;
+      m = raise ? mx : m;
+      mc = m * a.c;
 #pragma unroll
       for (int j = 0; j < K::kDT; ++j) acc[j] *= corr;
     }
+    // (s - m) c as one operation: m c is off by 2^-24 of itself, for all keys of a row alike, which o is not changed by;
+    // between a row's parts, and before and after the maximum is raised, weights are off by as much
     u32x4_t p[2], pl[2];  // P of two 16-key steps as bf16 hi + lo
 #pragma unroll
     for (int e = 0; e < 16; e += 2) {
-      const float x = __builtin_amdgcn_exp2f((s[e] - m) * a.c), y = __builtin_amdgcn_exp2f((s[e + 1] - m) * a.c);
+      const float x = __builtin_amdgcn_exp2f(fmaf(s[e], a.c, -mc)), y = __builtin_amdgcn_exp2f(fmaf(s[e + 1], a.c, -mc));
       l += x + y;
       uint32_t hw = pack_bf16x2(x, y);
       asm("" : "+v"(hw));  // (else x is rounded a second time for the difference)
@@ -590,8 +593,12 @@ hipError_t launch(const PrefixArgs &a, const PagedArgs &own, const PagedPlan &p,
 
 }  // namespace
 
-hipError_t launch_prefix_attention(const PrefixArgs &a, const PagedArgs &own, const PagedPlan &p, const PagedPlan &po,
+hipError_t launch_prefix_attention(PrefixArgs a, const PagedArgs &own, const PagedPlan &p, const PagedPlan &po,
                                    hipStream_t s) {
+  // u / page for u < 2^31 as (u f) >> (31 + s): 2^(s - 1) < page <= 2^s and f = floor(2^(31 + s) / page) + 1, which fits
+  // 32 bits; f page - 2^(31 + s) is at most page, so u times it stays below 2^(31 + s)
+  while ((1LL << a.page_shift) < a.page) ++a.page_shift;
+  a.page_factor = static_cast<unsigned>((1ULL << (31 + a.page_shift)) / a.page + 1);
   return a.k_scales ? launch<uint8_t>(a, own, p, po, s) : launch<bf16_t>(a, own, p, po, s);
 }
 

@@ -98,14 +98,14 @@ __device__ __forceinline__ f32x4_t mfma(u32x4_t a, u32x4_t b, f32x4_t c) {
 // 64 rows of DH bf16 in LDS, 64 bytes apart beyond their length, the 16-byte chunk c of each 64 bytes of row r at c ^
 // turn(r): what is read at once falls on different banks (16 rows at one chunk, 8 rows at 2 neighbouring chunks, 8 rows at
 // one and the 8 others at its neighbour), and the steps along a row are constant offsets. Lanes are c = lane % 16, g = lane / 16.
-template <int DH, int NT> struct Rows64 {
+template <int DH, int NT, bool ROOM> struct Rows64 {
   static constexpr unsigned kStride = 2 * DH + 64, kBytes = kC * kStride;
   static constexpr int kCPR = DH / 8, kN = kC * kCPR / NT;  // 16-byte chunks per row; per thread
   static constexpr int kRows = NT / kCPR;                   // rows that one of the threads' chunks covers
   // the chunks of rows `base` .. from memory, rows from `rows` on as zeros
-  // (here and in put the thread's terms are formed anew: kept through the walk, they take its registers)
+  // (without ROOM the thread's terms are formed anew here and in put: kept through the walk, they take its registers)
   __device__ __forceinline__ static void load(u32x4_t (&x)[kN], const bf16_t *base, unsigned row_bytes, int rows, int tid) {
-    asm volatile("" : "+v"(tid));
+    if constexpr (!ROOM) asm volatile("" : "+v"(tid));
     const auto src = __builtin_amdgcn_make_buffer_rsrc(
         const_cast<bf16_t *>(wave_uniform(base)), static_cast<short>(0),
         rows > 0 ? static_cast<int>(row_bytes * static_cast<unsigned>(min(rows, kC) - 1)) + DH * 2 : 0, kRawWord3);
@@ -121,7 +121,7 @@ template <int DH, int NT> struct Rows64 {
   // thread's chunk i is of row tid / kCPR + kRows i: its turn comes again after 16 rows
   static constexpr int kPar = kRows < 16 ? 16 / kRows : 1;
   __device__ __forceinline__ static void put(const u32x4_t (&x)[kN], unsigned lds, int tid) {
-    asm volatile("" : "+v"(tid));
+    if constexpr (!ROOM) asm volatile("" : "+v"(tid));
 #pragma unroll
     for (int i = 0; i < kN; ++i) {
       const int p = i % kPar;
@@ -131,7 +131,7 @@ template <int DH, int NT> struct Rows64 {
   }
   // put with the order of two accumulators' rows in each 32 values: chunk g has 4 g .. 4 g + 3 and 16 + 4 g .. 16 + 4 g + 3
   __device__ __forceinline__ static void put_paired(const u32x4_t (&x)[kN], unsigned lds, int tid) {
-    asm volatile("" : "+v"(tid));
+    if constexpr (!ROOM) asm volatile("" : "+v"(tid));
     const int r = tid / kCPR, c = tid % kCPR, to = (c & ~3) + 2 * (c & 1);
 #pragma unroll
     for (int i = 0; i < kN; ++i) {
@@ -327,17 +327,18 @@ template <int DK> __device__ __forceinline__ void load_state(f32x4_t (&S)[DK / 1
     for (int e = 0; e < 4; ++e) S[i][e] = at[static_cast<size_t>(16 * i + e) * dv];
 }
 
-// Threads of a workgroup, a wave for 16 values; waves a SIMD that the registers have to leave room for.
+// Threads of a workgroup, a wave for 16 values. Registers: ROOM for one workgroup a CU, which keeps its addresses, or
+// for two.
 constexpr int threads_of(int DVS) { return DVS * 4; }
-constexpr int waves_of(int DK, int DVS) { return (DK == 256 ? 1 : 2) * (DVS / 64); }
+constexpr int waves_of(int DVS, bool ROOM) { return (ROOM ? 1 : 2) * (DVS / 64); }
 
 // The state of the own tokens of a segment, or of a part of one, at its end (to the next one's a.seg), and its summed g (a.sums). Chunks from the
 // last one back: once what follows has decayed by 2^-150 in all, which is 0 in fp32, no earlier token counts.
 template <int DK, int DVS>
-__global__ __launch_bounds__(threads_of(DVS), waves_of(DK, DVS)) void linear_state(LinearArgs a) {
+__global__ __launch_bounds__(threads_of(DVS), waves_of(DVS, DK == 256)) void linear_state(LinearArgs a) {
   constexpr int NT = threads_of(DVS);
-  typedef Rows64<DK, NT> KB;
-  typedef Rows64<DVS, NT> VB;
+  typedef Rows64<DK, NT, true> KB;
+  typedef Rows64<DVS, NT, true> VB;
   __shared__ __attribute__((aligned(16))) unsigned char smem[KB::kBytes + VB::kBytes];
   __shared__ __attribute__((aligned(16))) float sw[DVS / 16][kC];  // each wave's own
   const int tid = threadIdx.x, lane = tid & 63, w = uni(tid >> 6), g = lane >> 4;
@@ -379,11 +380,11 @@ __global__ __launch_bounds__(threads_of(DVS), waves_of(DK, DVS)) void linear_sta
                   a.dv);
 }
 
-template <int DK, int DVS>
-__global__ __launch_bounds__(threads_of(DVS), waves_of(DK, DVS)) void linear_fwd(LinearArgs a) {
+template <int DK, int DVS, bool ROOM>
+__global__ __launch_bounds__(threads_of(DVS), waves_of(DVS, ROOM)) void linear_fwd(LinearArgs a) {
   constexpr int NW = DVS / 16, NT = threads_of(DVS);
-  typedef Rows64<DK, NT> KB;
-  typedef Rows64<DVS, NT> VB;
+  typedef Rows64<DK, NT, ROOM> KB;
+  typedef Rows64<DVS, NT, ROOM> VB;
   __shared__ __attribute__((aligned(16))) unsigned char smem[2 * KB::kBytes + VB::kBytes + 2 * kScores];
   // b, the number that forget, scale exp(b), exp(b_63 - b); exp(b_63)
   __shared__ __attribute__((aligned(16))) float mb[kC], me[kC], mw[kC];
@@ -448,7 +449,7 @@ __global__ __launch_bounds__(threads_of(DVS), waves_of(DK, DVS)) void linear_fwd
   constexpr bool kThrough = DK == DVS;
   auto store_rows = [&](int t0) {
     int x = tid;
-    asm volatile("" : "+v"(x));
+    if constexpr (!ROOM) asm volatile("" : "+v"(x));
 #pragma unroll
     for (int i = 0; i < VB::kN; ++i) {
       const int r = x / VB::kCPR + VB::kRows * i, row = t0 + r;
@@ -537,7 +538,7 @@ __global__ __launch_bounds__(threads_of(DVS), waves_of(DK, DVS)) void linear_fwd
       }
     if (odd) own_tokens<VB>(O, ldv, ldp, w, lane);
     int cr = c;
-    asm volatile("" : "+v"(cr));  // (addresses of rows formed here, as above)
+    if constexpr (!ROOM) asm volatile("" : "+v"(cr));  // (addresses of rows formed here, as above)
 #pragma unroll
     for (int j = 0; j < 4; ++j) {
       const int row = t + 16 * j + cr;
@@ -701,7 +702,16 @@ template <int DK, int DVS> hipError_t launch(LinearArgs a, hipStream_t s) {
   }
   a.run = a.segs;
   const long long g = rows * a.run;
-  linear_fwd<DK, DVS><<<dim3(grid_x(g), grid_rows(g)), threads_of(DVS), 0, s>>>(a);
+  // dk128 dv128: room for two workgroups a CU where there are more than 256 (384: 124 us, else 131; 512: 143 and 152; 256:
+  // 97 and 91.5). Smaller states leave it anyway, larger ones never.
+  const bool room = DK * DVS > 16384 || (DK * DVS == 16384 && (DK == 256 || g <= 256));
+  const dim3 grid(grid_x(g), grid_rows(g));
+  if constexpr (DK * DVS >= 16384)
+    if (room) {
+      linear_fwd<DK, DVS, true><<<grid, threads_of(DVS), 0, s>>>(a);
+      return hipGetLastError();
+    }
+  if constexpr (DK < 256) linear_fwd<DK, DVS, false><<<grid, threads_of(DVS), 0, s>>>(a);
   return hipGetLastError();
 }
 

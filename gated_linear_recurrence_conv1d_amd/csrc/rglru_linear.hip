@@ -23,11 +23,11 @@
 // before it: up to kFew states it forms the chain itself (at B8 T2048 H16 9.5 us of a launch less), else linear_carry has
 // done so in place.
 //
-// B8 T2048 H16 dk128 dv128: 24 us of states and 86; B1 T65536 H8 dk128 dv256: 30, 9 of the chain and 283 (607 MB in all,
-// 125 us at a copy's rate). A wave's chunk has 97 matrix instructions (59 without the lower terms) and 605 vector ones,
-// half of them the splitting into terms. With one workgroup on each CU matrix units are busy for 30% of the time, vector
-// units for 47%, LDS for 36%; two waves a SIMD hardly hide one behind the other, and the rest is waiting at the three
-// barriers. With two workgroups a CU the waits overlap, but the states of twice the segments cost as much.
+// B8 T2048 H16 dk128 dv128: 23 us of states and 82; B1 T65536 H8 dk128 dv256: 29, 9 of the chain and 267 (607 MB in all,
+// 125 us at a copy's rate). A wave's chunk has 97 matrix instructions (59 without the lower terms) and some 550 vector
+// ones, half of them the splitting into terms. With one workgroup on each CU matrix units are busy for 27% of the time (B1:
+// 33%), vector units for 38% (46%), LDS for 36%; two waves a SIMD hardly hide one behind the other, and the rest is waiting
+// at the three barriers. With two workgroups a CU the waits overlap, but the states of twice the segments cost as much.
 #include "rglru_attn.h"
 #include "rglru_grid.h"
 #include "rglru_launch.h"
@@ -596,7 +596,7 @@ __global__ __launch_bounds__(256) void linear_carry(LinearArgs a) {
 
 // One token: workgroup = (sequence, head, COLS of the values), the state read and written once. A row of the slice
 // is COLS / 4 lanes' 16 bytes; rows are dealt to the lane groups, whose shares of o meet in LDS. Bound by memory: 4096
-// states of dk128 dv256 in 210 us (1.07 GB, 5.1 TB/s: a plain copy's rate), 8 of dk128 dv128 in 3.7 us.
+// states of dk128 dv256 in 210 us (1.07 GB, 5.1 TB/s: a plain copy's rate), 8 of dk128 dv128 in 3.4 us.
 template <int COLS> __global__ __launch_bounds__(256) void linear_step(LinearStepArgs a) {
   constexpr int kLanes = COLS / 4, kGroups = 256 / kLanes, kFly = 8;
   __shared__ float qs[256], ks[256];

@@ -18,7 +18,7 @@
 // 0 * V is not 0 (a V that is infinite or NaN) the row is done again key by key.
 //
 // N256 Hq8 Hkv2 dh128 P32000 in e4m3, up to 400 own tokens: 72 us and 9.4 us of joining. Matrix units are busy for 30% of
-// the time (a third of it P's lower halves), vector units for nearly 50% (a quarter of it the exponentials), and with the
+// the time (a third of it P's lower halves), vector units for 45% (a quarter of it the exponentials), and with the
 // two or three waves that a SIMD's registers hold, the one hardly hides behind the other. The softmax of a block between
 // the matrix instructions of the one before, or of all three stages, gained nothing (79 us for then 77, and 188, spilled).
 // N64 Hq16 dh256 P1999 in bf16: 27 us and 6.7 us, most of it each chunk's latency and its O (17 MB).

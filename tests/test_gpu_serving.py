@@ -511,6 +511,16 @@ def test_linear_segments(T):
     assert torch.equal(o, o2) and torch.equal(s, mine)
 
 
+@pytest.mark.parametrize("B,H", [(32, 8), (33, 8)])  # a workgroup a CU, and more of them
+def test_linear_of_many_sequences(B, H):
+    rng = np.random.default_rng(B)
+    T, dk, dv = 70, 128, 128
+    q, k, v, g, s0 = linear_inputs(rng, B, T, 1, H, dk, dv, True, True)
+    lens = [(37 * b) % (T + 1) for b in range(B)]
+    o, s = rg.linear_attention(q, k, v, g, s0, ints(lens))
+    linear_check(o, s, q, k, v, g, s0, lens)
+
+
 def test_linear_decays_of_all_strengths():
     """No decay, decays that underflow within a chunk, and tokens that forget the state."""
     rng = np.random.default_rng(11)

@@ -442,10 +442,10 @@ rglru_status rglru_prefix_attention(const void *q, const void *k_pages, const vo
  * terms: the decayed scores and the state as two (about 16 bits), the decayed values that form the state as three (24
  * bits). A decay over several tokens of a chunk of 64 is taken from the difference of two of the chunk's running sums of
  * log decays (without those below -104, which are counted), and relatively off by up to 2^-23 times their size. Sums are
- * taken in a fixed order: results are bitwise reproducible. An infinite or NaN input reaches no row before
- * its own token, and the rows from there on until what it is in has decayed by 2^-150 (from then on it may or may not).
- * Outputs must not overlap the inputs (but for s_out = s0) or each other. Supported: dt = RGLRU_BF16, dk, dv in {64, 128,
- * 256}, H % Hk == 0, strides <= 2^20. */
+ * taken in a fixed order: results are bitwise reproducible. An infinite or NaN input reaches no row before its own token,
+ * and the rows from there on until what it is in has decayed by 2^-150 (from then on it may or may not). Outputs must not
+ * overlap the inputs (but for s_out = s0) or each other. Supported: dt = RGLRU_BF16, dk, dv in {64, 128, 256}, H % Hk ==
+ * 0, strides <= 2^20. */
 size_t rglru_linear_attention_workspace_size(int B, int T, int Hk, int H, int dk, int dv);
 rglru_status rglru_linear_attention(const void *q, const void *k, const void *v, const float *log_decay,
                                     const int *lens, const float *s0, void *o, float *s_out, int B, int T, int Hk,

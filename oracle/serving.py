@@ -71,7 +71,7 @@ def prefix_attention(q, k_pages, v_pages, prefix_table, prefix_len, table, lens,
 
 
 # ------------------------------------------------------------------------------------ linear attention
-LEAST = -104.0  # smaller log decays count as this
+LEAST = -104.0  # smaller log decays count as this (exp of it is below 2^-149)
 
 
 def linear_attention(q, k, v, log_decay, state=None, lens=None, scale=None):

@@ -141,10 +141,15 @@ template <typename T, typename C, int DH> hipError_t launch(const PagedArgs &a, 
   const int G = a.Hq / a.Hkv;
   const long long cols = static_cast<long long>(a.N) * p.splits;
   const dim3 grid(grid_x(cols), a.Hkv * ((G + 15) / 16), grid_rows(cols));
+  // Registers would let a third workgroup onto a CU at dh 128, but with few workgroups that gives some CUs more than their
+  // share: LDS for two then (Hq8 Hkv2, fp32, pages of 24: N300 146 us, else 188; N700 153 and 160; N3000 203 and 190. bf16,
+  // pages of 32: N300 63 and 72, N3000 105 and 97. e4m3 and dh 64 lose more than they win).
+  constexpr unsigned kThird = 21504;  // with the 33680 bytes of PagedLds, more than a third of 160 KB
+  const bool two = DH == 128 && sizeof(C) > 1 && cols * grid.y < 2048;
   if (a.page % 16 == 0)
-    paged_fwd<T, C, DH, true><<<grid, 64 * kPgWaves, 0, s>>>(a, p.chunk, p.splits);
+    paged_fwd<T, C, DH, true><<<grid, 64 * kPgWaves, two ? kThird : 0, s>>>(a, p.chunk, p.splits);
   else
-    paged_fwd<T, C, DH, false><<<grid, 64 * kPgWaves, 0, s>>>(a, p.chunk, p.splits);
+    paged_fwd<T, C, DH, false><<<grid, 64 * kPgWaves, two ? kThird : 0, s>>>(a, p.chunk, p.splits);
   const hipError_t e = hipGetLastError();
   if (e != hipSuccess || p.splits == 1) return e;
   // (rows are split only where they are few: N * Hq is at most 16 * 512, see paged_plan)

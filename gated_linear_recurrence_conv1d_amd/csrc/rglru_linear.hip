@@ -239,7 +239,7 @@ template <int DK, int DVS> struct Place {
     slice = r1 - h * nsl;
     len = clamp_len(a.lens, b, a.T);
     t_lo = seg * a.seg_len;
-    t_hi = min(a.T, t_lo + a.seg_len);
+    t_hi = t_lo + min(a.seg_len, a.T - t_lo);  // (t_lo + seg_len may pass 2^31)
     t_end = min(len, t_hi);
     tok = static_cast<size_t>(b) * a.T;
     head = static_cast<size_t>(b) * a.H + h;
@@ -673,7 +673,7 @@ LinearPlan linear_plan(int B, int T, int H, int dk, int dv) {
   const int in_state = (in_seg + sub - 1) / sub;
   p.sub = (in_seg + in_state - 1) / in_state;
   p.seg_len = p.sub * in_state * kC;
-  p.segs = (T + p.seg_len - 1) / p.seg_len;
+  p.segs = static_cast<int>((static_cast<long long>(T) + p.seg_len - 1) / p.seg_len);  // (T alone may be near 2^31)
   p.states = (p.segs - 1) * p.sub;
   return p;
 }

@@ -185,6 +185,16 @@ def test_linear_workspace():
     assert size(1, 0, 2, 4, 128, 64) == 0 and size(1, 8192, 3, 4, 128, 64) == 0
 
 
+@pytest.mark.parametrize("B,H", [(64, 16), (1, 256), (1, 1), (3, 1), (2, 8)])
+@pytest.mark.parametrize("T", [(1 << 30) + 1, 2_000_000_000, 0x7FFFFEFF])
+def test_linear_workspace_of_the_longest_prompts(B, H, T):
+    """Segments of more than 2^30 tokens: their number is that of half as many tokens, and a length behind the last one's
+    end passes 2^31."""
+    size = rg.rglru_linear_attention_workspace_size
+    assert size(B, T, 1, H, 64, 128) == size(B, 1 << 30, 1, H, 64, 128) < 1 << 32
+    assert size(B, 0x7FFFFF00, 1, H, 64, 128) == 0  # refused
+
+
 T_PTRS = ["q", "k", "v", "log_decay", "s_in", "s_out", "o"]
 TA = at(T_PTRS)
 

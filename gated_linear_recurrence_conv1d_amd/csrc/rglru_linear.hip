@@ -6,8 +6,9 @@
 //   o_t = scale (sum_{s <= t} exp(b_t - b_s) <q_t, k_s> v_s + exp(b_t) S^T q_t)
 //   S'  = exp(b_63) S + sum_s exp(b_63 - b_s) k_s v_s^T
 // All exponents are differences of one running sum taken before the exponential, so nothing is divided by a decay and
-// strong decays only underflow. Tokens that forget the state are counted beside that sum, not in it: the weights of the
-// tokens behind them stay as exact as their own decays are.
+// strong decays only underflow. The sum is held in 64 bits and each difference is rounded once, so that the weights of
+// tokens behind a strong decay are as exact as without it (in 32 bits, 48 decays of e^-103 in a chunk cost those behind
+// them 2^-13). Tokens that forget the state are counted beside the sum: their decays may be infinite.
 //
 // linear_fwd: a workgroup walks the chunks of one (sequence, head, slice of up to 128 values, segment); each wave
 // keeps S for 16 of the values (dk x 16 in accumulators). Per chunk, on 16x16x32 MFMAs:
@@ -43,17 +44,23 @@ namespace {
 constexpr int kC = 64;              // tokens per chunk
 constexpr int kFew = 4;             // states that are chained where they are needed
 constexpr float kLeast = -104.0f;   // exp of it is 0 in fp32: a smaller log decay (-inf) forgets the state
-constexpr float kGone = -150.0f;    // exp2 of it is 0 in fp32
+constexpr double kGone = -150.0;    // exp2 of it is 0 in fp32
+constexpr double kLog2E = 1.4426950408889634;
 
-// Inclusive running sum over the 64 lanes.
-__device__ __forceinline__ float wave_sum_up(float v) {
-  auto add = [](float x, int y) { return x + __int_as_float(y); };
-  v = add(v, __builtin_amdgcn_update_dpp(0, __float_as_int(v), 0x111, 0xF, 0xF, false));  // row_shr:1
-  v = add(v, __builtin_amdgcn_update_dpp(0, __float_as_int(v), 0x112, 0xF, 0xF, false));  // row_shr:2
-  v = add(v, __builtin_amdgcn_update_dpp(0, __float_as_int(v), 0x114, 0xF, 0xF, false));  // row_shr:4
-  v = add(v, __builtin_amdgcn_update_dpp(0, __float_as_int(v), 0x118, 0xF, 0xF, false));  // row_shr:8
-  v = add(v, __builtin_amdgcn_update_dpp(0, __float_as_int(v), 0x142, 0xA, 0xF, false));  // row_bcast:15
-  v = add(v, __builtin_amdgcn_update_dpp(0, __float_as_int(v), 0x143, 0xC, 0xF, false));  // row_bcast:31
+// Inclusive running sum over the 64 lanes, in 64 bits.
+template <int CTRL, int ROWS> __device__ __forceinline__ double plus_moved(double v) {
+  const uint2 x = __builtin_bit_cast(uint2, v);
+  const uint2 y = {static_cast<unsigned>(__builtin_amdgcn_update_dpp(0, static_cast<int>(x.x), CTRL, ROWS, 0xF, false)),
+                   static_cast<unsigned>(__builtin_amdgcn_update_dpp(0, static_cast<int>(x.y), CTRL, ROWS, 0xF, false))};
+  return v + __builtin_bit_cast(double, y);
+}
+__device__ __forceinline__ double wave_sum_up(double v) {
+  v = plus_moved<0x111, 0xF>(v);  // row_shr:1
+  v = plus_moved<0x112, 0xF>(v);  // row_shr:2
+  v = plus_moved<0x114, 0xF>(v);  // row_shr:4
+  v = plus_moved<0x118, 0xF>(v);  // row_shr:8
+  v = plus_moved<0x142, 0xA>(v);  // row_bcast:15
+  v = plus_moved<0x143, 0xC>(v);  // row_bcast:31
   return v;
 }
 
@@ -78,6 +85,7 @@ __device__ __forceinline__ u32x4_t rounded(const float (&x)[8]) {
 
 typedef __attribute__((address_space(3))) uint16_t lds_u16_t;
 typedef int i32x4_t __attribute__((ext_vector_type(4)));
+typedef double f64x4_t __attribute__((ext_vector_type(4), aligned(16)));
 
 // Whether any of 8 bf16 values is infinite or NaN: as integers without their sign, those are the largest.
 __device__ __forceinline__ bool not_finite(u32x4_t v) {
@@ -207,14 +215,18 @@ template <typename VB> __device__ __forceinline__ void own_tokens(f32x4_t (&O)[4
     }
 }
 
+// 2^b, b rounded once: relatively off by 2^-24 |b| ln 2 and the exponential's own 2^-23, however large the sums that b is
+// the difference of.
+__device__ __forceinline__ float decay_of(double b) { return __builtin_amdgcn_exp2f(static_cast<float>(b)); }
+
 // Of a chunk's tokens up to the lane's one, and of all: the summed log2 decays of those that do not forget the state, and
 // the number of those that do.
 struct Sums {
-  float b, b_end;
+  double b, b_end;
   int f, f_end;
   // what is left of the lane's token after the chunk, with 2^later to come; of the state before it
-  __device__ __forceinline__ float kept(float later) const { return f == f_end ? __builtin_amdgcn_exp2f(b_end - b + later) : 0.0f; }
-  __device__ __forceinline__ float before() const { return f == 0 ? __builtin_amdgcn_exp2f(b) : 0.0f; }
+  __device__ __forceinline__ float kept(double later) const { return f == f_end ? decay_of(b_end - b + later) : 0.0f; }
+  __device__ __forceinline__ float before() const { return f == 0 ? decay_of(b) : 0.0f; }
 };
 
 // This workgroup's (sequence, head, slice, segment), and where its tokens are.
@@ -259,9 +271,11 @@ template <int DK, int DVS> struct Place {
     const bool live = t + lane < t_end, forgets = live && x < kLeast;
     const unsigned long long all = __ballot(forgets);
     Sums r;
-    r.b = wave_sum_up(live && !forgets ? x * kLn2Inv : 0.0f);
+    r.b = wave_sum_up(live && !forgets ? x * kLog2E : 0.0);
     r.f = __builtin_amdgcn_mbcnt_hi(static_cast<unsigned>(all >> 32), __builtin_amdgcn_mbcnt_lo(static_cast<unsigned>(all), forgets));
-    r.b_end = __int_as_float(__builtin_amdgcn_readlane(__float_as_int(r.b), 63));
+    const uint2 last = __builtin_bit_cast(uint2, r.b);
+    r.b_end = __builtin_bit_cast(double, uint2{static_cast<unsigned>(__builtin_amdgcn_readlane(static_cast<int>(last.x), 63)),
+                                               static_cast<unsigned>(__builtin_amdgcn_readlane(static_cast<int>(last.y), 63))});
     r.f_end = __popcll(all);
     return r;
   }
@@ -349,7 +363,7 @@ __global__ __launch_bounds__(threads_of(DVS), waves_of(DVS, DK == 256)) void lin
   f32x4_t S[DK / 16];
 #pragma unroll
   for (int i = 0; i < DK / 16; ++i) S[i] = f32x4_t{};
-  float later = 0.0f;  // summed log2 decays of the chunks done
+  double later = 0.0;  // summed log2 decays of the chunks done
   u32x4_t kx[KB::kN], vx[VB::kN];
   float gx = 0.0f;
   auto load = [&](int t) {
@@ -375,7 +389,7 @@ __global__ __launch_bounds__(threads_of(DVS), waves_of(DVS, DK == 256)) void lin
     add_outer<DK, KB>(S, v, sw[w], ldk, kc, g);
     lds_barrier();  // everyone is done with the chunk
   }
-  if (tid == 0 && at.slice == 0) a.sums[at.head * a.states + at.seg] = later;
+  if (tid == 0 && at.slice == 0) a.sums[at.head * a.states + at.seg] = static_cast<float>(later);
   store_state<DK>(S, a.seg + (at.head * (a.states + 1) + at.seg + 1) * static_cast<size_t>(DK) * a.dv + at.slice * DVS + 16 * w,
                   a.dv);
 }
@@ -387,7 +401,8 @@ __global__ __launch_bounds__(threads_of(DVS), waves_of(DVS, ROOM)) void linear_f
   typedef Rows64<DVS, NT, ROOM> VB;
   __shared__ __attribute__((aligned(16))) unsigned char smem[2 * KB::kBytes + VB::kBytes + 2 * kScores];
   // b, the number that forget, scale exp(b), exp(b_63 - b); exp(b_63)
-  __shared__ __attribute__((aligned(16))) float mb[kC], me[kC], mw[kC];
+  __shared__ __attribute__((aligned(16))) double mb[kC];
+  __shared__ __attribute__((aligned(16))) float me[kC], mw[kC];
   __shared__ __attribute__((aligned(16))) int mf[kC];
   __shared__ float mkeep;
   const int tid = threadIdx.x, lane = tid & 63, w = uni(tid >> 6);
@@ -468,7 +483,7 @@ __global__ __launch_bounds__(threads_of(DVS), waves_of(DVS, ROOM)) void linear_f
       mb[lane] = sums.b;
       mf[lane] = sums.f;
       me[lane] = sums.before() * a.scale;
-      mw[lane] = sums.kept(0.0f);
+      mw[lane] = sums.kept(0.0);
       if (lane == 63) mkeep = sums.before();
     }
     lds_barrier();
@@ -500,14 +515,14 @@ __global__ __launch_bounds__(threads_of(DVS), waves_of(DVS, ROOM)) void linear_f
       const unsigned k0 = ldk + 16 * i * KB::kStride, q0 = qr + 16 * j * KB::kStride;
 #pragma unroll
       for (int d = 0; d < DK / 32; ++d) p = mfma(KB::pairs(k0, kr, d), KB::rows(0, q0, d), p);
-      const float btt = mb[16 * j + c];
+      const double btt = mb[16 * j + c];
       const int ftt = mf[16 * j + c];
-      const f32x4_t bs = *reinterpret_cast<const f32x4_t *>(&mb[16 * i + 4 * g]);
+      const f64x4_t bs = *reinterpret_cast<const f64x4_t *>(&mb[16 * i + 4 * g]);
       const i32x4_t fs = *reinterpret_cast<const i32x4_t *>(&mf[16 * i + 4 * g]);
       float x[4];
 #pragma unroll
       for (int e = 0; e < 4; ++e) {
-        const float f = p[e] * a.scale * __builtin_amdgcn_exp2f(btt - bs[e]);
+        const float f = p[e] * a.scale * decay_of(btt - bs[e]);
         x[e] = (i < j || 4 * g + e <= c) && fs[e] == ftt ? f : 0.0f;
       }
       const u32x2_t hi = {pack_bf16x2(x[0], x[1]), pack_bf16x2(x[2], x[3])};

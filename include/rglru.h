@@ -438,10 +438,11 @@ rglru_status rglru_prefix_attention(const void *q, const void *k_pages, const vo
  *  o [B][T][H][dv] bf16, contiguous, out
  *  scale > 0, or 0 for 1/sqrt(dk)
  *  workspace  at least rglru_linear_attention_workspace_size() bytes (NULL if that is 0)
- * The state, all sums and all decays are fp32. Operands of the contractions that are not inputs enter as sums of bf16
+ * The state, all decays and all sums but those of log decays are fp32. Operands of the contractions that are not inputs enter as sums of bf16
  * terms: the decayed scores and the state as two (about 16 bits), the decayed values that form the state as three (24
- * bits). A decay over several tokens of a chunk of 64 is taken from the difference of two of the chunk's running sums of
- * log decays (without those below -104, which are counted), and relatively off by up to 2^-23 times their size. Sums are
+ * bits). Log decays are summed in 64 bits within a chunk of 64 tokens (those below -104 are counted instead), and a sum
+ * of them is rounded to fp32 once, before its exponential: a decay exp(-x) is relatively off by at most 2^-24 (x + 2),
+ * however strong the decays before it are; over several chunks it is the product of theirs. Sums are
  * taken in a fixed order: results are bitwise reproducible. An infinite or NaN input reaches no row before its own token,
  * and the rows from there on until what it is in has decayed by 2^-150 (from then on it may or may not). Outputs must not
  * overlap the inputs (but for s_out = s0) or each other. Supported: dt = RGLRU_BF16, dk, dv in {64, 128, 256}, H % Hk ==

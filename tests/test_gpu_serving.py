@@ -560,6 +560,60 @@ def test_linear_forgetting_is_exact(T):
     check(o, ro, ((es + (dk + 64) * W24 + 2.0 ** -16) * ao + U * np.abs(ro)) * (1 + U), "o")
 
 
+# What follows holds a decay to its own size, however strong the ones before it are: a weight exp(-x) is 2^b with b = -x
+# log2 e from sums in 64 bits, rounded once to fp32 (|b| 2^-24, that is x w of the weight), and an exponential off by 2 w.
+# A state is rescaled once a chunk (w more): over c chunks (x + 3 c) w in all, x <= 104 (else the weight is 0, or below
+# 2^-149).
+def decay_error(T):
+    return (104 + 3 * (T // 64 + 2)) * W24
+
+
+STRONG = {"isolated": (-20.0, 9), "-60": (-60.0, 8), "-103": (-103.0, 30), "resets": (-103.9, 2), "none": (0.0, 1 << 20)}
+
+
+def strong_decays(rng, B, T, H, kind):
+    """Weak decays, and among them strong ones just above those that forget the state: one in so many tokens, and runs of
+    48 of them before weak ones."""
+    value, every = STRONG[kind]
+    g = -0.02 * np.abs(rng.standard_normal((B, T, H)))
+    g[rng.random((B, T, H)) < 1.0 / every] = value
+    if kind == "resets":
+        g[:, (np.arange(T) % 64) >= 48] = -0.01
+    return torch.from_numpy(g.astype(np.float32)).to(DEV)
+
+
+@pytest.mark.parametrize("kind", list(STRONG))
+@pytest.mark.parametrize("B,T,H,dk,dv", [(1, 64, 2, 64, 64), (2, 256, 4, 256, 64), (1, 250, 2, 256, 256), (40, 128, 8, 128, 128)])
+def test_linear_weights_of_single_tokens(B, T, H, dk, dv, kind):
+    """Token t's key is the unit vector t: row t of the state is then v_t times the token's weight alone, off by the
+    weight's own error, the product's and the three terms' (4 w with the exact values' conversion)."""
+    rng = np.random.default_rng(T + dk)
+    assert T <= dk
+    q, _, v, _, _ = linear_inputs(rng, B, T, 1, H, dk, dv, True, False)
+    k = torch.eye(T, dk, device=DEV, dtype=BF).view(1, T, 1, dk).expand(B, T, 1, dk).contiguous()
+    g = strong_decays(rng, B, T, H, kind)
+    o, s = rg.linear_attention(q, k, v, g)
+    x = num(g)[:, ::-1].cumsum(1)[:, ::-1] - num(g)  # what follows each token
+    w = np.exp(x)[..., None] * num(v)  # [B, T, H, dv]
+    rel = (-x[..., None] + 3 * (T // 64 + 2) + 4) * W24
+    check(s[:, :, :T], w.transpose(0, 2, 1, 3), (rel * np.abs(w)).transpose(0, 2, 1, 3), "state")
+    assert not s[:, :, T:].any()
+
+
+@pytest.mark.parametrize("kind", list(STRONG))
+@pytest.mark.parametrize("T,dk,dv", [(64, 64, 64), (333, 128, 128), (1100, 64, 128), (700, 256, 64)])
+def test_linear_strong_decays_among_weak(T, dk, dv, kind):
+    rng = np.random.default_rng(T + dv)
+    B, H = 2, 2
+    q, k, v, _, s0 = linear_inputs(rng, B, T, 1, H, dk, dv, True, True)
+    g = strong_decays(rng, B, T, H, kind)
+    o, s = rg.linear_attention(q, k, v, g, s0)
+    ro, rs, ao, as_ = sv.linear_attention(num(q), num(k), num(v), num(g), num(s0))
+    es = (2 * T + 200) * W24 + decay_error(T)
+    check(s, rs, es * as_, "state")
+    check(o, ro, ((es + (dk + 64) * W24 + 2.0 ** -16) * ao + U * np.abs(ro)) * (1 + U), "o")
+
+
 @pytest.mark.parametrize("bad", [float("nan"), float("inf")])
 @pytest.mark.parametrize("dk,dv", [(64, 64), (128, 256), (256, 128)])
 def test_linear_bad_inputs_reach_later_rows_only(bad, dk, dv):

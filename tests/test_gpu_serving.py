@@ -324,6 +324,38 @@ def test_prefix_attention(kind, P, lens, Hq, Hkv, dh, page, W, S, scale):
     assert torch.equal(got, run_prefix(q, cache, pt, P, table, lens, W, S, scale or 0.0))  # sums in a fixed order
 
 
+@pytest.mark.parametrize("bad", [False, True])
+@pytest.mark.parametrize("kind,dh,page", [("bf16", 64, 16), ("e4m3", 64, 12), ("bf16", 256, 12), ("e4m3", 256, 16), ("e4m3", 128, 64)])
+def test_prefix_of_long_chunks(kind, dh, page, bad):
+    """Chunks of 30 blocks of the prefix, the first one with sinks, a gap that no row sees and the rows' windows; bad: what
+    nobody sees there is NaN, and a v that some rows see makes the others' go key by key. A lane of a chunk sums 16 values
+    of each of 30 blocks, and 32 chunks and two halves are joined: so many operations behind one another."""
+    rng = np.random.default_rng(dh)
+    P, N, Hq, S, W = 30000, 256, 8, 70, 30000 - 400  # a row with n tokens of its own sees from 400 + n on
+    lens = rng.integers(0, 201, N)
+    lens[:6] = [0, 5, 10, 11, 200, 97]
+    q, cache, pools, pt, table = prefix_inputs(rng, kind, P, lens, Hq, 1, dh, page)
+    q = q * 2
+    some = np.array([0, 1, 2, 3, 4, 5, 100, 255])
+    o, mag, most = sv.prefix_attention(num(q)[some], *pools, pt, P, table[some], lens[some], W, S)
+    depth = 16 * 30 + 32 + 64
+    if bad:
+        for t, which in ((200, (0, 1)), (410, (1,))):  # in the gap; before the windows of more than 10 own tokens
+            for i in which:
+                if kind == "e4m3":
+                    cache[2 + i].view(torch.uint8)[int(pt[t // page]), t % page, 0] = 255
+                else:
+                    cache[i][int(pt[t // page]), t % page, 0, 3] = float("nan")
+    got = run_prefix(q, cache, pt, P, table, lens, W, S)
+    assert torch.equal(got.nan_to_num(7.0), run_prefix(q, cache, pt, P, table, lens, W, S).nan_to_num(7.0))
+    x, sees = num(got)[some], lens[some] <= 10
+    if bad:
+        assert np.isnan(x[sees][..., 3]).all() and np.isnan(num(got)[lens <= 10][..., 3]).all()
+        assert np.isfinite(num(got)[lens > 10]).all()
+        x, o, mag, most = (y[~sees] for y in (x, o, mag, most))
+    check(x, o, attention_bound(o, mag, most, dh, depth), "o")
+
+
 def test_prefix_scores_far_apart():
     """A prefix whose scores lie far above or below the own tokens' ones, and rising through it."""
     rng = np.random.default_rng(4)
@@ -519,6 +551,27 @@ def test_linear_of_many_sequences(B, H):
     lens = [(37 * b) % (T + 1) for b in range(B)]
     o, s = rg.linear_attention(q, k, v, g, s0, ints(lens))
     linear_check(o, s, q, k, v, g, s0, lens)
+
+
+@pytest.mark.parametrize("B,T,H,dk,dv", [(8, 1100, 64, 64, 64), (1, 16390, 64, 64, 64), (2, 5000, 32, 128, 128),
+                                         (1, 9000, 32, 256, 128), (40, 1300, 8, 128, 128)])
+def test_linear_of_many_chunks(B, T, H, dk, dv):
+    """18 chunks and more one after another in a workgroup, forming states (but in the first and the last case) and o, with
+    decays that let a token, some chunks, or everything through. Against the oracle for some sequences and heads."""
+    rng = np.random.default_rng(T)
+    q, k, v, g, s0 = linear_inputs(rng, B, T, 1, H, dk, dv, True, True)
+    g *= torch.tensor([1e-4, 1e-2, 0.1, 0.4, 3.0] * H, device=DEV)[:H]
+    lens = [T - 70 * (b % 3) for b in range(B)]
+    o, s = rg.linear_attention(q, k, v, g, s0, ints(lens))
+    assert torch.equal(o, rg.linear_attention(q, k, v, g, s0, ints(lens))[0])
+    for b in {0, B - 1}:
+        h = [0, 1, 2, 3, 4, H - 1]
+        part = q[b:b + 1], k[b:b + 1], v[b:b + 1, :, h], g[b:b + 1, :, h], s0[b:b + 1, h]
+        n = lens[b]
+        ro, rs, ao, as_ = sv.linear_attention(*(num(x) for x in part), [n])
+        es = (2 * n + 200) * W24 + decay_error(n)
+        check(s[b:b + 1, h], rs, es * as_, "state")
+        check(o[b:b + 1][:, :, h], ro, ((es + (dk + 64) * W24 + 2.0 ** -16) * ao + U * np.abs(ro)) * (1 + U), "o")
 
 
 def test_linear_decays_of_all_strengths():

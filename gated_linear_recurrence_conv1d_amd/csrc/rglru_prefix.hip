@@ -28,6 +28,7 @@
 #include "rglru_paged.h"
 
 #include <algorithm>
+#include <cmath>
 
 namespace rglru {
 
@@ -545,14 +546,18 @@ __global__ __launch_bounds__(256) void prefix_join(PrefixArgs a, PagedArgs own, 
   }
 }
 
-// Blocks per chunk of the prefix, and the most chunks it can have. At least 4 blocks, as each chunk leaves an O of all
-// rows to write and read again (N64 Hq16 dh256 P1999: 33.2 us, with 2 blocks 37.4, with 8 34.1); 2 where the rows are few
-// and a chunk's length is the time (N6 Hq10 dh256 P700: 13.2 us, with 4 15.7).
+// Blocks per chunk of the prefix, and the most chunks it can have. A chunk's length is time in which other CUs wait, and
+// each chunk leaves an O of all rows to write and read again: short chunks suit few blocks and few row tiles, and the best
+// length grows as the root of both (us at dh 256 in bf16, Hq16 Hkv1, with chunks of 1, 2, 4 and 8 blocks; other types and dh
+// turn at the same places: 10 blocks of 1 tile 13.4 14.7 16.9 22.8, of 8 tiles 19.4 17.5 19.0 24.8; 63 of 1 tile 18.5 17.2
+// 18.0 23.2, of 4 27.3 22.4 21.9 25.0; 250 of 1 tile 34.3 26.8 23.0 25.8, of 6 41.7 41.7 34.7 29.7). From 512 workgroups on,
+// two a CU, chunks grow with the blocks.
 PagedPlan prefix_plan(int N, int Hq, int Hkv, long long cap) {
   const long long tiles = (static_cast<long long>(N) * (Hq / Hkv) + kOwn - 1) / kOwn * Hkv;
-  const long long blocks = (cap + kBlk - 1) / kBlk;
+  const long long blocks = (cap + kBlk - 1) / kBlk, all = blocks * tiles;
   constexpr long long kTarget = 512;  // workgroups: two fit a CU at a time
-  const long long chunk = std::max<long long>((blocks * tiles + kTarget - 1) / kTarget, tiles > 2 ? 4 : 2);
+  const long long root = std::llround(std::sqrt(static_cast<double>(all)) / 5);
+  const long long chunk = std::max((all + kTarget - 1) / kTarget, std::min<long long>(std::max<long long>(root, 1), 8));
   PagedPlan p;
   p.chunk = static_cast<int>(std::min<long long>(chunk, 1 << 28));
   p.splits = static_cast<int>(std::max<long long>((blocks + p.chunk - 1) / p.chunk, 1));

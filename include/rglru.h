@@ -373,8 +373,9 @@ rglru_status rglru_cache_quantize(const void *k, const void *v, const long long 
                                   long long v_stride, long long n_slots, rglru_dtype dt, void *stream);
 
 /* The way back: row t of sequence b becomes token starts[b] + t (code * scale, exact; under scales below 2^-117, which
- * are not written above, values below 2^-126 may come as 0), for the prompt's attention over what an earlier chunk has
- * left in the cache.
+ * are not written above, values below 2^-126 may come as 0): what an earlier chunk of a prompt has left in the cache, for
+ * attention of the next one. (rglru_local_attention has a query for every key: rows of q before the chunk may hold any finite
+ * values, and their outputs are thrown away.)
  *  k_pages .. v_scales [num_pages][page_size][Hkv][dh] and [num_pages][page_size][Hkv], as above
  *  block_table [B][max_pages] int32, lens [B] int32: the tokens that a sequence has; starts [B] int32 or NULL (all 0)
  *  k_out, v_out [B][T][Hkv][dh] dtype (f32 or bf16), out, *_stride elements from row to row (a sequence's rows are
@@ -389,7 +390,9 @@ rglru_status rglru_cache_dequantize(const void *k_pages, const void *v_pages, co
                                     rglru_dtype dt, void *stream);
 
 /* rglru_paged_attention over that cache: k_pages, v_pages in e4m3 with k_scales, v_scales [num_pages][page_size][Hkv]
- * in e8m0; q and o bf16. Everything else is the same; the cached values enter both contractions exactly. */
+ * in e8m0; q and o bf16. Everything else is the same; the cached values enter both contractions exactly. (v's scale is a
+ * factor of the probability, so rows of v below 2^-100 in magnitude lose digits where that product is no longer a normal
+ * bf16 number.) */
 size_t rglru_paged_attention_e4m3_workspace_size(int N, int Hq, int Hkv, int dh, int page_size, int max_pages,
                                                  int window, int sinks);
 rglru_status rglru_paged_attention_e4m3(const void *q, const void *k_pages, const void *v_pages, const void *k_scales,
@@ -438,15 +441,15 @@ rglru_status rglru_prefix_attention(const void *q, const void *k_pages, const vo
  *  o [B][T][H][dv] bf16, contiguous, out
  *  scale > 0, or 0 for 1/sqrt(dk)
  *  workspace  at least rglru_linear_attention_workspace_size() bytes (NULL if that is 0)
- * The state, all decays and all sums but those of log decays are fp32. Operands of the contractions that are not inputs enter as sums of bf16
- * terms: the decayed scores and the state as two (about 16 bits), the decayed values that form the state as three (24
- * bits). Log decays are summed in 64 bits within a chunk of 64 tokens (those below -104 are counted instead), and a sum
- * of them is rounded to fp32 once, before its exponential: a decay exp(-x) is relatively off by at most 2^-24 (x + 2),
- * however strong the decays before it are; over several chunks it is the product of theirs. Sums are
- * taken in a fixed order: results are bitwise reproducible. An infinite or NaN input reaches no row before its own token,
- * and the rows from there on until what it is in has decayed by 2^-150 (from then on it may or may not). Outputs must not
- * overlap the inputs (but for s_out = s0) or each other. Supported: dt = RGLRU_BF16, dk, dv in {64, 128, 256}, H % Hk ==
- * 0, strides <= 2^20. */
+ * The state, all decays and all sums but those of log decays are fp32. Operands of the contractions that are not
+ * inputs enter as sums of bf16 terms: the decayed scores and the state as two (about 16 bits), the decayed values that
+ * form the state as three (24 bits, while they are above 2^-100). Log decays are summed in 64 bits within a chunk of
+ * 64 tokens (those below -104 are counted instead), and a sum of them is rounded to fp32 once, before its exponential:
+ * a decay exp(-x) is relatively off by at most 2^-24 (x + 2), however strong the decays before it are; over several
+ * chunks it is the product of theirs. Sums are taken in a fixed order: results are bitwise reproducible. An infinite
+ * or NaN input reaches no row before its own token, and the rows from there on until what it is in has decayed by
+ * 2^-150 (from then on it may or may not). Outputs must not overlap the inputs (but for s_out = s0) or each other.
+ * Supported: dt = RGLRU_BF16, dk, dv in {64, 128, 256}, H % Hk == 0, strides <= 2^20. */
 size_t rglru_linear_attention_workspace_size(int B, int T, int Hk, int H, int dk, int dv);
 rglru_status rglru_linear_attention(const void *q, const void *k, const void *v, const float *log_decay,
                                     const int *lens, const float *s0, void *o, float *s_out, int B, int T, int Hk,

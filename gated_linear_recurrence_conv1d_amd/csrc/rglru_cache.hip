@@ -7,8 +7,8 @@
 // on the bf16 side, 8-byte ones on the codes' side, both runs without holes over the heads of a row. The 8 .. 32 lanes
 // of a head find its largest magnitude by lane exchanges; as integers, so that a NaN wins.
 //
-// 16384 fp32 rows of Hkv2 dh128: written in 8.4 us (42 MB, 5.0 TB/s), 65000 read back in 30 us (166 MB, 5.5 TB/s: a plain
-// copy's rate); 8 times 2048 bf16 rows of dh256 read back in 6.6 us (25 MB).
+// 16384 fp32 rows of Hkv2 dh128: written in 8.4 us (42 MB, 5.0 TB/s), 65000 read back in 30 us (166 MB, 5.5 TB/s; a
+// plain copy of 256 MB reaches 5.4); 8 times 2048 bf16 rows of dh256 read back in 6.5 us (25 MB).
 #include "rglru_e4m3.h"
 #include "rglru_grid.h"
 #include "rglru_launch.h"

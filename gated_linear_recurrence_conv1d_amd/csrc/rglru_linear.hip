@@ -24,11 +24,13 @@
 // before it: up to kFew states it forms the chain itself (at B8 T2048 H16 9.5 us of a launch less), else linear_carry has
 // done so in place.
 //
-// B8 T2048 H16 dk128 dv128: 23 us of states and 82; B1 T65536 H8 dk128 dv256: 29, 9 of the chain and 267 (607 MB in all,
-// 125 us at a copy's rate). A wave's chunk has 97 matrix instructions (59 without the lower terms) and some 550 vector
-// ones, half of them the splitting into terms. With one workgroup on each CU matrix units are busy for 27% of the time (B1:
-// 33%), vector units for 38% (46%), LDS for 36%; two waves a SIMD hardly hide one behind the other, and the rest is waiting
-// at the three barriers. With two workgroups a CU the waits overlap, but the states of twice the segments cost as much.
+// Timed one call after another, all kernels: B8 T2048 H16 dk128 dv128 95 us, B1 T65536 H8 dk128 dv256 301 (607 MB, 110
+// us at the 5.5 TB/s that reading a cache back reaches). In a trace, at lower clocks, B8 has 24 us of states and 87 of
+// linear_fwd, B1 30, 9 of the chain and 351. A wave's chunk has 97 matrix instructions (59 without the lower terms) and
+// some 530 vector ones (650 where two workgroups share a CU), 200 of them the splitting into terms. With one workgroup
+// on each CU matrix units are busy for 27% of the time (B1: 33%), vector units for 39% (46%), LDS for 36%; two waves a
+// SIMD hardly hide one behind the other, and the rest is waiting at the three barriers. With two workgroups a CU the
+// waits overlap, but the states of twice the segments cost as much.
 #include "rglru_attn.h"
 #include "rglru_grid.h"
 #include "rglru_launch.h"
@@ -611,7 +613,7 @@ __global__ __launch_bounds__(256) void linear_carry(LinearArgs a) {
 
 // One token: workgroup = (sequence, head, COLS of the values), the state read and written once. A row of the slice
 // is COLS / 4 lanes' 16 bytes; rows are dealt to the lane groups, whose shares of o meet in LDS. Bound by memory: 4096
-// states of dk128 dv256 in 210 us (1.07 GB, 5.1 TB/s: a plain copy's rate), 8 of dk128 dv128 in 3.4 us.
+// states of dk128 dv256 in 210 us (1.07 GB, 5.1 TB/s; a plain copy of 1 GiB 5.2), 8 of dk128 dv128 in 3.4 us.
 template <int COLS> __global__ __launch_bounds__(256) void linear_step(LinearStepArgs a) {
   constexpr int kLanes = COLS / 4, kGroups = 256 / kLanes, kFly = 8;
   __shared__ float qs[256], ks[256];
@@ -667,9 +669,9 @@ template <int COLS> __global__ __launch_bounds__(256) void linear_step(LinearSte
 }
 
 // Segments of a prompt: 256 workgroups, one a CU, where a workgroup's state has 16384 values or more (more segments are
-// more states to form: B1 T32768 H16 dk256 dv256 503 us, with 512 workgroups 559; B8 T2048 H16 dk128 dv128 98 and 102),
-// else 512 (B6 T4096 H16 dk64 dv128 103 us, with 256 118); 320 leave some CUs twice the others' work (744, 99, 123). Of
-// two chunks at least (B1 T2048 H8 dk128 dv128 31 us, with four 38.6, with one 35; T128 12, with one 15.8).
+// more states to form: B1 T32768 H16 dk256 dv256 492 us, with 512 workgroups 550; B8 T2048 H16 dk128 dv128 95 and 107), else
+// 512 (B6 T4096 H16 dk64 dv128 109 us, with 256 128); 320 leave some CUs twice the others' work (728, 95, 140). Of two chunks
+// at least (B1 T2048 H8 dk128 dv128 30 us, with four 36, with one 34.5; T128 11.5, with one 15).
 LinearPlan linear_plan(int B, int T, int H, int dk, int dv) {
   const int dvs = dv == 64 ? 64 : 128;
   const long long groups = static_cast<long long>(B) * H * (dv / dvs);
@@ -680,8 +682,8 @@ LinearPlan linear_plan(int B, int T, int H, int dk, int dv) {
   const int in_seg = static_cast<int>((chunks + segs - 1) / segs);
   LinearPlan p;
   // the states of few segments in parts, where forming them leaves CUs idle and the chain of them stays short (B8 T2048
-  // H16 dk128 dv128, decays of heads: 101 us, whole 107; B16 T1024 H8 dk256 dv128 88 and 91; but B1 T2048 H8 dk128 dv128
-  // with 30 states 37, with 15 31)
+  // H16 dk128 dv128: 95 us, whole 103; B16 T1024 H8 dk256 dv128 88 and 91; but B1 T2048 H8 dk128 dv128 with 30 states 37,
+  // with 15 30)
   const long long before = std::max((chunks + in_seg - 1) / in_seg - 1, 1);
   const int sub = static_cast<int>(std::max<long long>(
       std::min<long long>({target / (before * groups), kFew / before, in_seg}), 1));
@@ -717,8 +719,8 @@ template <int DK, int DVS> hipError_t launch(LinearArgs a, hipStream_t s) {
   }
   a.run = a.segs;
   const long long g = rows * a.run;
-  // dk128 dv128: room for two workgroups a CU where there are more than 256 (384: 124 us, else 131; 512: 143 and 152; 256:
-  // 97 and 91.5). Smaller states leave it anyway, larger ones never.
+  // dk128 dv128: room for two workgroups a CU where there are more than 256 (B24 T2048 H16, 384: 245 us, with
+  // room for one 267; B32 T1024, 512: 148 and 158; but B8 T2048, 256: 101 and 95). Smaller states leave it anyway, larger ones never.
   const bool room = DK * DVS > 16384 || (DK * DVS == 16384 && (DK == 256 || g <= 256));
   const dim3 grid(grid_x(g), grid_rows(g));
   if constexpr (DK * DVS >= 16384)

@@ -27,13 +27,13 @@
 // A cache in e4m3 (rglru_e4m3.h) takes the same way: 16 bytes are then 16 values, converted to bf16 right before
 // their use. A K row's scale is an operand of that conversion; V's goes into P, in fp32. Pairs of keys of one value
 // are neighbouring bytes after one permute of two rows' words, and the conversion takes pairs: 2 permutes and 4
-// conversions for 8 values of a pair of rows. N128 Hq16 dh256 W2048: 113 MB in 26 us and 4.8 us of joining (bf16 50 and
+// conversions for 8 values of a pair of rows. N128 Hq16 dh256 W2048: 113 MB in 26 us and 4.7 us of joining (bf16 48 and
 // 5): 4.3 TB/s, as a tile has half the bytes of a bf16 one behind the same two dependent loads, of its page and of its rows.
 // The part of attention behind a shared prefix that each sequence has for itself (rglru_prefix.hip) is the same work:
 // every chunk is then left as O, m and l for the join there.
 //
-// N4 Hq8 Hkv2 dh128 to 131k tokens: 401 MB in 77.6 us (5.2 TB/s, a plain copy's rate); N128 Hq16 dh256 W2048:
-// 224 MB in 50 us and 5 us of joining, in fp32 449 MB in 97 and 5.
+// N4 Hq8 Hkv2 dh128 to 131k tokens: 401 MB in 77.9 us (5.2 TB/s; a plain copy of 1 GiB 5.2); N128 Hq16 dh256
+// W2048: 224 MB in 48 us and 5 us of joining, in fp32 449 MB in 94 and 5.
 #include "rglru_grid.h"
 #include "rglru_paged.h"
 

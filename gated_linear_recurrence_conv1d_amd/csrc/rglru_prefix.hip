@@ -17,11 +17,13 @@
 // A window may have left a part of the prefix for some rows and not for others: masked entries get P = 0, and where
 // 0 * V is not 0 (a V that is infinite or NaN) the row is done again key by key.
 //
-// N256 Hq8 Hkv2 dh128 P32000 in e4m3, up to 400 own tokens: 72 us and 9.4 us of joining. Matrix units are busy for 30% of
-// the time (a third of it P's lower halves), vector units for 45% (a quarter of it the exponentials), and with the
-// two or three waves that a SIMD's registers hold, the one hardly hides behind the other. The softmax of a block between
-// the matrix instructions of the one before, or of all three stages, gained nothing (79 us for then 77, and 188, spilled).
-// N64 Hq16 dh256 P1999 in bf16: 27 us and 6.7 us, most of it each chunk's latency and its O (17 MB).
+// N256 Hq8 Hkv2 dh128 P32000 in e4m3, up to 400 own tokens: in a trace 71 us and 9.4 of joining, 73 in all timed among other
+// passes. Matrix units are busy for 31% of the time (a third of it P's lower halves), vector units for 46% (a quarter of it the
+// exponentials), and with the two or three waves that a SIMD's registers hold, the one hardly hides behind the other. The
+// softmax of a block between the matrix instructions of the one before, or of all three stages, gained nothing (79 us for then
+// 77, and 188, spilled).
+// N64 Hq16 dh256 P1999 in bf16: 26 us and 6.4, most of it each chunk's latency and its O (17 MB); in e4m3 27 and 6.6, with 19
+// registers spilled, 10 of which are read back in each block.
 #include "rglru_attn.h"
 #include "rglru_e4m3.h"
 #include "rglru_grid.h"

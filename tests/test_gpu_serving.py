@@ -356,6 +356,19 @@ def test_prefix_of_long_chunks(kind, dh, page, bad):
     check(x, o, attention_bound(o, mag, most, dh, depth), "o")
 
 
+@pytest.mark.parametrize("kind", ["bf16", "e4m3"])
+@pytest.mark.parametrize("P", [31, 700, 2000, 7000, 13000, 20000, 30000, 45000, 52000])  # 1 to 8 blocks a chunk
+def test_prefix_of_all_chunk_lengths(kind, P):
+    """A lane sums 16 values of each of up to 8 blocks; up to 245 chunks are joined, in four waves."""
+    rng = np.random.default_rng(P)
+    lens, Hq, dh, page, S, W = [7, 0, 90], 3, 64, 48, 40, P - P // 3
+    q, cache, pools, pt, table = prefix_inputs(rng, kind, P, lens, Hq, 1, dh, page)
+    q = q * 2
+    got = run_prefix(q, cache, pt, P, table, lens, W, S)
+    o, mag, most = sv.prefix_attention(num(q), *pools, pt, P, table, lens, W, S)
+    check(got, o, attention_bound(o, mag, most, dh, 16 * 8 + 245 // 4 + 64), "o")
+
+
 def test_prefix_scores_far_apart():
     """A prefix whose scores lie far above or below the own tokens' ones, and rising through it."""
     rng = np.random.default_rng(4)

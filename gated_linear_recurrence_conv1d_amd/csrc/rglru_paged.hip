@@ -142,10 +142,10 @@ template <typename T, typename C, int DH> hipError_t launch(const PagedArgs &a, 
   const dim3 grid(grid_x(cols), a.Hkv * ((G + 15) / 16), grid_rows(cols));
   // Registers would let a third workgroup onto a CU at dh 128. That hides the latency of short walks, but on longer ones
   // three share what two can use, and of few workgroups some CUs get more than their share: LDS for two then. Hq8 Hkv2,
-  // lengths spread to L, us with two and three: bf16, pages of 32: 11 tiles a workgroup N300 L300 14.7 and 14.2, N2000 69.3
-  // and 62.8; 19 tiles N300 L600 21.2 and 22.1, N1000 59.8 and 58.1; 25 tiles N600 L800 43.3 and 44.6; 74 tiles N300 L4000
+  // lengths spread to L, us with two and three: bf16, pages of 32: 10 tiles a workgroup N300 L300 14.7 and 14.2, N2000 69.3
+  // and 62.8; 19 tiles N300 L600 21.2 and 22.1, N1000 59.8 and 58.1; 25 tiles N600 L800 43.3 and 44.6; 125 tiles N300 L4000
   // 136 and 145, N2000 723 and 729. fp32, pages of 24: 11 tiles N2000 L150 81.1 and 70.6; 20 tiles N300 L300 27.1 and 28.4,
-  // N2000 137.5 and 133.5; 38 tiles N2000 L600 240 and 246; 148 tiles N300 L4000 286 and 338. (e4m3 and dh 64 lose more than
+  // N2000 137.5 and 133.5; 38 tiles N2000 L600 240 and 246; 251 tiles N300 L4000 286 and 338. (e4m3 and dh 64 lose more than
   // they win.)
   constexpr unsigned kThird = 21504;  // with the 33680 bytes of PagedLds, more than a third of 160 KB
   const bool two = DH == 128 && sizeof(C) > 1 && p.chunk >= 20;
